@@ -3,8 +3,9 @@
  * (gfx950): encode, bit-exact decode, the memory-bound decode/verification GEMM
  * (M = 1..32 rows of BF16 x against W12 weights, FP32 accumulate, BF16 out; up to 128
  * rows for several requests verified together), the greedy verification epilogue
- * (exact-logit argmax per row, accepted-prefix length per request), and the same GEMM
- * for the FP8 weights of FP8 targets (E4M3 codes with 128 x 128 block scales).
+ * (exact-logit argmax per row, accepted-prefix length per request), the same GEMM
+ * for the FP8 weights of FP8 targets (E4M3 codes with 128 x 128 block scales), and the
+ * attention side of the decode step (paged cache, block tables, attention of the new rows).
  *
  * Sources (pages cited by title and section):
  *  - "StargazerX0/SpecPilot" (hotrepo.ai), "What it is": W12 is a 12-bit weight
@@ -72,9 +73,9 @@ typedef int32_t w12_status;
 
 #define W12_OK             0
 #define W12_ERR_NULL      -1  /* a required pointer is NULL */
-#define W12_ERR_SHAPE     -2  /* n % 16, k % 128, k >= 2^20, n == 0, m * n >= 2^32 */
+#define W12_ERR_SHAPE     -2  /* n % 16, k % 128, k >= 2^20, n == 0, m * n >= 2^32; cache geometry */
 #define W12_ERR_RANGE     -3  /* m outside 1..W12_MAX_M, n_draft > m, n_req outside 1..m */
-#define W12_ERR_FORMAT    -4  /* codebook not strictly ascending, e_max >= 255 */
+#define W12_ERR_FORMAT    -4  /* codebook not strictly ascending, e_max >= 255; cache type, scales */
 #define W12_ERR_WORKSPACE -5  /* workspace smaller than w12_workspace_bytes() */
 #define W12_ERR_HIP       -6  /* a HIP runtime call or kernel launch failed */
 #define W12_ERR_ALIGN     -7  /* tiles/x/w/y/ws not aligned as documented */
@@ -419,6 +420,125 @@ w12_status w12_screen_logits_f32(const uint16_t* x, uint32_t m, const w12_desc* 
  * method itself. */
 w12_status w12_rms_rescale(const uint16_t* x, uint32_t m, uint64_t k, uint16_t* y,
                            void* stream);
+
+/* ---- The attention side of a decode step: a paged key-value cache, its block tables, and
+ * the attention of the new rows over it.  Not part of the W12 method itself: these calls
+ * stand between the q, k, v GEMM and the o GEMM of a layer and use the request table of the
+ * batched verification (request r owns rows req_off[r] .. req_off[r+1]-1 of the batch).
+ *
+ * Cache of one layer: K as [n_pages][n_kv_heads][page_size][head_dim] and V transposed
+ * inside its page, [n_pages][n_kv_heads][head_dim][page_size], both BF16 or both FP8 E4M3
+ * (a stored code stands for code * k_scale or code * v_scale).  A slot is page * page_size +
+ * place.  Token t of request r lives in page table[r][t / page_size], place t % page_size.
+ * (In this layout the 16 bytes a lane loads are what the matrix cores take from it in both
+ * products: 8 or 16 dimensions of one key, 8 or 16 consecutive tokens of one dimension of V.) */
+#define W12_KV_BF16 0
+#define W12_KV_E4M3 1
+#define W12_MAX_REQ 4096        /* requests of one call, at most */
+#define W12_MAX_KV_ROWS (1u << 20)   /* rows of one w12_kv_plan / w12_qk_rope / w12_attn_paged call */
+#define W12_MAX_HEADS 1024      /* query heads, at most */
+
+/* Block tables over one pool of pages (host-side descriptor of device arrays, all 4-byte
+ * aligned).  Free pages form a ring: entries head .. head + count - 1 (mod n_pages). */
+typedef struct w12_pages {
+  uint32_t n_pages;       /* pages of the pool; n_pages * page_size < 2^31 */
+  uint32_t page_size;     /* 16, 32, 64, 128 or 256 tokens */
+  uint32_t max_req;       /* rows of the table, 1..W12_MAX_REQ */
+  uint32_t max_pages;     /* entries of a table row; max_pages * page_size < 2^31 */
+  int32_t* table;         /* device [max_req][max_pages] page ids */
+  int32_t* held;          /* device [max_req] pages each request holds */
+  int32_t* ring;          /* device [n_pages] free page ids */
+  int32_t* state;         /* device [4]: head, count, 0, 0 */
+} w12_pages;
+
+/* Brings the block tables in line with the requests' lengths and maps the new rows.
+ * Request r (r < n_req <= max_req) keeps len[r] tokens and adds rows_r = req_off[r+1] -
+ * req_off[r] rows, so it shall hold want_r = ceil((len[r] + rows_r) / page_size) pages:
+ * pages past want_r go to the end of the free ring (in request order, each request's in
+ * table order), which trims the pages of rejected draft rows and, at length 0 without rows,
+ * releases the request; missing pages come from the start of the ring, in request order,
+ * pages given back in the same call included.  A request that finds too few pages, and every
+ * later one that needs any, is refused: its pages stay as they are.  Refused too is a request
+ * with len[r] < 0, len[r] + rows_r > max_pages * page_size or held[r] outside
+ * 0..max_pages; and every request, with nothing changed, when req_off is not
+ * 0 <= req_off[0] <= req_off[1] <= ... <= m or state is not a ring's.
+ * Written: kv_len [n_req] = len[r] + rows_r, -1 if refused; pos [m] = the row's position in
+ * its request; slot [m] = its place in the cache; both -1 for rows of a refused request or of
+ * none; table, held, ring, state.  Table entries past want_r keep their old values.
+ * All arrays device int32; len and req_off [n_req + 1] are only read; pos and slot may be
+ * NULL when m = 0.  No result depends on the order of threads.  Calls on one w12_pages must
+ * be ordered.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (page_size, n_pages, max_pages, max_req);
+ * W12_ERR_RANGE (n_req outside 1..max_req, m > W12_MAX_KV_ROWS); W12_ERR_ALIGN. */
+w12_status w12_kv_plan(const w12_pages* p, const int32_t* len, const int32_t* req_off,
+                       uint32_t n_req, uint32_t m, int32_t* kv_len, int32_t* pos,
+                       int32_t* slot, void* stream);
+
+/* Host-side descriptor of one layer's cache. */
+typedef struct w12_kv {
+  uint32_t n_pages;       /* n_pages * page_size < 2^31 */
+  uint32_t page_size;     /* 16, 32, 64, 128 or 256 */
+  uint32_t n_kv_heads;
+  uint32_t head_dim;      /* 64, 128 or 256 */
+  uint32_t dtype;         /* W12_KV_BF16 or W12_KV_E4M3 */
+  float k_scale, v_scale; /* finite, > 0; 1 for W12_KV_BF16 */
+  void* k;                /* device, 16-byte aligned */
+  void* v;                /* device, 16-byte aligned */
+} w12_kv;
+
+/* Norm and rotation of the heads of q and k. */
+typedef struct w12_rope {
+  const uint16_t* q_norm;   /* device BF16 [head_dim], 16-byte aligned; NULL: no norm of q */
+  const uint16_t* k_norm;   /* the same for k */
+  const double* inv_freq;   /* device FP64 [rot_dim / 2], radians per position, 8-byte aligned */
+  uint32_t rot_dim;         /* leading dimensions that turn: multiple of 16, 0..head_dim */
+  uint32_t interleaved;     /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1) */
+  float eps;                /* >= 0, finite */
+} w12_rope;
+
+/* Per row and head: y = x / sqrt(mean(x^2) + eps) * norm (FP32; left out where norm is NULL),
+ * the pairs of the first rot_dim dimensions turned by pos[row] * inv_freq[i] (the angle in
+ * FP64, its sine and cosine in FP32), rounded once: q to q_out (BF16), k to the cache at
+ * slot[row] (BF16, or E4M3 of y / k_scale, saturating at 448), and v to the cache as it is
+ * (or E4M3 of v / v_scale).  NaN stays NaN.  q [m][n_heads][head_dim], k and v
+ * [m][n_kv_heads][head_dim], q_out as q: device BF16, heads contiguous, rows *_stride
+ * elements apart (a multiple of 8, at least the row's length); q_out may be q with the same
+ * stride, nothing else may overlap.  A row with pos < 0 is passed over: nothing of it is
+ * written.  A row whose slot is outside 0 .. n_pages * page_size - 1 gets its q and leaves the
+ * cache alone.  The slots of one call are distinct (of rows that share one, either's
+ * values stay).  m = 0 does nothing.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (cache geometry,
+ * n_heads outside 1..W12_MAX_HEADS or no multiple of n_kv_heads, rot_dim, strides);
+ * W12_ERR_RANGE (m > W12_MAX_KV_ROWS); W12_ERR_FORMAT (dtype, scales, eps, interleaved);
+ * W12_ERR_ALIGN (pointers 16 bytes, pos and slot 4, inv_freq 8). */
+w12_status w12_qk_rope(const uint16_t* q, uint64_t q_stride, const uint16_t* k, uint64_t k_stride,
+                       const uint16_t* v, uint64_t v_stride, uint32_t m, uint32_t n_heads,
+                       const w12_kv* kv, const w12_rope* rope, const int32_t* pos,
+                       const int32_t* slot, uint16_t* q_out, uint64_t q_out_stride, void* stream);
+
+/* out[row][h] = sum_t softmax_t(scale * q[row][h] . K[t]) V[t], K and V of head h / (n_heads /
+ * n_kv_heads): row i of the rows_r rows of request r sees the tokens t <= kv_len[r] - rows_r
+ * + i (the last row sees all kv_len[r] tokens, so the draft block is causal).  FP32 scores,
+ * maxima and sums; the weights enter the second product rounded to BF16.  A row that sees no
+ * token gets zeros.  What lies in the cache behind a row's last token never reaches it, NaN
+ * included.  Rows of no request are left as they were.  A request whose kv_len is outside
+ * 0 .. max_pages * page_size (kv_len -1: refused by w12_kv_plan) gets NaN, and so does a row
+ * that sees a token whose table entry is outside 0 .. n_pages - 1; every row gets NaN when
+ * req_off is not 0 <= req_off[0] <= req_off[1] <= ... <= m.
+ * q and out device BF16 [m][n_heads][head_dim], rows *_stride elements apart (a multiple of 8,
+ * at least the row's length), 16-byte aligned; table device int32 [>= n_req][max_pages],
+ * kv_len [n_req], req_off [n_req + 1].  The sequence is split over workgroups and joined
+ * inside the launch in a fixed order: same inputs, same bits.  ws: W12_ATTN_WS_BYTES bytes,
+ * 256-byte aligned, beginning with 4096 bytes of tickets that must be zero before its first
+ * use (w12_workspace_init) and that every call leaves zero; calls sharing a workspace must be
+ * ordered.  m = 0 does nothing.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (cache geometry, heads,
+ * max_pages * page_size >= 2^31, strides); W12_ERR_RANGE (n_req outside 1..W12_MAX_REQ, m >
+ * W12_MAX_KV_ROWS); W12_ERR_FORMAT (dtype, scales, scale not finite); W12_ERR_WORKSPACE;
+ * W12_ERR_ALIGN. */
+#define W12_ATTN_WS_BYTES (36u << 20)
+w12_status w12_attn_paged(const uint16_t* q, uint64_t q_stride, uint32_t m, uint32_t n_heads,
+                          const w12_kv* kv, const int32_t* table, uint32_t max_pages,
+                          const int32_t* kv_len, const int32_t* req_off, uint32_t n_req,
+                          float scale, uint16_t* out, uint64_t out_stride, void* ws,
+                          size_t ws_bytes, void* stream);
 
 /* Measurement helper, not part of the W12 method: streams `bytes` (a multiple of 16,
  * below 2^32) of device memory at `buf` (16-byte aligned) with the nontemporal 16-byte

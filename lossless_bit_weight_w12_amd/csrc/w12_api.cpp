@@ -1010,9 +1010,10 @@ const char* w12_status_str(w12_status s) {
   switch (s) {
     case W12_OK: return "ok";
     case W12_ERR_NULL: return "null pointer";
-    case W12_ERR_SHAPE: return "bad shape (n % 16, k % 128, 0 < k < 2^20)";
-    case W12_ERR_RANGE: return "value out of range (m in 1..128, n_draft <= m, n_req in 1..m)";
-    case W12_ERR_FORMAT: return "bad W12 descriptor (codebook not ascending, e_max, n_esc)";
+    case W12_ERR_SHAPE: return "bad shape (n % 16, k % 128, 0 < k < 2^20; cache geometry, heads, strides)";
+    case W12_ERR_RANGE: return "value out of range (GEMM and verification: m in 1..128, n_draft <= m, n_req in 1..m; "
+                               "cache calls: m <= 2^20, n_req in 1..4096)";
+    case W12_ERR_FORMAT: return "bad W12 descriptor (codebook not ascending, e_max, n_esc) or cache type, scale or eps";
     case W12_ERR_WORKSPACE: return "workspace too small";
     case W12_ERR_HIP: return "HIP runtime error";
     case W12_ERR_ALIGN: return "misaligned pointer";

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_int, c_int32, c_size_t, c_uint8, c_uint32, c_uint64, c_void_p
+from ctypes import c_float, c_int, c_int32, c_size_t, c_uint8, c_uint32, c_uint64, c_void_p
 from dataclasses import dataclass
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw12.so")
@@ -18,6 +18,11 @@ OP_ENCODE, OP_DECODE, OP_GEMM, OP_GEMM_BF16, OP_VERIFY, OP_GEMM_GROUP, OP_VERIFY
     0, 1, 2, 3, 4, 5, 6, 7
 MAX_M = 128
 MAX_GROUP = 4
+KV_BF16, KV_E4M3 = 0, 1
+MAX_REQ = 4096                 # W12_MAX_REQ: requests of one cache call
+MAX_KV_ROWS = 1 << 20          # W12_MAX_KV_ROWS: rows of one cache call
+MAX_HEADS = 1024               # W12_MAX_HEADS
+ATTN_WS_BYTES = 36 << 20       # W12_ATTN_WS_BYTES
 STATUS = {0: "W12_OK", -1: "W12_ERR_NULL", -2: "W12_ERR_SHAPE", -3: "W12_ERR_RANGE",
           -4: "W12_ERR_FORMAT", -5: "W12_ERR_WORKSPACE", -6: "W12_ERR_HIP", -7: "W12_ERR_ALIGN"}
 EXPORTS = ("w12_tiles_bytes", "w12_workspace_bytes", "w12_workspace_init", "w12_encode_count",
@@ -28,7 +33,8 @@ EXPORTS = ("w12_tiles_bytes", "w12_workspace_bytes", "w12_workspace_init", "w12_
            "w12_rms_rescale", "w12_status_str", "w12_version", "w12_gemm_noalloc", "w12_stream_read",
            "w12_screen_bytes", "w12_screen_encode", "w12_lmhead_verify2", "w12_lmhead_verify2_batched",
            "w12_screen_logits_f32", "w12_f8_tile", "w12_gemm_f8", "w12_gemm_f8_group",
-           "w12_gemm_f8_rms", "w12_gemm_f8_group_rms")
+           "w12_gemm_f8_rms", "w12_gemm_f8_group_rms", "w12_kv_plan", "w12_qk_rope",
+           "w12_attn_paged")
 NOALLOC_SCRATCH_BYTES = 32 << 20   # W12_NOALLOC_SCRATCH_BYTES
 ENCODE_TOTAL_OFFSET = 2112   # W12_ENCODE_TOTAL_OFFSET: true escape count in an encode workspace
 
@@ -43,6 +49,23 @@ class W12Desc(ctypes.Structure):
     _fields_ = [("n", c_uint64), ("k", c_uint64), ("n_esc", c_uint64),
                 ("codebook", c_uint8 * 16), ("e_max", c_uint8), ("reserved", c_uint8 * 7),
                 ("tiles", c_void_p), ("esc_off", c_void_p), ("esc", c_void_p)]
+
+
+class W12Pages(ctypes.Structure):
+    _fields_ = [("n_pages", c_uint32), ("page_size", c_uint32), ("max_req", c_uint32),
+                ("max_pages", c_uint32), ("table", c_void_p), ("held", c_void_p),
+                ("ring", c_void_p), ("state", c_void_p)]
+
+
+class W12Kv(ctypes.Structure):
+    _fields_ = [("n_pages", c_uint32), ("page_size", c_uint32), ("n_kv_heads", c_uint32),
+                ("head_dim", c_uint32), ("dtype", c_uint32), ("k_scale", c_float),
+                ("v_scale", c_float), ("k", c_void_p), ("v", c_void_p)]
+
+
+class W12Rope(ctypes.Structure):
+    _fields_ = [("q_norm", c_void_p), ("k_norm", c_void_p), ("inv_freq", c_void_p),
+                ("rot_dim", c_uint32), ("interleaved", c_uint32), ("eps", c_float)]
 
 
 def lib_path() -> str:
@@ -136,6 +159,17 @@ def lib():
                                             c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
         L.w12_rms_rescale.restype = c_int32
         L.w12_rms_rescale.argtypes = [c_void_p, c_uint32, c_uint64, c_void_p, c_void_p]
+        L.w12_kv_plan.restype = c_int32
+        L.w12_kv_plan.argtypes = [ctypes.POINTER(W12Pages), c_void_p, c_void_p, c_uint32, c_uint32,
+                                  c_void_p, c_void_p, c_void_p, c_void_p]
+        L.w12_qk_rope.restype = c_int32
+        L.w12_qk_rope.argtypes = [c_void_p, c_uint64, c_void_p, c_uint64, c_void_p, c_uint64,
+                                  c_uint32, c_uint32, ctypes.POINTER(W12Kv), ctypes.POINTER(W12Rope),
+                                  c_void_p, c_void_p, c_void_p, c_uint64, c_void_p]
+        L.w12_attn_paged.restype = c_int32
+        L.w12_attn_paged.argtypes = [c_void_p, c_uint64, c_uint32, c_uint32, ctypes.POINTER(W12Kv),
+                                     c_void_p, c_uint32, c_void_p, c_void_p, c_uint32, c_float,
+                                     c_void_p, c_uint64, c_void_p, c_size_t, c_void_p]
         L.w12_status_str.restype = ctypes.c_char_p
         L.w12_status_str.argtypes = [c_int32]
         L.w12_version.restype = c_uint32
@@ -678,6 +712,284 @@ def rms_rescale(x, out=None):
     return out
 
 
+# ----------------------------------------------------------------------------- paged cache
+@dataclass
+class PageTable:
+    """Block tables of up to max_req requests over one pool of pages (page_table makes an
+    empty one).  Request r's token t lies in page table[r, t // page_size].  The free pages are
+    ring[state[0]], ring[state[0] + 1], ... (state[1] of them, indices modulo n_pages)."""
+    page_size: int
+    table: object      # torch.int32 [max_req, max_pages]
+    held: object       # torch.int32 [max_req]: pages each request holds
+    ring: object       # torch.int32 [n_pages]
+    state: object      # torch.int32 [4]: head, count, 0, 0
+
+    @property
+    def n_pages(self) -> int:
+        return self.ring.numel()
+
+    @property
+    def device(self):
+        return self.table.device
+
+    def desc(self) -> W12Pages:
+        if self.table.dim() != 2:
+            raise ValueError("PageTable: table must be [max_req, max_pages]")
+        max_req, max_pages = self.table.shape
+        for name, t, size in (("table", self.table, max_req * max_pages), ("held", self.held, max_req),
+                              ("ring", self.ring, self.n_pages), ("state", self.state, 4)):
+            _int32(f"PageTable: {name}", t, size, self.device)
+        p = W12Pages()
+        p.n_pages, p.page_size, p.max_req, p.max_pages = self.n_pages, self.page_size, max_req, max_pages
+        p.table, p.held, p.ring, p.state = (t.data_ptr() for t in
+                                            (self.table, self.held, self.ring, self.state))
+        return p
+
+
+def page_table(n_pages: int, page_size: int, max_req: int, max_pages: int, device="cuda") -> PageTable:
+    """A pool of n_pages free pages and empty tables for max_req requests of at most
+    max_pages pages each."""
+    torch = _torch()
+    i32 = dict(dtype=torch.int32, device=device)
+    return PageTable(page_size, torch.full((max_req, max_pages), -1, **i32),
+                     torch.zeros(max_req, **i32), torch.arange(n_pages, **i32),
+                     torch.tensor([0, n_pages, 0, 0], **i32))
+
+
+@dataclass
+class KvCache:
+    """One layer's paged keys and values: k [n_pages, n_kv_heads, page_size, head_dim] and v
+    transposed inside its page, [n_pages, n_kv_heads, head_dim, page_size]; both bfloat16, or
+    both float8_e4m3fn with a stored code standing for code * scale."""
+    k: object
+    v: object
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+
+    @property
+    def device(self):
+        return self.k.device
+
+    def desc(self) -> W12Kv:
+        torch = _torch()
+        k, v = self.k, self.v
+        if not k.is_cuda:
+            raise ValueError("W12 calls need CUDA (HIP) tensors")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            raise ValueError("KvCache: k and v must both be bfloat16 or both float8_e4m3fn")
+        if k.dim() != 4 or tuple(v.shape) != (k.shape[0], k.shape[1], k.shape[3], k.shape[2]) or \
+                v.device != k.device or not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("KvCache: k must be [n_pages, n_kv_heads, page_size, head_dim] and v "
+                             "[n_pages, n_kv_heads, head_dim, page_size], contiguous, on one device")
+        d = W12Kv()
+        d.n_pages, d.n_kv_heads, d.page_size, d.head_dim = k.shape
+        d.dtype = KV_BF16 if k.dtype == torch.bfloat16 else KV_E4M3
+        d.k_scale, d.v_scale = self.k_scale, self.v_scale
+        d.k, d.v = k.data_ptr(), v.data_ptr()
+        return d
+
+
+def kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=None,
+             k_scale: float = 1.0, v_scale: float = 1.0, device="cuda") -> KvCache:
+    """An empty (zero) cache of n_pages pages; dtype bfloat16 (default) or float8_e4m3fn."""
+    torch = _torch()
+    dtype = dtype or torch.bfloat16
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.uint8
+    k = torch.zeros((n_pages, n_kv_heads, page_size, head_dim), dtype=bits, device=device).view(dtype)
+    v = torch.zeros((n_pages, n_kv_heads, head_dim, page_size), dtype=bits, device=device).view(dtype)
+    return KvCache(k, v, k_scale, v_scale)
+
+
+@dataclass
+class Rope:
+    """Norm and rotation of query and key heads: inv_freq float64 [rot_dim / 2] in radians per
+    position (None: no rotation), BF16 norm weights [head_dim] (None: no norm), pairs
+    (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved."""
+    inv_freq: object = None
+    q_norm: object = None
+    k_norm: object = None
+    eps: float = 1e-6
+    interleaved: bool = False
+
+    def desc(self, head_dim: int, device) -> W12Rope:
+        torch = _torch()
+        f = self.inv_freq
+        if f is not None and (f.dtype != torch.float64 or f.device != device or not f.is_contiguous()):
+            raise ValueError("Rope: inv_freq must be a contiguous float64 tensor on the cache's device")
+        for w in (self.q_norm, self.k_norm):
+            if w is not None and (_as_bits(w).numel() != head_dim or w.device != device):
+                raise ValueError("Rope: norm weights must be BF16 [head_dim] on the cache's device")
+        d = W12Rope()
+        d.q_norm = self.q_norm.data_ptr() if self.q_norm is not None else None
+        d.k_norm = self.k_norm.data_ptr() if self.k_norm is not None else None
+        d.inv_freq = f.data_ptr() if f is not None and f.numel() else None
+        d.rot_dim = 2 * f.numel() if f is not None else 0
+        d.interleaved, d.eps = int(self.interleaved), self.eps
+        return d
+
+
+def _int32(name: str, t, size: int, device):
+    if t.dtype != _torch().int32 or t.numel() != size or t.device != device or not t.is_cuda \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {size} on {device}")
+
+
+def _heads(name: str, t, m: int, n: int, d: int, device) -> int:
+    """Row stride (elements) of a BF16 tensor [m, n, d] whose rows hold n contiguous heads."""
+    torch = _torch()
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be BF16 on {device}")
+    if tuple(t.shape) != (m, n, d) or (m > 0 and (t.stride(2) != 1 or (n > 1 and t.stride(1) != d))):
+        raise ValueError(f"{name} must be [{m}, {n}, {d}] with contiguous heads")
+    if m > 1 and t.stride(0) < n * d:
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0) if m > 1 else n * d
+
+
+def _apart(name: str, out, *ins):
+    for t in ins:
+        a, b = out.data_ptr(), t.data_ptr()
+        if out.numel() and t.numel() and a < b + t.numel() * t.element_size() \
+                and b < a + out.numel() * out.element_size():
+            raise ValueError(f"{name} overlaps another argument")
+
+
+def _issue(name: str, args, device):
+    torch = _torch()
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            _check(name, getattr(lib(), name)(*args))
+    else:
+        _check(name, getattr(lib(), name)(*args))
+
+
+def _plan_args(pt: PageTable, length, req_off, kv_len, pos, slot):
+    dev, n_req, m = pt.device, int(length.numel()), int(pos.numel())
+    for name, t, size in (("length", length, n_req), ("req_off", req_off, n_req + 1),
+                          ("kv_len", kv_len, n_req), ("pos", pos, m), ("slot", slot, m)):
+        _int32(f"kv_plan: {name}", t, size, dev)
+    state = (pt.table, pt.held, pt.ring, pt.state)
+    for name, t, others in (("kv_len", kv_len, (length, req_off, pos, slot)),
+                            ("pos", pos, (length, req_off, slot)), ("slot", slot, (length, req_off))):
+        _apart(f"kv_plan: {name}", t, *others, *state)
+    d = pt.desc()
+    args = (ctypes.byref(d), _ptr(length), _ptr(req_off), n_req, m, _ptr(kv_len),
+            _ptr(pos) if m else None, _ptr(slot) if m else None, _stream(dev))
+    return args, (pt, length, req_off, kv_len, pos, slot, d)
+
+
+def kv_plan(pt: PageTable, length, req_off, m: int, kv_len=None, pos=None, slot=None):
+    """Bring the block tables in line with the requests' lengths and map the m new rows
+    (w12_kv_plan): request r keeps length[r] tokens and adds rows req_off[r] ..
+    req_off[r+1]-1.  Pages past its need go back to the pool (rejected drafts; everything at
+    length 0 without rows), missing ones are taken.  length int32 [n_req], req_off int32
+    [n_req + 1].  Returns int32 (kv_len [n_req], pos [m], slot [m]); -1 marks a request that
+    found too few pages or has invalid lengths, and its rows."""
+    torch = _torch()
+    new = lambda n: torch.empty(n, dtype=torch.int32, device=pt.device)
+    kv_len = new(length.numel()) if kv_len is None else kv_len
+    pos = new(m) if pos is None else pos
+    slot = new(m) if slot is None else slot
+    if pos.numel() != m:
+        raise ValueError(f"kv_plan: pos must have m = {m} entries")
+    args, keep = _plan_args(pt, length, req_off, kv_len, pos, slot)
+    _issue("w12_kv_plan", args, pt.device)
+    return kv_len, pos, slot
+
+
+def _rope_args(q, k, v, cache: KvCache, rope: Rope, pos, slot, q_out):
+    c = cache.desc()
+    dev, m, n, d = cache.device, q.shape[0], q.shape[1], c.head_dim
+    strides = [_heads("qk_rope: q", q, m, n, d, dev), _heads("qk_rope: k", k, m, c.n_kv_heads, d, dev),
+               _heads("qk_rope: v", v, m, c.n_kv_heads, d, dev),
+               _heads("qk_rope: q_out", q_out, m, n, d, dev)]
+    for name, t in (("pos", pos), ("slot", slot)):
+        _int32(f"qk_rope: {name}", t, m, dev)
+    if q_out.data_ptr() == q.data_ptr() and strides[3] != strides[0]:
+        raise ValueError("qk_rope: q_out may be q itself, with the same strides")
+    r = rope.desc(d, dev)
+    args = (_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], m, n, ctypes.byref(c),
+            ctypes.byref(r), _ptr(pos), _ptr(slot), _ptr(q_out), strides[3], _stream(dev))
+    return args, (q, k, v, cache, rope, pos, slot, q_out, c, r)
+
+
+def qk_rope(q, k, v, cache: KvCache, rope: Rope, pos, slot, q_out=None):
+    """Norm and rotate the heads of q [m, n_heads, head_dim] and k [m, n_kv_heads, head_dim] at
+    the rows' positions, and append k and v to the cache at their slots (w12_qk_rope; pos and
+    slot int32 [m] as kv_plan gives them).  Rows may be strided.  Rows with pos < 0 are passed
+    over, rows without a slot leave the cache alone.  Returns q_out (BF16; may be q)."""
+    if q.dim() != 3:
+        raise ValueError("qk_rope: q must be [m, n_heads, head_dim]")
+    if q_out is None:
+        q_out = _torch().empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+    args, _keep = _rope_args(q, k, v, cache, rope, pos, slot, q_out)
+    _issue("w12_qk_rope", args, cache.device)
+    return q_out
+
+
+_ATTN_WS = {}
+
+
+def attn_workspace(device="cuda"):
+    """A workspace for attn_paged (zero tickets), for callers that keep their own: one for each
+    stream or captured graph that may run at the same time as others."""
+    torch = _torch()
+    return torch.zeros(ATTN_WS_BYTES, dtype=torch.uint8, device=device)
+
+
+def _attn_ws(dev, ws):
+    """The caller's workspace, or one per device and stream.  Under graph capture without the
+    caller's: memory of the graph itself, its tickets zeroed inside the graph, so no other
+    graph or stream shares it."""
+    torch = _torch()
+    if ws is not None:
+        if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"attn_paged: ws must be a contiguous uint8 tensor on {dev}")
+        return ws
+    with torch.cuda.device(dev):
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(ATTN_WS_BYTES, dtype=torch.uint8, device=dev)
+            _check("w12_workspace_init", lib().w12_workspace_init(_ptr(ws), 4096, _stream(dev)))
+            return ws
+        key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+        if key not in _ATTN_WS:
+            _ATTN_WS[key] = attn_workspace(dev)
+        return _ATTN_WS[key]
+
+
+def _attn_args(q, cache: KvCache, table, kv_len, req_off, out, scale, ws):
+    c = cache.desc()
+    dev, m, n, d, n_req = cache.device, q.shape[0], q.shape[1], c.head_dim, int(kv_len.numel())
+    qs, os_ = _heads("attn_paged: q", q, m, n, d, dev), _heads("attn_paged: out", out, m, n, d, dev)
+    if out.data_ptr() == q.data_ptr() and m:
+        raise ValueError("attn_paged: out overlaps q")
+    if table.dim() != 2 or table.shape[0] < n_req:
+        raise ValueError("attn_paged: table must be [>= n_req, max_pages]")
+    _int32("attn_paged: table", table, table.shape[0] * table.shape[1], dev)
+    _int32("attn_paged: kv_len", kv_len, n_req, dev)
+    _int32("attn_paged: req_off", req_off, n_req + 1, dev)
+    ws = _attn_ws(dev, ws)
+    scale = d ** -0.5 if scale is None else float(scale)
+    args = (_ptr(q), qs, m, n, ctypes.byref(c), _ptr(table), table.shape[1], _ptr(kv_len), _ptr(req_off),
+            n_req, scale, _ptr(out), os_, _ptr(ws), ws.numel(), _stream(dev))
+    return args, (q, cache, table, kv_len, req_off, out, ws, c)
+
+
+def attn_paged(q, cache: KvCache, table, kv_len, req_off, out=None, scale=None, ws=None):
+    """Attention of the new rows q [m, n_heads, head_dim] over the paged cache (w12_attn_paged):
+    request r owns rows req_off[r] .. req_off[r+1]-1, the last kv_len[r] tokens' newest; row i
+    sees the tokens up to its own.  table int32 [>= n_req, max_pages], kv_len int32 [n_req],
+    req_off int32 [n_req + 1]; scale defaults to head_dim ** -0.5; n_heads any multiple of the
+    cache's heads.  Returns out (BF16; rows of no request are left as they were)."""
+    if q.dim() != 3:
+        raise ValueError("attn_paged: q must be [m, n_heads, head_dim]")
+    if out is None:
+        out = _torch().zeros(tuple(q.shape), dtype=q.dtype, device=q.device)
+    args, _keep = _attn_args(q, cache, table, kv_len, req_off, out, scale, ws)
+    _issue("w12_attn_paged", args, cache.device)
+    return out
+
+
 # ----------------------------------------------------------------------------- prepared calls
 class Prepared:
     """One library call with its arguments marshalled once (device pointers, descriptor,
@@ -772,3 +1084,32 @@ def prepare_verify_batched(x, t: W12Tensor, req_off, req_ndraft, draft, argmax_o
                            accepted_out) -> Prepared:
     args, keep = _batched_args(x, t, req_off, req_ndraft, draft, argmax_out, accepted_out)
     return Prepared("w12_lmhead_verify_batched", lib().w12_lmhead_verify_batched, args, keep)
+
+
+class _PreparedOn(Prepared):
+    """A prepared call that is issued with its tensors' device current."""
+
+    def __init__(self, name: str, args, keep, device):
+        super().__init__(name, getattr(lib(), name), args, keep)
+        self._device = device
+
+    def __call__(self):
+        _issue(self.name, self._args, self._device)
+
+
+def prepare_kv_plan(pt: PageTable, length, req_off, kv_len, pos, slot) -> Prepared:
+    """kv_plan of m = pos.numel() rows into kv_len, pos and slot."""
+    args, keep = _plan_args(pt, length, req_off, kv_len, pos, slot)
+    return _PreparedOn("w12_kv_plan", args, keep, pt.device)
+
+
+def prepare_qk_rope(q, k, v, cache: KvCache, rope: Rope, pos, slot, q_out) -> Prepared:
+    args, keep = _rope_args(q, k, v, cache, rope, pos, slot, q_out)
+    return _PreparedOn("w12_qk_rope", args, keep, cache.device)
+
+
+def prepare_attn_paged(q, cache: KvCache, table, kv_len, req_off, out, scale=None, ws=None) -> Prepared:
+    """attn_paged into out.  A captured prepared call keeps its workspace: graphs that may run
+    at the same time are prepared with a ws of their own (attn_workspace)."""
+    args, keep = _attn_args(q, cache, table, kv_len, req_off, out, scale, ws)
+    return _PreparedOn("w12_attn_paged", args, keep, cache.device)
