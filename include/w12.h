@@ -531,7 +531,8 @@ w12_status w12_qk_rope(const uint16_t* q, uint64_t q_stride, const uint16_t* k, 
  * use (w12_workspace_init) and that every call leaves zero; calls sharing a workspace must be
  * ordered.  m = 0 does nothing.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (cache geometry, heads,
  * max_pages * page_size >= 2^31, strides); W12_ERR_RANGE (n_req outside 1..W12_MAX_REQ, m >
- * W12_MAX_KV_ROWS); W12_ERR_FORMAT (dtype, scales, scale not finite); W12_ERR_WORKSPACE;
+ * W12_MAX_KV_ROWS, (m * n_heads + 64 * n_req * n_kv_heads) * (max_pages * page_size + 1024) >=
+ * 2^40); W12_ERR_FORMAT (dtype, scales, scale not finite); W12_ERR_WORKSPACE;
  * W12_ERR_ALIGN. */
 #define W12_ATTN_WS_BYTES (36u << 20)
 w12_status w12_attn_paged(const uint16_t* q, uint64_t q_stride, uint32_t m, uint32_t n_heads,

@@ -1,4 +1,24 @@
 // Attention of a decode step's new rows over the paged cache (w12_attn_paged).
+//
+// Mathematics: per request, key head and tile of query rows (a query row is a pair of a batch
+// row and one of the group's query heads), one pass over the tokens with the running maximum
+// and sum of the softmax.  Both products run on the matrix cores with the tokens as the
+// rows of the first and the summed index of the second:
+//   S^T [token][query] = K Q^T,   O^T [dim][query] += V^T P^T,
+// so that a lane keeps one query row (column l % 16) through both, and the scores it computes
+// are the weights it feeds back: the matrix core leaves lane group g = l / 16 with rows 4g ..
+// 4g + 3 of each 16-token tile and wants 8 consecutive summed indices of it, and since the
+// order in which tokens are dealt to tile rows is free, tile row 4a + i takes the token that
+// makes a lane's scores 8 (BF16) or 16 (E4M3) consecutive tokens: the ones its 16-byte loads
+// of V^T hold.  Nothing passes through LDS inside the loop, and every load is 16 bytes used
+// as it comes.
+//
+// Split: the work of all requests, heads and tiles is one line of units of UT tokens, cut into
+// equal pieces, one per workgroup; inside a piece each wave takes every NW-th unit.  Lengths
+// can be as uneven as they like and a single long request still fills the chip.  A workgroup
+// joins its waves in LDS; an item (request, tile, head) cut by a piece's border is joined by
+// the workgroup that finishes it last, in piece order, so the result does not depend on
+// which that is.
 #include "w12.h"
 #include "w12_kv.h"
 
@@ -7,112 +27,831 @@ namespace w12 {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ float bf(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+constexpr uint32_t kAttnWG = 256;       // workgroups of a launch, at most (one ticket each)
+constexpr uint32_t kTicketBytes = 4096;
 
-template <bool F8>
-__device__ __forceinline__ float kv_value(const uint8_t* p, uint64_t i) {
-  if constexpr (F8) return __builtin_amdgcn_cvt_f32_fp8((int)p[i], 0);
-  else return bf(reinterpret_cast<const uint16_t*>(p)[i]);
+__device__ __forceinline__ int32_t uniform_load(const int32_t* p, uint64_t i) {
+  // read through the constant address space (a scalar load): nothing here writes it
+  return reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)p)[i];
+}
+__device__ __forceinline__ uint32_t uni(uint32_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
+
+__device__ __forceinline__ uint32_t bf_pack(float a, float b) {
+  const __bf16 x = (__bf16)a, y = (__bf16)b;   // round to nearest even
+  return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
 }
 
-// One wave per row and head: 64 tokens at a time, one per lane for the scores, then D / 64
-// dimensions per lane for the weighted sum, with the running maximum and sum of the softmax.
-template <int D, bool F8>
-__global__ __launch_bounds__(64) void k_attn_simple(AttnArgs a) {
-  __shared__ float s_q[D], s_p[64];
-  const int lane = threadIdx.x;
+// 2^x as the hardware has it (one ulp; results below 2^-126 are zero, far below any rounding
+// of a sum that holds the weight 1 of the maximum).
+__device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Nothing is scheduled across: a load stays behind the products that free its registers.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// Largest value (sum) over the four lanes that share a query row (l % 16).
+__device__ __forceinline__ float group_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float group_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// Partial results pass between workgroups on any XCD, whose L2 caches are not coherent for
+// plain accesses: stores and loads at device scope (sc1), a ticket taken after the stores
+// are complete.
+constexpr int kCpolDevice = 16;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t ws_rsrc(const float* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), (short)0,
+                                           (int)(W12_ATTN_WS_BYTES - kTicketBytes), 0x00020000);
+}
+__device__ __forceinline__ void st_dev4(__amdgpu_buffer_rsrc_t rs, uint32_t off, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, off, 0, kCpolDevice);
+}
+__device__ __forceinline__ void st_dev2(__amdgpu_buffer_rsrc_t rs, uint32_t off, float a, float b) {
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(a), __float_as_uint(b)}, rs, off, 0, kCpolDevice);
+}
+__device__ __forceinline__ f32x4 ld_dev4(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, kCpolDevice));
+}
+__device__ __forceinline__ u32x2 ld_dev2(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, kCpolDevice);
+}
+
+// One request: its rows and what it lays on the line.
+struct Req {
+  int32_t row0, len;
+  uint32_t rows;
+  bool broken;       // len is none
+  uint32_t units;    // units of UT tokens of an item (at least one, which may be empty)
+  uint32_t tiles;    // tiles of query rows, per key head
+};
+
+template <int D, bool F8, int NT, int NW, int UT>
+struct Attn {
+  static constexpr int ES = F8 ? 1 : 2;          // bytes per cached value
+  static constexpr int QT = 16 * NT;             // query rows of a tile
+  static constexpr int KS = D / 32;              // matrix steps of a score
+  static constexpr int KL = F8 ? KS / 2 : KS;    // 16-byte loads of one key per lane
+  static constexpr int DT = D / 16;              // 16-dimension tiles of the output
+  static constexpr int TT = UT / 16;             // 16-token tiles of a unit
+  static constexpr int PS = UT / 32;             // matrix steps over a unit's tokens
+  static constexpr int VL = F8 ? PS / 2 : PS;    // 16-byte loads of one dimension of V per lane
+  static constexpr int ROW = D + 4;              // LDS row of the join, padded
+  static constexpr int T = 64 * NW;
+  // What an item costs a workgroup beside its units (its queries' load, the join, the writes:
+  // about 15000 cycles under load, the time of 128 KB), in units.
+  static constexpr uint32_t kLead = 131072 / (2 * UT * D * ES);
+  static_assert(!F8 || UT == 64, "an E4M3 lane load holds 16 tokens of a 64-token unit");
+
+  // Page ids of a unit's 16-token groups; groups past `end` read page 0 (masked).
+  struct Ids {
+    u32x4 id;          // (a vector and no array: it has to stay in registers)
+    uint32_t bad;      // bit j: group j holds tokens the tile sees and a page that is none
+  };
+  static __device__ __forceinline__ Ids load_ids(const AttnArgs& a, uint64_t trow, uint32_t u, uint32_t end) {
+    Ids x = {{0u, 0u, 0u, 0u}, 0u};
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      const uint32_t t = u * UT + 16 * j;
+      const bool need = t < end;
+      const uint32_t p = need ? (uint32_t)uniform_load(a.table, trow + (t >> a.page_shift)) : 0u;
+      const bool ok = p < a.n_pages;
+      x.bad |= ok ? 0u : 1u << j;
+      x.id[j] = ok ? p : 0u;
+    }
+    return x;
+  }
+
+  static __device__ __forceinline__ u32x4 load16(const uint8_t* p) {
+    return *reinterpret_cast<const u32x4*>(p);
+  }
+
+  // K of a unit: lane (row r = l % 16 of each token tile, group g) the 16 bytes g of each
+  // 64-byte step of its token's key.
+  static __device__ __forceinline__ void load_k(const AttnArgs& a, const Ids& x, uint32_t u, uint32_t head,
+                                                int lane, u32x4 (&k)[TT][KL]) {
+    const uint32_t r = lane & 15, g = lane >> 4, mask = (1u << a.page_shift) - 1u;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const uint32_t tok = F8 ? 16 * (r >> 2) + 4 * t + (r & 3) : 32 * (t / 2) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);
+      uint32_t id;
+      if constexpr (F8) {
+        const uint32_t lo = (r & 4) ? x.id[1] : x.id[0], hi = (r & 4) ? x.id[3] : x.id[2];
+        id = (r & 8) ? hi : lo;
+      } else {
+        id = (r & 8) ? x.id[2 * (t / 2) + 1] : x.id[2 * (t / 2)];
+      }
+      const uint32_t place = (u * UT + tok) & mask;
+      const uint8_t* p = a.kc + ((((uint64_t)id * a.n_kv_heads + head) << a.page_shift) + place) * (D * ES) + 16 * g;
+#pragma unroll
+      for (int i = 0; i < KL; ++i) k[t][i] = load16(p + 64 * i);
+    }
+  }
+
+  // V^T of a unit: lane (dimension l % 16 of each dimension tile, group g) 16 bytes of
+  // consecutive tokens: 32 s + 8 g .. + 7 (BF16), 16 g .. + 15 (E4M3).
+  static __device__ __forceinline__ void load_v(const AttnArgs& a, const Ids& x, uint32_t u, uint32_t head,
+                                                int lane, u32x4 (&v)[DT][VL]) {
+    const uint32_t g = lane >> 4, mask = (1u << a.page_shift) - 1u;
+#pragma unroll
+    for (int s = 0; s < VL; ++s) {
+      uint32_t id, tok;
+      if constexpr (F8) {
+        const uint32_t lo = (g & 1) ? x.id[1] : x.id[0], hi = (g & 1) ? x.id[3] : x.id[2];
+        id = (g & 2) ? hi : lo;
+        tok = 16 * g;
+      } else {
+        id = (g & 2) ? x.id[2 * s + 1] : x.id[2 * s];
+        tok = 32 * s + 8 * g;
+      }
+      const uint32_t place = (u * UT + tok) & mask;
+      const uint8_t* p = a.vc + (((((uint64_t)id * a.n_kv_heads + head) * D + (lane & 15)) << a.page_shift) + place) * ES;
+      const uint32_t step = (16u * ES) << a.page_shift;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        v[d][s] = load16(p);
+        p += step;
+      }
+    }
+  }
+
+  // The A operand of step s (32 dimensions or tokens) from the lane's loads.
+  template <int L>
+  static __device__ __forceinline__ bf16x8_t operand(const u32x4 (&x)[L], int s) {
+    if constexpr (F8) {
+      u32x4 o;   // every E4M3 value is a BF16 value
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = x[s / 2][2 * (s & 1) + h];
+        o[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+        o[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+      }
+      return __builtin_bit_cast(bf16x8_t, o);
+    } else {
+      return __builtin_bit_cast(bf16x8_t, x[s]);
+    }
+  }
+
+  // S^T of a unit.
+  static __device__ __forceinline__ void scores(const u32x4 (&kf)[TT][KL], const bf16x8_t (&q)[NT][KS],
+                                                f32x4 (&s)[NT][TT]) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const bf16x8_t kk = operand(kf[t], i);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[nt][i], s[nt][t], 0, 0, 0);
+      }
+      fence();
+    }
+  }
+
+  // O^T += V^T P^T.
+  static __device__ __forceinline__ void product(const u32x4 (&vf)[DT][VL], const bf16x8_t (&p)[NT][PS],
+                                                 f32x4 (&o)[NT][DT]) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+#pragma unroll
+      for (int i = 0; i < PS; ++i) {
+        const bf16x8_t vv = operand(vf[d], i);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, p[nt][i], o[nt][d], 0, 0, 0);
+      }
+      fence();
+    }
+  }
+
+  // Scores of tokens in pages that are none.
+  static __device__ __forceinline__ void spoil(uint32_t bad, int lane, f32x4 (&s)[NT][TT]) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const uint32_t grp = F8 ? lane >> 4 : 2 * (t / 2) + (lane >> 5);
+      if ((bad >> grp) & 1u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][t] = f32x4{NAN, NAN, NAN, NAN};
+      }
+    }
+  }
+
+  // One step of the running softmax of a query row: raw scores s to weights exp2(c (s - top)),
+  // in BF16 for the second product (8 bits, the type of V: 2^-8 of each weight), their FP32
+  // sum, and the old results faded where the maximum rose.  top is the same in the four
+  // lanes of a row, sum is each lane's own part.  A NaN score leaves the maximum alone and
+  // makes the sum NaN.
+  template <bool EDGE>
+  static __device__ __forceinline__ void weights(float c, uint32_t seen, f32x4 (&s)[TT], float& top, float& sum,
+                                                 f32x4 (&o)[DT], bf16x8_t (&p)[PS]) {
+    float mx = top;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, !EDGE || ((seen >> (4 * t + i)) & 1u) ? s[t][i] : -INFINITY);
+    mx = group_max(mx);
+    if (__any(mx > top)) {
+      const float fade = top == -INFINITY ? 0.f : pow2((top - mx) * c);
+      sum *= fade;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= fade;
+      top = mx;
+    }
+    const float base = mx == -INFINITY ? 0.f : mx * c;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = pow2(fmaf(s[t][i], c, -base));
+        s[t][i] = !EDGE || ((seen >> (4 * t + i)) & 1u) ? e : 0.f;
+        sum += s[t][i];
+      }
+#pragma unroll
+    for (int i = 0; i < PS; ++i) {
+      const f32x4 x = s[2 * i], y = s[2 * i + 1];
+      p[i] = __builtin_bit_cast(bf16x8_t, u32x4{bf_pack(x[0], x[1]), bf_pack(x[2], x[3]),
+                                                bf_pack(y[0], y[1]), bf_pack(y[2], y[3])});
+    }
+    fence();
+  }
+
+  // Bytes of the lane's dword w (0..3) of load s that hold tokens below `end` (from the
+  // lane's first token of the load).
+  static __device__ __forceinline__ uint32_t token_mask(int32_t left, int w) {
+    const int32_t n = left - (F8 ? 4 : 2) * w;   // tokens of this dword below the end
+    constexpr int per = F8 ? 4 : 2;
+    return n >= per ? 0xffffffffu : (n <= 0 ? 0u : (1u << (n * (F8 ? 8 : 16))) - 1u);
+  }
+};
+
+template <int D, bool F8, int NT, int NW, int UT>
+__global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
+  using A = Attn<D, F8, NT, NW, UT>;
+  constexpr int QT = A::QT, KS = A::KS, DT = A::DT, TT = A::TT, PS = A::PS, T = A::T;
+  // the waves' results of one 16-row tile, and later the (max, sum) pairs of an item's pieces
+  __shared__ __attribute__((aligned(16))) uint8_t s_buf[sizeof(float) * NW * 16 * A::ROW];
+  constexpr uint32_t kPairs = sizeof(s_buf) / sizeof(float2);
+  static_assert(kPairs >= kAttnWG, "one row of every piece");
+  auto& s_o = *reinterpret_cast<float (*)[NW][16][A::ROW]>(s_buf);
+  float2* const s_ml = reinterpret_cast<float2*>(s_buf);
+  __shared__ float s_m[NW][QT], s_l[NW][QT];
+  __shared__ uint32_t s_scan[NW], s_few[NW], s_items[NW], s_bad[NW];
+  __shared__ uint32_t s_start[5];
+  __shared__ uint32_t s_flag;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const uint32_t wave = uni(tid >> 6);
+  const uint32_t hkv = a.n_kv_heads, n_req = a.n_req;
+
+  auto request = [&](int32_t row0, int32_t row1, int32_t len) {
+    Req q;
+    q.row0 = row0;
+    q.len = len;
+    q.rows = (uint32_t)(row1 - row0);
+    q.broken = len < 0 || (uint64_t)len > ((uint64_t)a.max_pages << a.page_shift);
+    q.units = q.broken || len == 0 ? 1u : ((uint32_t)len + UT - 1) / UT;
+    q.tiles = (q.rows * a.group + QT - 1) / QT;
+    return q;
+  };
+
+  // ---- the line, and this workgroup's piece of it
+  const uint32_t per_t = (n_req + T - 1) / T;
+  auto mine_at = [&](uint32_t i) {   // this thread's i-th request
+    const uint32_t r = tid * per_t + i;
+    return r < n_req ? request(a.req_off[r], a.req_off[r + 1], a.kv_len[r]) : Req{0, 0, 0, false, 1, 0};
+  };
+  const Req mine_0 = mine_at(0);   // the only one up to T requests: loaded once
+  auto mine = [&](uint32_t i) { return i == 0 ? mine_0 : mine_at(i); };
+  uint32_t all_units = 0, few_units = 0, all_items = 0;   // with items of one tile, of NW tiles
+  // (the host layer keeps the whole line below 2^31)
   bool bad = false;
-  for (uint32_t r = lane; r <= a.n_req; r += 64) {
-    const int32_t o = a.req_off[r], before = r ? a.req_off[r - 1] : 0;
-    bad |= o < before || o > (int32_t)a.m;
+  for (uint32_t i = 0; i < per_t; ++i) {
+    const Req q = mine(i);
+    bad |= q.row0 < 0 || (int32_t)q.rows < 0 || (int64_t)q.row0 + q.rows > (int64_t)a.m;
+    all_units += q.tiles * hkv * q.units;
+    few_units += (q.tiles + NW - 1) / NW * hkv * q.units;
+    all_items += q.tiles * hkv;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    all_units += __shfl_xor(all_units, o);
+    few_units += __shfl_xor(few_units, o);
+    all_items += __shfl_xor(all_items, o);
   }
   bad = __any(bad);
-  const uint32_t ps = 1u << a.page_shift;
-  for (uint64_t w = blockIdx.x; w < (uint64_t)a.m * a.n_heads; w += gridDim.x) {
-    const uint32_t row = (uint32_t)(w / a.n_heads), h = (uint32_t)(w % a.n_heads), hk = h / a.group;
-    uint32_t r = 0;
-    int32_t len = -1, limit = 0;
-    if (!bad) {
-      if ((int32_t)row < a.req_off[0] || (int32_t)row >= a.req_off[a.n_req]) continue;
-      uint32_t lo = 1, hi = a.n_req;
-      while (lo < hi) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (a.req_off[mid] > (int32_t)row) hi = mid; else lo = mid + 1;
-      }
-      r = lo - 1;
-      len = a.kv_len[r];
-      limit = len - (a.req_off[r + 1] - (int32_t)row) + 1;
-    }
-    const bool broken = len < 0 || (uint64_t)len > (uint64_t)a.max_pages * ps;
-    if (broken) limit = 0;
-    __syncthreads();
-    for (int d = lane; d < D; d += 64) s_q[d] = bf(a.q[row * a.q_stride + (uint64_t)h * D + d]);
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f, acc[D / 64];
+  if (lane == 0) {
+    s_scan[wave] = all_units;
+    s_few[wave] = few_units;
+    s_items[wave] = all_items;
+    s_bad[wave] = bad;
+  }
+  __syncthreads();
+  all_units = few_units = all_items = 0;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) acc[i] = 0.f;
-    for (int32_t t0 = 0; t0 < limit; t0 += 64) {
-      const int32_t t = t0 + lane;
-      float s = -INFINITY;
-      if (t < limit) {
-        const int32_t page = a.table[(uint64_t)r * a.max_pages + ((uint32_t)t >> a.page_shift)];
-        if (page < 0 || (uint32_t)page >= a.n_pages) {
-          s = NAN;
-        } else {
-          const uint64_t at = (((uint64_t)page * a.n_kv_heads + hk) * ps + (t & (ps - 1))) * D;
-          s = 0.f;
-          for (int d = 0; d < D; ++d) s = fmaf(s_q[d], kv_value<F8>(a.kc, at + d), s);
-          s *= a.score_scale;
+  for (int w = 0; w < NW; ++w) {
+    all_units += uni(s_scan[w]);
+    few_units += uni(s_few[w]);
+    all_items += uni(s_items[w]);
+    bad |= uni(s_bad[w]) != 0;
+  }
+  if (bad) {   // no request table: NaN everywhere
+    for (uint64_t i = (uint64_t)blockIdx.x * T + tid; i < (uint64_t)a.m * a.n_heads * D; i += (uint64_t)gridDim.x * T) {
+      const uint64_t row = i / (a.n_heads * D);
+      a.out[row * a.out_stride + i % (a.n_heads * D)] = 0x7fc0u;
+    }
+    return;
+  }
+  // A long item is a tile, or, where there is work for every workgroup anyway, up to NW tiles of
+  // one head, one for each wave, so that K and V are read once for all of them (16 rows of 5
+  // heads each against 98k tokens: 207 us apart, 170 us together; but 8 heads of 1 to 4 rows
+  // against 10k tokens, 2 units per workgroup: 26 us apart, 36 us together).
+  const uint32_t span = all_units >= 16 * gridDim.x ? NW : 1u;   // tiles of a long item, at most
+  const uint32_t mean = min(((span > 1 ? few_units : all_units) + gridDim.x - 1) / gridDim.x, 1u << 20);
+  auto wide = [&](const Req& q) { return (q.tiles + span - 1) / span; };   // long items per head
+  // A long item has a lead of kLead places on the line, then one per unit; its units may fall
+  // into several pieces.  A brief one (few enough units that a wave does better with an
+  // item of its own than all waves one after the other: with k = mean / units items per
+  // piece, (k - 1) kLead >= units) is never cut: it belongs to the piece it begins in.
+  auto brief = [&](const Req& q) { return q.units < 4096 && q.units * (q.units + A::kLead) <= A::kLead * mean; };
+  auto lead = [&](const Req& q) { return brief(q) ? (A::kLead + NW - 1) / NW : A::kLead; };
+  auto places = [&](const Req& q) { return lead(q) + q.units; };   // of one item
+  auto items = [&](const Req& q) { return (brief(q) ? q.tiles : wide(q)) * hkv; };
+  uint32_t line = 0;
+  for (uint32_t i = 0; i < per_t; ++i) {
+    const Req q = mine(i);
+    line += items(q) * places(q);
+  }
+  uint32_t upto = line;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t v = __shfl_up(upto, o);
+    if (lane >= o) upto += v;
+  }
+  __syncthreads();
+  if (lane == 63) s_scan[wave] = upto;
+  __syncthreads();
+  uint32_t total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const uint32_t v = uni(s_scan[w]);
+    if (w < (int)wave) upto += v;
+    total += v;
+  }
+  // Equal pieces.  While there are more workgroups than needed a piece is as long as the join
+  // of an item's pieces pays for (with p of them the item takes units / p + p join_cost), and
+  // of at least 4 units, so that a workgroup's waves share an item before it is cut; but of
+  // no more than the mean item.
+  const float units = all_items ? (float)all_units / (float)all_items : 1.f;   // of the mean item
+  const uint32_t least = (uint32_t)fminf(units, fmaxf(4.f, __builtin_amdgcn_sqrtf(units * a.join_cost)));
+  const uint32_t per = uni(max((total + gridDim.x - 1) / gridDim.x, least));
+  uint32_t pos = blockIdx.x * per;
+  const uint32_t end = min(pos + per, total);
+  if (pos >= total) return;
+  if (pos >= upto - line && pos < upto) {   // one thread: the request it starts in
+    uint32_t at = upto - line;
+    uint32_t i = 0;
+    Req q = mine(0);
+    while (pos >= at + items(q) * places(q)) {
+      at += items(q) * places(q);
+      q = mine(++i);
+    }
+    s_start[0] = tid * per_t + i;
+    s_start[1] = at;
+    s_start[2] = (uint32_t)q.row0;
+    s_start[3] = q.rows;
+    s_start[4] = (uint32_t)q.len;
+  }
+  __syncthreads();
+  uint32_t r = uni(s_start[0]), start = uni(s_start[1]);   // a request and its place on the line
+
+  const float c = fabsf(a.score_scale);
+  const uint32_t flip = a.score_scale < 0.f ? 0x80008000u : 0u;
+  const __amdgpu_buffer_rsrc_t rs = ws_rsrc(a.partial);
+  constexpr uint32_t kSlot = NW * QT * (D + 2) * 4;   // bytes of one partial: values, then (max, sum)
+  auto load_req = [&](uint32_t i) {
+    return request(uniform_load(a.req_off, i), uniform_load(a.req_off, i + 1), uniform_load(a.kv_len, i));
+  };
+  Req now = request((int32_t)uni(s_start[2]), (int32_t)(uni(s_start[2]) + uni(s_start[3])), (int32_t)uni(s_start[4]));
+  // From item i of request r (which begins at place s): on to the k-th brief item, over
+  // requests without items; false if the piece or the run of brief items ends before.
+  auto skip = [&](uint32_t& i_r, uint32_t& s, Req& q, uint32_t& i, uint32_t k) {
+    i += k;
+    while (i >= items(q)) {
+      i -= items(q);
+      s += items(q) * places(q);
+      if (s >= end) return false;
+      q = load_req(++i_r);
+      if (q.tiles && !brief(q)) {
+        i = 0;
+        return false;
+      }
+    }
+    return s + i * places(q) < end;
+  };
+
+  while (pos < end) {
+    while (pos >= start + items(now) * places(now)) {
+      start += items(now) * places(now);
+      now = load_req(++r);
+    }
+    const bool alone = brief(now);   // a wave takes an item by itself
+    Req q = now;
+    uint32_t r_item, item, first = 0, ua = 0, ub;
+    if (alone) {
+      uint32_t at = start;
+      r_item = r;
+      item = (pos - start + places(now) - 1) / places(now);
+      uint32_t next = item;
+      const bool have = skip(r_item, at, q, item, wave);
+      skip(r, start, now, next, NW);
+      pos = start + next * places(now);
+      if (!have) continue;
+      ub = q.units;
+    } else {
+      const uint32_t len1 = places(now), ld = lead(now);
+      item = (pos - start) / len1;
+      first = start + item * len1;
+      const uint32_t la = pos - first, n_here = min(len1 - la, end - pos);
+      pos += n_here;
+      if (la + n_here <= ld) continue;   // only its lead falls into this piece
+      r_item = r;
+      ua = la > ld ? la - ld : 0u;
+      ub = la + n_here - ld;
+    }
+    {
+      // ---- units [ua, ub) of item (r_item, tile, head)
+      const int32_t row0 = q.row0;
+      const bool broken = q.broken;
+      // a wave's rows: a tile of its own; a long item of up to NW tiles deals its waves out to
+      // them, and waves of the same tile take units in turn
+      const uint32_t per_head = alone ? q.tiles : wide(q);
+      const uint32_t head = item / per_head, q0 = (item - head * per_head) * (alone ? 1u : span) * QT;
+      const uint32_t nq = min((alone ? 1u : span) * QT, q.rows * a.group - q0);
+      const uint32_t deal = alone || nq <= (uint32_t)QT ? 1u : (nq <= 2u * QT ? 2u : (uint32_t)NW);   // tiles dealt to
+      const uint32_t sub = alone ? 0u : wave & (deal - 1), turn = alone ? 0u : wave / deal;
+      const uint32_t stride = alone ? 1u : NW / deal;
+      const uint32_t qw = q0 + sub * QT, nw = nq > sub * QT ? min((uint32_t)QT, nq - sub * QT) : 0u;   // the wave's rows
+      const int32_t base = broken ? -(1 << 30) : q.len - (int32_t)q.rows + 1;   // what the request's row 0 sees
+      const int32_t see_min = base + (int32_t)(qw / a.group);
+      const int32_t see_max = nw ? base + (int32_t)((qw + nw - 1) / a.group) : 0;
+      // units past what the tile's last row sees are passed over
+      const uint32_t see = see_max > 0 ? (uint32_t)see_max : 0u;
+      const uint32_t uz = min(ub, (see + UT - 1) / UT);
+
+      int32_t lim[NT];
+      bf16x8_t qf[NT][KS];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t qi = qw + nt * 16 + (lane & 15);
+        const uint32_t row = qi / a.group, gq = qi - row * a.group;
+        const bool on = nt * 16 + (lane & 15) < (int)nw;
+        lim[nt] = on ? base + (int32_t)row : 0;
+        const uint16_t* p = a.q + (uint64_t)(row0 + (on ? row : 0u)) * a.q_stride +
+                            (uint64_t)(head * a.group + (on ? gq : 0u)) * D;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int d = F8 ? 64 * (s / 2) + 16 * (lane >> 4) + 8 * (s & 1) : 32 * s + 8 * (lane >> 4);
+          u32x4 w = *reinterpret_cast<const u32x4*>(p + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] ^= flip;
+          qf[nt][s] = __builtin_bit_cast(bf16x8_t, w);
         }
       }
-      float mx = s;
+      f32x4 o[NT][DT];
+      float top[NT], sum[NT];   // running maximum of the raw scores, this lane's part of the sum
 #pragma unroll
-      for (int o = 32; o; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-      const float now = fmaxf(top, mx);
-      const float base = now == -INFINITY ? 0.f : now;
-      const float fade = exp2f(top - base), p = t < limit ? exp2f(s - base) : 0.f;
-      top = now;
-      sum = sum * fade + p;
-      s_p[lane] = p;
+      for (int nt = 0; nt < NT; ++nt) {
+        top[nt] = -INFINITY;
+        sum[nt] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[nt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+
+      const uint64_t trow = (uint64_t)r_item * a.max_pages;
+      u32x4 kf[TT][A::KL], vf[DT][A::VL];
+      uint32_t u = ua + turn;
+      typename A::Ids ids = {{0u, 0u, 0u, 0u}, 0u};
+      if (u < uz) {
+        ids = A::load_ids(a, trow, u, see);
+        A::load_k(a, ids, u, head, lane, kf);
+        A::load_v(a, ids, u, head, lane, vf);
+      }
+      // full units: every row sees every token; the next unit's pages, K and V are requested as
+      // soon as the registers they go to are free
+      const uint32_t full = min(uz, see_min > 0 ? (uint32_t)see_min / UT : 0u);
+      for (; u < full; u += stride) {
+        const bool more = u + stride < uz;
+        typename A::Ids next = ids;
+        if (more) next = A::load_ids(a, trow, u + stride, see);
+        f32x4 s[NT][TT];
+        A::scores(kf, qf, s);
+        fence();
+        if (more) A::load_k(a, next, u + stride, head, lane, kf);
+        fence();
+        if (ids.bad) A::spoil(ids.bad, lane, s);
+        bf16x8_t p[NT][PS];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) A::template weights<false>(c, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
+        fence();
+        A::product(vf, p, o);
+        fence();
+        if (more) {
+          A::load_v(a, next, u + stride, head, lane, vf);
+          ids = next;
+        }
+      }
+      // units in which some row's tokens end
+      for (; u < uz; u += stride) {
+        f32x4 s[NT][TT];
+        A::scores(kf, qf, s);
+        if (ids.bad) A::spoil(ids.bad, lane, s);
+        const int32_t t_lane = (int32_t)(u * UT) + (F8 ? 16 : 8) * (lane >> 4);   // the lane's first token
+        bf16x8_t p[NT][PS];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t seen = 0;   // bit 4t + i: the row sees the token
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int32_t tok = t_lane + (F8 ? 4 * t + i : 32 * (t / 2) + 4 * (t & 1) + i);
+              seen |= tok < lim[nt] ? 1u << (4 * t + i) : 0u;
+            }
+          A::template weights<true>(c, seen, s[nt], top[nt], sum[nt], o[nt], p[nt]);
+        }
+        // What lies past a row's last token may be anything: zeros in its place.  Between the
+        // first row's last token and the last row's, a value that is not finite would reach
+        // rows that do not see it (0 * inf): then each row takes a product of its own.
+        uint32_t odd = 0;
+        if (see_min < see_max) {
+#pragma unroll
+          for (int l = 0; l < A::VL; ++l)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t look = A::token_mask((int32_t)see - (t_lane + 32 * l), w) &
+                                    ~A::token_mask(see_min - (t_lane + 32 * l), w) & (F8 ? 0x7f7f7f7fu : 0x7f807f80u);
+#pragma unroll
+              for (int d = 0; d < DT; ++d)   // E4M3 NaN: S.1111.111; BF16: exponent all ones
+                odd |= (vf[d][l][w] & look) + (F8 ? 0x01010101u : 0x00800080u);
+            }
+          odd &= F8 ? 0x80808080u : 0x80008000u;
+        }
+        const bool apart = __any(odd != 0);
+        for (int32_t row = apart ? max(see_min, 1) : see_max; row <= see_max; ++row) {
+          uint32_t keep[A::VL][4];
+#pragma unroll
+          for (int l = 0; l < A::VL; ++l)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) keep[l][w] = A::token_mask(row - (t_lane + 32 * l), w);
+          fence();
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            u32x4 x[A::VL];
+#pragma unroll
+            for (int l = 0; l < A::VL; ++l)
+#pragma unroll
+              for (int w = 0; w < 4; ++w) x[l][w] = vf[d][l][w] & keep[l][w];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              f32x4 sum_d = o[nt][d];
+#pragma unroll
+              for (int i = 0; i < PS; ++i)
+                sum_d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A::operand(x, i), p[nt][i], sum_d, 0, 0, 0);
+              if (!apart || lim[nt] == row) o[nt][d] = sum_d;   // a lane holds one row's sums
+            }
+            fence();
+          }
+        }
+        if (u + stride < uz) {
+          ids = A::load_ids(a, trow, u + stride, see);
+          A::load_k(a, ids, u + stride, head, lane, kf);
+          A::load_v(a, ids, u + stride, head, lane, vf);
+        }
+      }
+
+      // (values of the thread's place, hidden from the optimiser: it would compute what the
+      // join needs before the loops above and keep it there, in registers they have not got)
+      const int tj = opaque(tid), lj = tj & 63;
+      auto out_at = [&](uint32_t qi) {   // query row qi of the tile
+        const uint32_t row = (q0 + qi) / a.group, gq = q0 + qi - row * a.group;
+        return a.out + (uint64_t)(row0 + row) * a.out_stride + (uint64_t)(head * a.group + gq) * D;
+      };
+      auto scale_of = [&](uint32_t qi, float l) {
+        const int32_t sees = base + (int32_t)((q0 + qi) / a.group);
+        return broken ? NAN : (sees > 0 ? a.v_scale / l : 0.f);   // (without a token the values are 0)
+      };
+      auto put = [](uint16_t* p, f32x4 v, float f) {
+        *reinterpret_cast<u32x2*>(p) = u32x2{bf_pack(v[0] * f, v[1] * f), bf_pack(v[2] * f, v[3] * f)};
+      };
+      if (alone) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float l = group_sum(sum[nt]);
+          const uint32_t qi = nt * 16 + (lj & 15);
+          if (qi < nq) {
+            uint16_t* const p = out_at(qi) + 4 * (lj >> 4);
+            const float f = scale_of(qi, l);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) put(p + 16 * d, o[nt][d], f);
+          }
+        }
+        continue;
+      }
+
+      // ---- the waves' results joined in LDS, one 16-row tile at a time
+      const uint32_t real = first + lead(q);   // the item's first unit on the line
+      const uint32_t w0 = real / per, w1 = (real + q.units - 1) / per;
+      const bool whole = w0 == w1;
+      const uint32_t late = first > w0 * per ? 1u : 0u;   // the first piece's second partial
+      const uint32_t my_slot = (blockIdx.x * 2 + (blockIdx.x == w0 ? late : 0u)) * kSlot;
+      const uint32_t active = min(ub - ua, stride);   // waves of a tile that had a unit
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) acc[i] *= fade;
-      const int32_t n = min(64, limit - t0);
-      for (int32_t j = 0; j < n; ++j) {
-        const int32_t page = a.table[(uint64_t)r * a.max_pages + ((uint32_t)(t0 + j) >> a.page_shift)];
-        if (page < 0 || (uint32_t)page >= a.n_pages) continue;
-        const uint64_t at = ((uint64_t)page * a.n_kv_heads + hk) * D * ps + ((t0 + j) & (ps - 1));
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-          acc[i] = fmaf(s_p[j], kv_value<F8>(a.vc, at + (uint64_t)(lane + 64 * i) * ps), acc[i]);
+      for (int nt = 0; nt < NT; ++nt) {
+        const float l = group_sum(sum[nt]);
+        if (lj < 16) {
+          s_m[wave][nt * 16 + lj] = top[nt];
+          s_l[wave][nt * 16 + lj] = l;
+        }
       }
       __syncthreads();
-    }
 #pragma unroll
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt * 16 < (int)nq) {   // (uniform)
+          if (turn < active) {
+            float mx = -INFINITY;
+            for (uint32_t w = 0; w < active; ++w) mx = fmaxf(mx, s_m[sub + w * deal][nt * 16 + (lj & 15)]);
+            const float f = top[nt] == -INFINITY ? 1.f : pow2((top[nt] - mx) * c);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const float y = bad || broken ? NAN : (limit > 0 ? acc[i] / sum * a.v_scale : 0.f);
-      a.out[row * a.out_stride + (uint64_t)h * D + lane + 64 * i] = __builtin_bit_cast(uint16_t, (__bf16)y);
+            for (int d = 0; d < DT; ++d)
+              *reinterpret_cast<f32x4*>(&s_o[wave][lj & 15][16 * d + 4 * (lj >> 4)]) = o[nt][d] * f;
+          }
+          __syncthreads();
+          for (uint32_t e = tj; e < deal * (16 * (D / 4)); e += T) {
+            const uint32_t tile = e / (16 * (D / 4)), n = e / (D / 4) % 16, d = 4 * (e % (D / 4));
+            const uint32_t row = tile * QT + nt * 16 + n;   // of the item
+            if (row < nq) {
+              float m = -INFINITY, l = 0.f;
+              f32x4 v = {0.f, 0.f, 0.f, 0.f};
+              for (uint32_t w = 0; w < active; ++w) m = fmaxf(m, s_m[tile + w * deal][nt * 16 + n]);
+              for (uint32_t w = 0; w < active; ++w) {
+                const float t = s_m[tile + w * deal][nt * 16 + n], x = s_l[tile + w * deal][nt * 16 + n];
+                l += t == -INFINITY ? x : x * pow2((t - m) * c);   // (x is 0 or NaN without a maximum)
+                v += *reinterpret_cast<const f32x4*>(&s_o[tile + w * deal][n][d]);
+              }
+              if (whole) {
+                put(out_at(row) + d, v, scale_of(row, l));
+              } else {
+                st_dev4(rs, my_slot + (row * D + d) * 4, v);
+                if (d == 0) st_dev2(rs, my_slot + (NW * QT * D + 2 * row) * 4, m, l);
+              }
+            }
+          }
+          __syncthreads();
+        }
+      }
+      if (!whole) {
+        // ---- the item's last workgroup joins its pieces in order
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (tj == 0) {
+          const uint32_t old = __hip_atomic_fetch_add(a.tickets + w0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          const bool last = old == w1 - w0;
+          if (last) __hip_atomic_store(a.tickets + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          s_flag = last;
+        }
+        __syncthreads();
+        if (s_flag) {
+          // as many rows at a time as the pieces' maxima and sums leave room for in LDS
+          const uint32_t pieces = w1 - w0 + 1;   // at most kAttnWG
+          const uint32_t most = min(nq, kPairs / pieces);
+          auto slot_of = [&](uint32_t w) { return ((w0 + w) * 2 + (w == 0 ? late : 0u)) * kSlot; };
+          for (uint32_t n0 = 0; n0 < nq; n0 += most) {
+            const uint32_t rows = min(most, nq - n0);
+            for (uint32_t e = tj; e < pieces * rows; e += T) {
+              const uint32_t w = e / rows, n = n0 + e - w * rows;
+              const u32x2 ml = ld_dev2(rs, slot_of(w) + (NW * QT * D + 2 * n) * 4);
+              s_ml[e] = make_float2(__uint_as_float(ml[0]), __uint_as_float(ml[1]));
+            }
+            __syncthreads();
+            // into factors, by 16 lanes per row
+            for (uint32_t n = tj >> 4; n < rows; n += T / 16) {
+              float m = -INFINITY, l = 0.f;
+              for (uint32_t w = tj & 15; w < pieces; w += 16) m = fmaxf(m, s_ml[w * rows + n].x);
+#pragma unroll
+              for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+              for (uint32_t w = tj & 15; w < pieces; w += 16) {
+                const float2 ml = s_ml[w * rows + n];
+                const float f = ml.x == -INFINITY ? 1.f : pow2((ml.x - m) * c);
+                l += ml.y * f;
+                s_ml[w * rows + n].x = f;
+              }
+#pragma unroll
+              for (int o = 1; o < 16; o <<= 1) l += __shfl_xor(l, o);
+              if ((tj & 15) == 0) (&s_l[0][0])[n] = l;
+            }
+            __syncthreads();
+            // the values, PU places of a thread and B pieces of each in flight: another
+            // workgroup's write takes about 5000 cycles to read, and only the number of reads at
+            // once helps
+            constexpr uint32_t PU = QT * (D / 4) / T < 2 ? 1 : (QT * (D / 4) / T < 4 ? 2 : 4), B = 16 / PU;
+            const uint32_t n_places = rows * (D / 4);
+            for (uint32_t e = tj; e < n_places; e += PU * T) {
+              f32x4 v[PU];
+#pragma unroll
+              for (uint32_t i = 0; i < PU; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+              for (uint32_t w = 0; w < pieces; w += B) {
+                f32x4 x[PU][B];
+#pragma unroll
+                for (uint32_t i = 0; i < PU; ++i)
+                  if (e + i * T < n_places) {
+#pragma unroll
+                    for (uint32_t b = 0; b < B; ++b)
+                      if (w + b < pieces) x[i][b] = ld_dev4(rs, slot_of(w + b) + (n0 * (D / 4) + e + i * T) * 16);
+                  }
+#pragma unroll
+                for (uint32_t i = 0; i < PU; ++i)
+                  if (e + i * T < n_places) {
+#pragma unroll
+                    for (uint32_t b = 0; b < B; ++b)
+                      if (w + b < pieces) v[i] += x[i][b] * s_ml[(w + b) * rows + (e + i * T) / (D / 4)].x;
+                  }
+              }
+#pragma unroll
+              for (uint32_t i = 0; i < PU; ++i)
+                if (e + i * T < n_places) {
+                  const uint32_t n = (e + i * T) / (D / 4);
+                  put(out_at(n0 + n) + 4 * ((e + i * T) % (D / 4)), v[i], scale_of(n0 + n, (&s_l[0][0])[n]));
+                }
+            }
+            __syncthreads();
+          }
+        }
+        __syncthreads();
+      }
     }
   }
 }
 
-template <bool F8>
-hipError_t attn_launch(const AttnArgs& a, uint32_t d, hipStream_t s) {
-  const uint64_t all = (uint64_t)a.m * a.n_heads;
-  const dim3 g((uint32_t)(all < 65536 ? all : 65536)), b(64);
-  if (d == 64) hipLaunchKernelGGL((k_attn_simple<64, F8>), g, b, 0, s, a);
-  else if (d == 128) hipLaunchKernelGGL((k_attn_simple<128, F8>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((k_attn_simple<256, F8>), g, b, 0, s, a);
+template <int D, bool F8, int NT, int NW, int UT>
+hipError_t attn_go(const AttnArgs& a, hipStream_t s) {
+  // no more workgroups than units that the widest table could fill
+  const uint64_t tiles = ((uint64_t)a.m * a.group + (uint64_t)a.n_req * (16 * NT - 1)) / (16 * NT) + 1;
+  const uint64_t units = (((uint64_t)a.max_pages << a.page_shift) + UT - 1) / UT;
+  uint64_t wg = kAttnWG;
+  if (units < wg && tiles * a.n_kv_heads * units < wg) wg = tiles * a.n_kv_heads * units;
+  // What one more piece costs the join of an item, in units: a read's latency, and the values
+  // of its rows at 30 bytes per cycle against a unit's at 10.
+  const uint64_t mean = ((uint64_t)a.m + a.n_req - 1) / a.n_req * a.group;
+  AttnArgs b = a;
+  b.join_cost = 0.3f + (float)(mean < 16 * NT * NW ? mean : 16 * NT * NW) * 4.f / (6.f * UT * (F8 ? 1 : 2));
+  static_assert(kAttnWG * 2ull * NW * 16 * NT * (D + 2) * 4 <= W12_ATTN_WS_BYTES - kTicketBytes, "workspace");
+  static_assert(kAttnWG * 4 <= kTicketBytes, "tickets");
+  hipLaunchKernelGGL((k_attn<D, F8, NT, NW, UT>), dim3((uint32_t)wg), dim3(64 * NW), 0, s, b);
   return hipGetLastError();
+}
+
+// Tile of query rows by the mean number per request: 16 while it holds them, else 32 (what the
+// registers hold; with a head_dim of 256 that is 16).  Units of 64 tokens; of 32 where 64 do
+// not fit or fit only just (two BF16 tiles at 128: 24 requests of 25 query rows over 98k tokens
+// 95 us with 32, 99 us with 64; of 80 query rows, whose waves take a tile each and read the
+// same unit at once, 177 us with 32, 154 us with 64).
+template <int D, bool F8>
+hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
+  const uint64_t rows = ((uint64_t)a.m + a.n_req - 1) / a.n_req * a.group;
+  if constexpr (D < 256) {
+    if (rows > 16) {
+      if constexpr (D == 128 && !F8)
+        if (rows <= 32) return attn_go<D, F8, 2, 4, 32>(a, s);
+      return attn_go<D, F8, 2, 4, 64>(a, s);
+    }
+  }
+  return attn_go<D, F8, 1, 4, F8 || D < 256 ? 64 : 32>(a, s);
+}
+
+template <bool F8>
+hipError_t attn_dim(const AttnArgs& a, uint32_t d, hipStream_t s) {
+  if (d == 64) return attn_rows<64, F8>(a, s);
+  if (d == 128) return attn_rows<128, F8>(a, s);
+  return attn_rows<256, F8>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_attn_paged(const AttnArgs& a, uint32_t head_dim, uint32_t dtype, hipStream_t s) {
-  return dtype == W12_KV_E4M3 ? attn_launch<true>(a, head_dim, s) : attn_launch<false>(a, head_dim, s);
+  return dtype == W12_KV_E4M3 ? attn_dim<true>(a, head_dim, s) : attn_dim<false>(a, head_dim, s);
 }
 
 }  // namespace w12

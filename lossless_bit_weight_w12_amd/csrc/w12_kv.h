@@ -59,6 +59,7 @@ struct AttnArgs {
   uint32_t n_req;
   float score_scale;       // scale * k_scale * log2(e): scores in powers of two
   float v_scale;
+  float join_cost;         // of one more piece of an item, in units (set per kernel)
   uint16_t* out;
   uint32_t* tickets;       // workspace: 1024 tickets (zero before and after) ...
   float* partial;          // ... then the partial results

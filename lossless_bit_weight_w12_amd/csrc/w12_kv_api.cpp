@@ -144,6 +144,11 @@ w12_status w12_attn_paged(const uint16_t* q, uint64_t q_stride, uint32_t m, uint
   if (!slots_ok(max_pages, kv->page_size)) return W12_ERR_SHAPE;
   if (!stride_ok(q_stride, n_heads, d) || !stride_ok(out_stride, n_heads, d)) return W12_ERR_SHAPE;
   if (n_req < 1 || n_req > W12_MAX_REQ || m > W12_MAX_KV_ROWS) return W12_ERR_RANGE;
+  // Units of at least 32 tokens for tiles of at least 16 query rows, with up to 16 units of
+  // overhead each: their number stays below 2^31.
+  const uint64_t tokens = (uint64_t)max_pages * kv->page_size + 1024;   // < 2^31 + 2^10
+  const uint64_t qrows = (uint64_t)m * n_heads + 64ull * n_req * kv->n_kv_heads;   // < 2^31
+  if (qrows * tokens >= (1ull << 40)) return W12_ERR_RANGE;
   // scores in powers of two: exp(scale q.k) = exp2(score_scale q.code)
   const float score_scale = (float)((double)scale * (double)kv->k_scale * 1.4426950408889634);
   if (!isfinite(score_scale)) return W12_ERR_FORMAT;

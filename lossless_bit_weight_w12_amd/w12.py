@@ -1094,7 +1094,12 @@ class _PreparedOn(Prepared):
         self._device = device
 
     def __call__(self):
-        _issue(self.name, self._args, self._device)
+        torch = _torch()
+        if torch.cuda.current_device() == self._device.index:
+            super().__call__()
+        else:
+            with torch.cuda.device(self._device):
+                super().__call__()
 
 
 def prepare_kv_plan(pt: PageTable, length, req_off, kv_len, pos, slot) -> Prepared:
