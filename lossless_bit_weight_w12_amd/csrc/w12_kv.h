@@ -8,11 +8,11 @@
 namespace w12 {
 
 struct PlanArgs {
-  uint32_t n_pages, page_size, max_pages;
+  uint32_t n_pages, page_shift, max_pages;   // page_shift: log2(page_size)
   int32_t* table;          // [max_req][max_pages]
   int32_t* held;           // [max_req]
   int32_t* ring;           // [n_pages]
-  int32_t* state;          // [4]: head, count, 0, 0
+  int32_t* state;          // [4]: head, count, ticket (zero before and after), 0
   const int32_t* len;      // [n_req]
   const int32_t* req_off;  // [n_req + 1]
   uint32_t n_req, m;

@@ -65,7 +65,7 @@ w12_status w12_kv_plan(const w12_pages* p, const int32_t* len, const int32_t* re
     if (!aligned(a, 4)) return W12_ERR_ALIGN;
   PlanArgs a{};
   a.n_pages = p->n_pages;
-  a.page_size = p->page_size;
+  a.page_shift = log2u(p->page_size);
   a.max_pages = p->max_pages;
   a.table = p->table;
   a.held = p->held;

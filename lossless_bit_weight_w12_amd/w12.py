@@ -1089,32 +1089,35 @@ def prepare_verify_batched(x, t: W12Tensor, req_off, req_ndraft, draft, argmax_o
 class _PreparedOn(Prepared):
     """A prepared call that is issued with its tensors' device current."""
 
-    def __init__(self, name: str, args, keep, device):
-        super().__init__(name, getattr(lib(), name), args, keep)
+    def __init__(self, name: str, fn, args, keep, device):
+        super().__init__(name, fn, args, keep)
         self._device = device
 
     def __call__(self):
-        torch = _torch()
-        if torch.cuda.current_device() == self._device.index:
+        with _torch().cuda.device(self._device):
             super().__call__()
-        else:
-            with torch.cuda.device(self._device):
-                super().__call__()
+
+
+def _prepared(name: str, args, keep, device) -> Prepared:
+    fn = getattr(lib(), name)
+    if _torch().cuda.device_count() == 1:
+        return Prepared(name, fn, args, keep)
+    return _PreparedOn(name, fn, args, keep, device)
 
 
 def prepare_kv_plan(pt: PageTable, length, req_off, kv_len, pos, slot) -> Prepared:
     """kv_plan of m = pos.numel() rows into kv_len, pos and slot."""
     args, keep = _plan_args(pt, length, req_off, kv_len, pos, slot)
-    return _PreparedOn("w12_kv_plan", args, keep, pt.device)
+    return _prepared("w12_kv_plan", args, keep, pt.device)
 
 
 def prepare_qk_rope(q, k, v, cache: KvCache, rope: Rope, pos, slot, q_out) -> Prepared:
     args, keep = _rope_args(q, k, v, cache, rope, pos, slot, q_out)
-    return _PreparedOn("w12_qk_rope", args, keep, cache.device)
+    return _prepared("w12_qk_rope", args, keep, cache.device)
 
 
 def prepare_attn_paged(q, cache: KvCache, table, kv_len, req_off, out, scale=None, ws=None) -> Prepared:
     """attn_paged into out.  A captured prepared call keeps its workspace: graphs that may run
     at the same time are prepared with a ws of their own (attn_workspace)."""
     args, keep = _attn_args(q, cache, table, kv_len, req_off, out, scale, ws)
-    return _PreparedOn("w12_attn_paged", args, keep, cache.device)
+    return _prepared("w12_attn_paged", args, keep, cache.device)
