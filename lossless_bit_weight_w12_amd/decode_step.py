@@ -14,23 +14,47 @@ accepted-prefix length), which is the verification step of greedy speculative de
 in "StargazerX0/SpecPilot" (hotrepo.ai digest), section "Results and verification"; W12
 weights are read inside the GEMMs as in "SpecPilot: an agent doubled speculative
 decoding speed, and the 10.87x needs context", section "The mechanisms it found".
+
+With a DecodeAttention the step is a decoder's own: q and k are normed and turned per head and
+appended with v to the layer's paged cache (w12_qk_rope), the rows of every request attend over
+its cache (w12_attn_paged), and o reads that (o = attention W_o^T) in place of rms(q); the block
+tables are brought in line with the requests' lengths once per step (w12_kv_plan).
 """
 from __future__ import annotations
+
+from dataclasses import dataclass
 
 from . import w12
 
 MATS = ("q", "k", "v", "o", "gate", "up", "down")
 
 
+@dataclass
+class DecodeAttention:
+    """The attention of a DecodeStack: request r keeps length[r] tokens in the cache and its
+    new rows are req_off[r] .. req_off[r+1]-1 of the batch (int32 device tensors, read anew by
+    every step: after a verification add the accepted tokens and the one that follows them,
+    length += accepted + 1; the tokens rejected are overwritten by the next step)."""
+    n_heads: int
+    pages: object      # w12.PageTable, shared by the layers
+    caches: list       # w12.KvCache per layer
+    ropes: list        # w12.Rope per layer
+    length: object     # int32 [n_req]
+    req_off: object    # int32 [n_req + 1]
+    scale: float = None    # default head_dim ** -0.5
+
+
 class DecodeStack:
     """Layers: a list of dicts name -> W12Tensor (names as in MATS); head: W12Tensor of
-    the LM head.  All activation buffers are allocated once for m rows."""
+    the LM head.  All activation buffers are allocated once for m rows.  attention: a
+    DecodeAttention, or None for the chain without it."""
 
-    def __init__(self, layers, head, m: int, fused_rms: bool = True):
+    def __init__(self, layers, head, m: int, fused_rms: bool = True, attention=None):
         import torch
         if not layers:
             raise ValueError("empty layer stack")
         self.layers, self.head, self.m, self.fused_rms = layers, head, m, fused_rms
+        self.attention = attention
         hid = layers[0]["q"].k
         dev = head.device
         bf = dict(dtype=torch.bfloat16, device=dev)
@@ -42,8 +66,45 @@ class DecodeStack:
         self.h = torch.empty((m, hid), **bf)
         self.argmax = torch.empty(m, dtype=torch.int32, device=dev)
         self.accepted = torch.empty(1, dtype=torch.int32, device=dev)
+        if attention is not None:
+            self._attention_buffers(attention, dev)
 
-    def _layer_calls(self, L, first: bool):
+    def _attention_buffers(self, at, dev):
+        import torch
+        if len(at.caches) != len(self.layers) or len(at.ropes) != len(self.layers):
+            raise ValueError("DecodeAttention: one cache and one rope per layer")
+        for L, c in zip(self.layers, at.caches):
+            _, kv_heads, _, d = c.k.shape
+            if (L["q"].n, L["k"].n, L["v"].n, L["o"].k) != (at.n_heads * d, kv_heads * d, kv_heads * d, at.n_heads * d):
+                raise ValueError("DecodeAttention: the heads do not fit q, k, v and o")
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.kv_len = torch.empty_like(at.length)
+        self.pos, self.slot = torch.empty(self.m, **i32), torch.empty(self.m, **i32)
+        # rows of no request are left as they are by the attention: zeros, so that o stays finite
+        self.turned, self.a = torch.zeros_like(self.out["q"]), torch.zeros_like(self.a)
+        self.accepted = torch.empty(at.length.numel(), **i32)
+        self.attn_ws = w12.attn_workspace(dev)
+
+    def _attention_calls(self, li: int):
+        """Norm, rotation and append of the layer's heads, then the attention into self.a."""
+        at, o, c = self.attention, self.out, self.attention.caches[li]
+        heads = lambda t: t.view(self.m, -1, c.k.shape[3])
+        q = heads(self.turned)
+        return [w12.prepare_qk_rope(heads(o["q"]), heads(o["k"]), heads(o["v"]), c, at.ropes[li], self.pos,
+                                    self.slot, q),
+                w12.prepare_attn_paged(q, c, at.pages.table, self.kv_len, at.req_off, heads(self.a), at.scale,
+                                       self.attn_ws)]
+
+    def _layer_calls(self, L, first: bool, li: int):
+        calls = self._chain_calls(L, first)
+        if self.attention is None:
+            return calls
+        # o reads the attention's output as it is, where the chain reads rms(q)
+        after_o = 2 if self.fused_rms else 3
+        return (calls[:1] + self._attention_calls(li) + [w12.prepare_gemm(self.a, L["o"], self.out["o"])] +
+                calls[after_o:])
+
+    def _chain_calls(self, L, first: bool):
         o = self.out
         if self.fused_rms:
             # q, k, v read h (first layer) or the previous down through its RMS; o, gate/up
@@ -65,31 +126,46 @@ class DecodeStack:
                 w12.prepare_gemm(self.c, L["down"], o["down"]),
                 w12.prepare_rms(o["down"], self.h)]
 
-    def prepare(self, draft):
+    def prepare(self, draft, req_ndraft=None):
         """Marshal every call of the step once (on the current stream): the layers read
-        and write the stack's own buffers; the step starts from self.h."""
-        self.calls = [self._layer_calls(L, li == 0) for li, L in enumerate(self.layers)]
+        and write the stack's own buffers; the step starts from self.h.  With attention the
+        verification is of its requests: draft int32 [m], req_ndraft int32 [n_req] (see
+        w12.lmhead_verify_batched), accepted [n_req]."""
+        self.calls = [self._layer_calls(L, li == 0, li) for li, L in enumerate(self.layers)]
         if self.fused_rms:   # the final h, rescaled on its own for the LM head
             self.calls[-1].append(w12.prepare_rms(self.out["down"], self.h))
         self.draft = draft
-        self.verify_call = w12.prepare_verify(self.h, self.head, draft, self.argmax, self.accepted)
+        at = self.attention
+        if at is None:
+            self.verify_call = w12.prepare_verify(self.h, self.head, draft, self.argmax, self.accepted)
+            return
+        if req_ndraft is None:
+            raise ValueError("a step with attention verifies its requests: req_ndraft is missing")
+        self.plan_call = w12.prepare_kv_plan(at.pages, at.length, at.req_off, self.kv_len, self.pos, self.slot)
+        self.verify_call = w12.prepare_verify_batched(self.h, self.head, at.req_off, req_ndraft, draft,
+                                                      self.argmax, self.accepted)
 
     def run(self):
         """One step from the current contents of self.h (after prepare)."""
+        if self.attention is not None:
+            self.plan_call()
         for calls in self.calls:
             for c in calls:
                 c()
         self.verify_call()
 
-    def step(self, h0, draft, capture=()):
+    def step(self, h0, draft, capture=(), req_ndraft=None):
         """Run every layer from h0 [m, hidden] and verify `draft` on the final h.
         capture: layer indices whose GEMM inputs and outputs are cloned and returned as
-        {layer: {"in": {name: (input, rms applied)}, name: output for name in MATS}}.
+        {layer: {"in": {name: (input, rms applied)}, name: output for name in MATS}}; with
+        attention also "turned", q after norm and rotation.
         Returns (h, argmax, accepted, captured)."""
-        self.prepare(draft)
+        self.prepare(draft, req_ndraft)
         caps = {}
         self.h.copy_(h0)
         o = self.out
+        if self.attention is not None:
+            self.plan_call()
         for li, calls in enumerate(self.calls):
             if li in capture:
                 x_qkv = (self.h if li == 0 or not self.fused_rms else o["down"]).clone()
@@ -105,7 +181,11 @@ class DecodeStack:
                     ins = {"q": (x_qkv, False), "k": (x_qkv, False), "v": (x_qkv, False),
                            "o": (self.a.clone(), False), "gate": (self.b.clone(), False),
                            "up": (self.b.clone(), False), "down": (self.c.clone(), False)}
+                if self.attention is not None:
+                    ins["o"] = (self.a.clone(), False)
                 caps[li] = {"in": ins, **{k: v.clone() for k, v in o.items()}}
+                if self.attention is not None:
+                    caps[li]["turned"] = self.turned.clone()
         self.verify_call()
         return self.h, self.argmax, self.accepted, caps
 
@@ -115,7 +195,7 @@ class DecodeStack:
     def io_bytes(self) -> int:
         """Activation bytes the GEMMs, rescales and the verification read and write."""
         m = self.m
-        total = 0
+        total = 0      # (without the attention's: what it reads depends on the lengths)
         for L in self.layers:
             for name in MATS:
                 t = L[name]
