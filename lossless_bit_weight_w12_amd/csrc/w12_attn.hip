@@ -59,12 +59,52 @@ __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // Largest value (sum) over the four lanes that share a query row (l % 16).
 __device__ __forceinline__ float group_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 __device__ __forceinline__ float group_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Inclusive sum over the wave, lane 63 with all of it (row shifts by 1, 2, 4, 8, then the rows'
+// last lanes broadcast on).
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return v;
+}
+
+// Largest value (sum) over 16 lanes (a row of the wave), by rotations.
+template <int R>
+__device__ __forceinline__ float row_turn(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x120 + R, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, row_turn<8>(v));
+  v = fmaxf(v, row_turn<4>(v));
+  v = fmaxf(v, row_turn<2>(v));
+  return fmaxf(v, row_turn<1>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += row_turn<8>(v);
+  v += row_turn<4>(v);
+  v += row_turn<2>(v);
+  return v + row_turn<1>(v);
+}
+
+// x / d from inv = floor(2^32 / d) (2^32 - 1 for d = 1): the product is x / d or one below.
+__device__ __forceinline__ uint32_t div_by(uint32_t x, uint32_t d, uint32_t inv) {
+  const uint32_t q = (uint32_t)(((uint64_t)x * inv) >> 32);
+  return q + (x - q * d >= d ? 1u : 0u);
 }
 
 // Partial results pass between workgroups on any XCD, whose L2 caches are not coherent for
@@ -301,14 +341,14 @@ template <int D, bool F8, int NT, int NW, int UT>
 __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
   using A = Attn<D, F8, NT, NW, UT>;
   constexpr int QT = A::QT, KS = A::KS, DT = A::DT, TT = A::TT, PS = A::PS, T = A::T;
-  // the waves' results of one 16-row tile, and later the (max, sum) pairs of an item's pieces
-  __shared__ __attribute__((aligned(16))) uint8_t s_buf[sizeof(float) * NW * 16 * A::ROW];
+  // the waves' results, and later the (max, sum) pairs of an item's pieces
+  __shared__ __attribute__((aligned(16))) uint8_t s_buf[sizeof(float) * NT * NW * 16 * A::ROW];
   constexpr uint32_t kPairs = sizeof(s_buf) / sizeof(float2);
   static_assert(kPairs >= kAttnWG, "one row of every piece");
-  auto& s_o = *reinterpret_cast<float (*)[NW][16][A::ROW]>(s_buf);
+  auto& s_o = *reinterpret_cast<float (*)[NT][NW][16][A::ROW]>(s_buf);
   float2* const s_ml = reinterpret_cast<float2*>(s_buf);
   __shared__ float s_m[NW][QT], s_l[NW][QT];
-  __shared__ uint32_t s_scan[NW], s_few[NW], s_items[NW], s_bad[NW];
+  __shared__ uint32_t s_scan[NW], s_line[NW], s_few[NW], s_items[NW], s_bad[NW];
   __shared__ uint32_t s_start[5];
   __shared__ uint32_t s_flag;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -344,14 +384,11 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
     few_units += (q.tiles + NW - 1) / NW * hkv * q.units;
     all_items += q.tiles * hkv;
   }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    all_units += __shfl_xor(all_units, o);
-    few_units += __shfl_xor(few_units, o);
-    all_items += __shfl_xor(all_items, o);
-  }
+  all_units = wave_scan(all_units);
+  few_units = wave_scan(few_units);
+  all_items = wave_scan(all_items);
   bad = __any(bad);
-  if (lane == 0) {
+  if (lane == 63) {
     s_scan[wave] = all_units;
     s_few[wave] = few_units;
     s_items[wave] = all_items;
@@ -367,7 +404,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
     bad |= uni(s_bad[w]) != 0;
   }
   if (bad) {   // no request table: NaN everywhere
-    for (uint64_t i = (uint64_t)blockIdx.x * T + tid; i < (uint64_t)a.m * a.n_heads * D; i += (uint64_t)gridDim.x * T) {
+    for (uint64_t i = (uint64_t)blockIdx.x * T + tid; i < (uint64_t)a.m * a.n_heads * D; i += (uint64_t)a.grid * T) {
       const uint64_t row = i / (a.n_heads * D);
       a.out[row * a.out_stride + i % (a.n_heads * D)] = 0x7fc0u;
     }
@@ -377,9 +414,10 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
   // one head, one for each wave, so that K and V are read once for all of them (16 rows of 5
   // heads each against 98k tokens: 207 us apart, 170 us together; but 8 heads of 1 to 4 rows
   // against 10k tokens, 2 units per workgroup: 26 us apart, 36 us together).
-  const uint32_t span = all_units >= 16 * gridDim.x ? NW : 1u;   // tiles of a long item, at most
-  const uint32_t mean = min(((span > 1 ? few_units : all_units) + gridDim.x - 1) / gridDim.x, 1u << 20);
-  auto wide = [&](const Req& q) { return (q.tiles + span - 1) / span; };   // long items per head
+  auto per_grid = [&](uint32_t x) { return div_by(x, a.grid, a.grid_inv); };
+  const uint32_t span = all_units >= 16 * a.grid ? NW : 1u;   // tiles of a long item, at most
+  const uint32_t mean = min(per_grid((span > 1 ? few_units : all_units) + a.grid - 1), 1u << 20);
+  auto wide = [&](const Req& q) { return span > 1 ? (q.tiles + NW - 1) / NW : q.tiles; };   // long items per head
   // A long item has a lead of kLead places on the line, then one per unit; its units may fall
   // into several pieces.  A brief one (few enough units that a wave does better with an
   // item of its own than all waves one after the other: with k = mean / units items per
@@ -393,19 +431,13 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
     const Req q = mine(i);
     line += items(q) * places(q);
   }
-  uint32_t upto = line;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t v = __shfl_up(upto, o);
-    if (lane >= o) upto += v;
-  }
-  __syncthreads();
-  if (lane == 63) s_scan[wave] = upto;
+  uint32_t upto = wave_scan(line);
+  if (lane == 63) s_line[wave] = upto;
   __syncthreads();
   uint32_t total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const uint32_t v = uni(s_scan[w]);
+    const uint32_t v = uni(s_line[w]);
     if (w < (int)wave) upto += v;
     total += v;
   }
@@ -415,8 +447,9 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
   // no more than the mean item.
   const float units = all_items ? (float)all_units / (float)all_items : 1.f;   // of the mean item
   const uint32_t least = (uint32_t)fminf(units, fmaxf(4.f, __builtin_amdgcn_sqrtf(units * a.join_cost)));
-  const uint32_t per = uni(max((total + gridDim.x - 1) / gridDim.x, least));
-  uint32_t pos = blockIdx.x * per;
+  const uint32_t per = uni(max(per_grid(total + a.grid - 1), least));
+  const uint32_t here = blockIdx.x * per;   // where the piece begins
+  uint32_t pos = here;
   const uint32_t end = min(pos + per, total);
   if (pos >= total) return;
   if (pos >= upto - line && pos < upto) {   // one thread: the request it starts in
@@ -440,6 +473,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
   const uint32_t flip = a.score_scale < 0.f ? 0x80008000u : 0u;
   const __amdgpu_buffer_rsrc_t rs = ws_rsrc(a.partial);
   constexpr uint32_t kSlot = NW * QT * (D + 2) * 4;   // bytes of one partial: values, then (max, sum)
+  auto per_group = [&](uint32_t x) { return div_by(x, a.group, a.group_inv); };
   auto load_req = [&](uint32_t i) {
     return request(uniform_load(a.req_off, i), uniform_load(a.req_off, i + 1), uniform_load(a.kv_len, i));
   };
@@ -481,7 +515,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
       ub = q.units;
     } else {
       const uint32_t len1 = places(now), ld = lead(now);
-      item = (pos - start) / len1;
+      item = pos - start < len1 ? 0u : (pos - start) / len1;
       first = start + item * len1;
       const uint32_t la = pos - first, n_here = min(len1 - la, end - pos);
       pos += n_here;
@@ -497,15 +531,15 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
       // a wave's rows: a tile of its own; a long item of up to NW tiles deals its waves out to
       // them, and waves of the same tile take units in turn
       const uint32_t per_head = alone ? q.tiles : wide(q);
-      const uint32_t head = item / per_head, q0 = (item - head * per_head) * (alone ? 1u : span) * QT;
+      const uint32_t head = per_head == 1 ? item : item / per_head, q0 = (item - head * per_head) * (alone ? 1u : span) * QT;
       const uint32_t nq = min((alone ? 1u : span) * QT, q.rows * a.group - q0);
       const uint32_t deal = alone || nq <= (uint32_t)QT ? 1u : (nq <= 2u * QT ? 2u : (uint32_t)NW);   // tiles dealt to
       const uint32_t sub = alone ? 0u : wave & (deal - 1), turn = alone ? 0u : wave / deal;
       const uint32_t stride = alone ? 1u : NW / deal;
       const uint32_t qw = q0 + sub * QT, nw = nq > sub * QT ? min((uint32_t)QT, nq - sub * QT) : 0u;   // the wave's rows
       const int32_t base = broken ? -(1 << 30) : q.len - (int32_t)q.rows + 1;   // what the request's row 0 sees
-      const int32_t see_min = base + (int32_t)(qw / a.group);
-      const int32_t see_max = nw ? base + (int32_t)((qw + nw - 1) / a.group) : 0;
+      const int32_t see_min = base + (int32_t)per_group(qw);
+      const int32_t see_max = nw ? base + (int32_t)per_group(qw + nw - 1) : 0;
       // units past what the tile's last row sees are passed over
       const uint32_t see = see_max > 0 ? (uint32_t)see_max : 0u;
       const uint32_t uz = min(ub, (see + UT - 1) / UT);
@@ -515,7 +549,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint32_t qi = qw + nt * 16 + (lane & 15);
-        const uint32_t row = qi / a.group, gq = qi - row * a.group;
+        const uint32_t row = per_group(qi), gq = qi - row * a.group;
         const bool on = nt * 16 + (lane & 15) < (int)nw;
         lim[nt] = on ? base + (int32_t)row : 0;
         const uint16_t* p = a.q + (uint64_t)(row0 + (on ? row : 0u)) * a.q_stride +
@@ -645,11 +679,11 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
       // join needs before the loops above and keep it there, in registers they have not got)
       const int tj = opaque(tid), lj = tj & 63;
       auto out_at = [&](uint32_t qi) {   // query row qi of the tile
-        const uint32_t row = (q0 + qi) / a.group, gq = q0 + qi - row * a.group;
+        const uint32_t row = per_group(q0 + qi), gq = q0 + qi - row * a.group;
         return a.out + (uint64_t)(row0 + row) * a.out_stride + (uint64_t)(head * a.group + gq) * D;
       };
       auto scale_of = [&](uint32_t qi, float l) {
-        const int32_t sees = base + (int32_t)((q0 + qi) / a.group);
+        const int32_t sees = base + (int32_t)per_group(q0 + qi);
         return broken ? NAN : (sees > 0 ? a.v_scale / l : 0.f);   // (without a token the values are 0)
       };
       auto put = [](uint16_t* p, f32x4 v, float f) {
@@ -670,13 +704,13 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
         continue;
       }
 
-      // ---- the waves' results joined in LDS, one 16-row tile at a time
+      // ---- the waves' results joined in LDS
       const uint32_t real = first + lead(q);   // the item's first unit on the line
-      const uint32_t w0 = real / per, w1 = (real + q.units - 1) / per;
+      const uint32_t w0 = real >= here ? blockIdx.x : real / per;   // (it reaches into this piece)
+      const uint32_t w1 = real + q.units <= end ? blockIdx.x : (real + q.units - 1) / per;
       const bool whole = w0 == w1;
       const uint32_t late = first > w0 * per ? 1u : 0u;   // the first piece's second partial
       const uint32_t my_slot = (blockIdx.x * 2 + (blockIdx.x == w0 ? late : 0u)) * kSlot;
-      const uint32_t active = min(ub - ua, stride);   // waves of a tile that had a unit
       __syncthreads();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -685,42 +719,42 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
           s_m[wave][nt * 16 + lj] = top[nt];
           s_l[wave][nt * 16 + lj] = l;
         }
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          *reinterpret_cast<f32x4*>(&s_o[nt][wave][lj & 15][16 * d + 4 * (lj >> 4)]) = o[nt][d];
       }
       __syncthreads();
+      // a row's factors once, in place of the maxima
+      for (uint32_t row = tj; row < nq; row += T) {
+        const uint32_t tile = row / QT, n = row % QT;
+        float t[NW], m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt * 16 < (int)nq) {   // (uniform)
-          if (turn < active) {
-            float mx = -INFINITY;
-            for (uint32_t w = 0; w < active; ++w) mx = fmaxf(mx, s_m[sub + w * deal][nt * 16 + (lj & 15)]);
-            const float f = top[nt] == -INFINITY ? 1.f : pow2((top[nt] - mx) * c);
+        for (int j = 0; j < NW; ++j)   // the waves that share the tile
+          t[j] = j < (int)stride ? s_m[tile + j * deal][n] : -INFINITY;
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
-              *reinterpret_cast<f32x4*>(&s_o[wave][lj & 15][16 * d + 4 * (lj >> 4)]) = o[nt][d] * f;
+        for (int j = 0; j < NW; ++j) m = fmaxf(m, t[j]);
+#pragma unroll
+        for (int j = 0; j < NW; ++j)
+          if (j < (int)stride) {
+            const float f = t[j] == -INFINITY ? 1.f : pow2((t[j] - m) * c);   // (without a maximum: 0, or NaN that stays)
+            l += s_l[tile + j * deal][n] * f;
+            s_m[tile + j * deal][n] = f;
           }
-          __syncthreads();
-          for (uint32_t e = tj; e < deal * (16 * (D / 4)); e += T) {
-            const uint32_t tile = e / (16 * (D / 4)), n = e / (D / 4) % 16, d = 4 * (e % (D / 4));
-            const uint32_t row = tile * QT + nt * 16 + n;   // of the item
-            if (row < nq) {
-              float m = -INFINITY, l = 0.f;
-              f32x4 v = {0.f, 0.f, 0.f, 0.f};
-              for (uint32_t w = 0; w < active; ++w) m = fmaxf(m, s_m[tile + w * deal][nt * 16 + n]);
-              for (uint32_t w = 0; w < active; ++w) {
-                const float t = s_m[tile + w * deal][nt * 16 + n], x = s_l[tile + w * deal][nt * 16 + n];
-                l += t == -INFINITY ? x : x * pow2((t - m) * c);   // (x is 0 or NaN without a maximum)
-                v += *reinterpret_cast<const f32x4*>(&s_o[tile + w * deal][n][d]);
-              }
-              if (whole) {
-                put(out_at(row) + d, v, scale_of(row, l));
-              } else {
-                st_dev4(rs, my_slot + (row * D + d) * 4, v);
-                if (d == 0) st_dev2(rs, my_slot + (NW * QT * D + 2 * row) * 4, m, l);
-              }
-            }
-          }
-          __syncthreads();
-        }
+        s_l[tile][n] = l;
+        if (!whole) st_dev2(rs, my_slot + (NW * QT * D + 2 * row) * 4, m, l);
+      }
+      __syncthreads();
+#pragma unroll 2
+      for (uint32_t e = tj; e < nq * (D / 4); e += T) {
+        const uint32_t row = e / (D / 4), d = 4 * (e % (D / 4));   // of the item
+        const uint32_t tile = row / QT, nt = row % QT / 16, n = row % 16;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NW; ++j)
+          if (j < (int)stride)
+            v += *reinterpret_cast<const f32x4*>(&s_o[nt][tile + j * deal][n][d]) * s_m[tile + j * deal][nt * 16 + n];
+        if (whole) put(out_at(row) + d, v, scale_of(row, s_l[tile][nt * 16 + n]));
+        else st_dev4(rs, my_slot + (row * D + d) * 4, v);
       }
       if (!whole) {
         // ---- the item's last workgroup joins its pieces in order
@@ -738,49 +772,67 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
           const uint32_t pieces = w1 - w0 + 1;   // at most kAttnWG
           const uint32_t most = min(nq, kPairs / pieces);
           auto slot_of = [&](uint32_t w) { return ((w0 + w) * 2 + (w == 0 ? late : 0u)) * kSlot; };
+          // the values, PU places of a thread and B pieces of each in flight: another
+          // workgroup's write takes about 5000 cycles to read, and only the number of reads at
+          // once helps; the first ones are requested together with the maxima
+          constexpr uint32_t PU = QT * (D / 4) / T < 4 ? 1 : (NT == 1 ? 2 : 4), B = 16 / PU;
           for (uint32_t n0 = 0; n0 < nq; n0 += most) {
-            const uint32_t rows = min(most, nq - n0);
-            for (uint32_t e = tj; e < pieces * rows; e += T) {
-              const uint32_t w = e / rows, n = n0 + e - w * rows;
-              const u32x2 ml = ld_dev2(rs, slot_of(w) + (NW * QT * D + 2 * n) * 4);
-              s_ml[e] = make_float2(__uint_as_float(ml[0]), __uint_as_float(ml[1]));
-            }
-            __syncthreads();
-            // into factors, by 16 lanes per row
-            for (uint32_t n = tj >> 4; n < rows; n += T / 16) {
-              float m = -INFINITY, l = 0.f;
-              for (uint32_t w = tj & 15; w < pieces; w += 16) m = fmaxf(m, s_ml[w * rows + n].x);
+            const uint32_t rows = min(most, nq - n0), n_places = rows * (D / 4);
+            f32x4 x[PU][B];
+            auto request_values = [&](uint32_t e, uint32_t w) {
 #pragma unroll
-              for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+              for (uint32_t i = 0; i < PU; ++i)
+                if (e + i * T < n_places) {
+#pragma unroll
+                  for (uint32_t b = 0; b < B; ++b)
+                    if (w + b < pieces) x[i][b] = ld_dev4(rs, slot_of(w + b) + (n0 * (D / 4) + e + i * T) * 16);
+                }
+            };
+            request_values(tj, 0);
+            // 16 lanes per row: its pieces' maxima and sums, each lane's own kept in LDS, and
+            // turned into factors there; two rows at once
+            for (uint32_t n1 = tj >> 4; n1 < rows; n1 += 2 * T / 16) {
+              float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll 2
               for (uint32_t w = tj & 15; w < pieces; w += 16) {
-                const float2 ml = s_ml[w * rows + n];
-                const float f = ml.x == -INFINITY ? 1.f : pow2((ml.x - m) * c);
-                l += ml.y * f;
-                s_ml[w * rows + n].x = f;
+                u32x2 ml[2];
+#pragma unroll
+                for (uint32_t k = 0; k < 2; ++k)
+                  if (n1 + k * (T / 16) < rows)
+                    ml[k] = ld_dev2(rs, slot_of(w) + (NW * QT * D + 2 * (n0 + n1 + k * (T / 16))) * 4);
+#pragma unroll
+                for (uint32_t k = 0; k < 2; ++k)
+                  if (n1 + k * (T / 16) < rows) {
+                    s_ml[w * rows + n1 + k * (T / 16)] = make_float2(__uint_as_float(ml[k][0]), __uint_as_float(ml[k][1]));
+                    m[k] = fmaxf(m[k], __uint_as_float(ml[k][0]));
+                  }
               }
 #pragma unroll
-              for (int o = 1; o < 16; o <<= 1) l += __shfl_xor(l, o);
-              if ((tj & 15) == 0) (&s_l[0][0])[n] = l;
+              for (uint32_t k = 0; k < 2; ++k) m[k] = row_max(m[k]);
+              for (uint32_t w = tj & 15; w < pieces; w += 16)
+#pragma unroll
+                for (uint32_t k = 0; k < 2; ++k)
+                  if (n1 + k * (T / 16) < rows) {
+                    const float2 ml = s_ml[w * rows + n1 + k * (T / 16)];
+                    const float f = ml.x == -INFINITY ? 1.f : pow2((ml.x - m[k]) * c);
+                    l[k] += ml.y * f;
+                    s_ml[w * rows + n1 + k * (T / 16)].x = f;
+                  }
+#pragma unroll
+              for (uint32_t k = 0; k < 2; ++k) {
+                const float all = row_sum(l[k]);
+                if ((tj & 15) == 0 && n1 + k * (T / 16) < rows) (&s_l[0][0])[n1 + k * (T / 16)] = all;
+              }
             }
             __syncthreads();
-            // the values, PU places of a thread and B pieces of each in flight: another
-            // workgroup's write takes about 5000 cycles to read, and only the number of reads at
-            // once helps
-            constexpr uint32_t PU = QT * (D / 4) / T < 2 ? 1 : (QT * (D / 4) / T < 4 ? 2 : 4), B = 16 / PU;
-            const uint32_t n_places = rows * (D / 4);
+            bool there = true;   // the first values were requested above
             for (uint32_t e = tj; e < n_places; e += PU * T) {
               f32x4 v[PU];
 #pragma unroll
               for (uint32_t i = 0; i < PU; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
               for (uint32_t w = 0; w < pieces; w += B) {
-                f32x4 x[PU][B];
-#pragma unroll
-                for (uint32_t i = 0; i < PU; ++i)
-                  if (e + i * T < n_places) {
-#pragma unroll
-                    for (uint32_t b = 0; b < B; ++b)
-                      if (w + b < pieces) x[i][b] = ld_dev4(rs, slot_of(w + b) + (n0 * (D / 4) + e + i * T) * 16);
-                  }
+                if (!there) request_values(e, w);
+                there = false;
 #pragma unroll
                 for (uint32_t i = 0; i < PU; ++i)
                   if (e + i * T < n_places) {
@@ -819,6 +871,8 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t s) {
   b.join_cost = 0.3f + (float)(mean < 16 * NT * NW ? mean : 16 * NT * NW) * 4.f / (6.f * UT * (F8 ? 1 : 2));
   static_assert(kAttnWG * 2ull * NW * 16 * NT * (D + 2) * 4 <= W12_ATTN_WS_BYTES - kTicketBytes, "workspace");
   static_assert(kAttnWG * 4 <= kTicketBytes, "tickets");
+  b.grid = (uint32_t)wg;
+  b.grid_inv = wg == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / wg);
   hipLaunchKernelGGL((k_attn<D, F8, NT, NW, UT>), dim3((uint32_t)wg), dim3(64 * NW), 0, s, b);
   return hipGetLastError();
 }

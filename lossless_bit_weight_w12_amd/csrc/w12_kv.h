@@ -49,6 +49,7 @@ struct AttnArgs {
   const uint16_t* q;
   uint64_t q_stride, out_stride;   // elements
   uint32_t m, n_heads, n_kv_heads, group;   // group = n_heads / n_kv_heads
+  uint32_t group_inv;      // floor(2^32 / group), 2^32 - 1 for 1
   uint32_t n_pages, page_shift;
   const uint8_t* kc;
   const uint8_t* vc;
@@ -59,7 +60,9 @@ struct AttnArgs {
   uint32_t n_req;
   float score_scale;       // scale * k_scale * log2(e): scores in powers of two
   float v_scale;
-  float join_cost;         // of one more piece of an item, in units (set per kernel)
+  // set per kernel:
+  float join_cost;         // of one more piece of an item, in units
+  uint32_t grid, grid_inv; // workgroups, and their inverse as group_inv
   uint16_t* out;
   uint32_t* tickets;       // workspace: 1024 tickets (zero before and after) ...
   float* partial;          // ... then the partial results

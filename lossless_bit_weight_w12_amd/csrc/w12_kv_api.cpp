@@ -165,6 +165,7 @@ w12_status w12_attn_paged(const uint16_t* q, uint64_t q_stride, uint32_t m, uint
   a.n_heads = n_heads;
   a.n_kv_heads = kv->n_kv_heads;
   a.group = n_heads / kv->n_kv_heads;
+  a.group_inv = a.group == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / a.group);
   a.n_pages = kv->n_pages;
   a.page_shift = log2u(kv->page_size);
   a.kc = (const uint8_t*)kv->k;
