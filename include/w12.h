@@ -444,7 +444,7 @@ typedef struct w12_pages {
   uint32_t n_pages;       /* pages of the pool; n_pages * page_size < 2^31 */
   uint32_t page_size;     /* 16, 32, 64, 128 or 256 tokens */
   uint32_t max_req;       /* rows of the table, 1..W12_MAX_REQ */
-  uint32_t max_pages;     /* entries of a table row; max_pages * page_size < 2^31 */
+  uint32_t max_pages;     /* entries of a table row; max_pages * page_size <= 2^30 */
   int32_t* table;         /* device [max_req][max_pages] page ids */
   int32_t* held;          /* device [max_req] pages each request holds */
   int32_t* ring;          /* device [n_pages] free page ids */
@@ -507,7 +507,8 @@ typedef struct w12_rope {
  * cache alone.  The slots of one call are distinct (of rows that share one, either's
  * values stay).  m = 0 does nothing.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (cache geometry,
  * n_heads outside 1..W12_MAX_HEADS or no multiple of n_kv_heads, rot_dim, strides);
- * W12_ERR_RANGE (m > W12_MAX_KV_ROWS); W12_ERR_FORMAT (dtype, scales, eps, interleaved);
+ * W12_ERR_RANGE (m > W12_MAX_KV_ROWS, m * n_kv_heads >= 2^26); W12_ERR_FORMAT (dtype, scales,
+ * eps, interleaved);
  * W12_ERR_ALIGN (pointers 16 bytes, pos and slot 4, inv_freq 8). */
 w12_status w12_qk_rope(const uint16_t* q, uint64_t q_stride, const uint16_t* k, uint64_t k_stride,
                        const uint16_t* v, uint64_t v_stride, uint32_t m, uint32_t n_heads,
@@ -530,7 +531,7 @@ w12_status w12_qk_rope(const uint16_t* q, uint64_t q_stride, const uint16_t* k, 
  * 256-byte aligned, beginning with 4096 bytes of tickets that must be zero before its first
  * use (w12_workspace_init) and that every call leaves zero; calls sharing a workspace must be
  * ordered.  m = 0 does nothing.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (cache geometry, heads,
- * max_pages * page_size >= 2^31, strides); W12_ERR_RANGE (n_req outside 1..W12_MAX_REQ, m >
+ * max_pages * page_size > 2^30, strides); W12_ERR_RANGE (n_req outside 1..W12_MAX_REQ, m >
  * W12_MAX_KV_ROWS, (m * n_heads + 64 * n_req * n_kv_heads) * (max_pages * page_size + 1024) >=
  * 2^40); W12_ERR_FORMAT (dtype, scales, scale not finite); W12_ERR_WORKSPACE;
  * W12_ERR_ALIGN. */

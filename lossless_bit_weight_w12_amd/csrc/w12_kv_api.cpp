@@ -19,6 +19,11 @@ inline bool slots_ok(uint32_t pages, uint32_t page_size) {
   return pages > 0 && (uint64_t)pages * page_size < (1ull << 31);
 }
 
+// Tokens of one request: positions and the ends of 64-token units stay below 2^31.
+inline bool length_ok(uint32_t pages, uint32_t page_size) {
+  return pages > 0 && (uint64_t)pages * page_size <= (1ull << 30);
+}
+
 inline uint32_t log2u(uint32_t v) {
   uint32_t s = 0;
   while ((1u << s) < v) ++s;
@@ -56,7 +61,7 @@ w12_status w12_kv_plan(const w12_pages* p, const int32_t* len, const int32_t* re
     return W12_ERR_NULL;
   if (m > 0 && (!pos || !slot)) return W12_ERR_NULL;
   if (!page_size_ok(p->page_size) || !slots_ok(p->n_pages, p->page_size) ||
-      !slots_ok(p->max_pages, p->page_size) || p->max_req < 1 || p->max_req > W12_MAX_REQ)
+      !length_ok(p->max_pages, p->page_size) || p->max_req < 1 || p->max_req > W12_MAX_REQ)
     return W12_ERR_SHAPE;
   if (n_req < 1 || n_req > p->max_req || m > W12_MAX_KV_ROWS) return W12_ERR_RANGE;
   for (const void* a : {(const void*)len, (const void*)req_off, (const void*)kv_len, (const void*)pos,
@@ -95,7 +100,7 @@ w12_status w12_qk_rope(const uint16_t* q, uint64_t q_stride, const uint16_t* k, 
   if (!stride_ok(q_stride, n_heads, d) || !stride_ok(q_out_stride, n_heads, d) ||
       !stride_ok(k_stride, kv->n_kv_heads, d) || !stride_ok(v_stride, kv->n_kv_heads, d))
     return W12_ERR_SHAPE;
-  if (m > W12_MAX_KV_ROWS) return W12_ERR_RANGE;
+  if (m > W12_MAX_KV_ROWS || (uint64_t)m * kv->n_kv_heads >= (1ull << 26)) return W12_ERR_RANGE;
   if (rope->interleaved > 1 || !(rope->eps >= 0.f) || !isfinite(rope->eps)) return W12_ERR_FORMAT;
   for (const void* a : {(const void*)q, (const void*)k, (const void*)v, (const void*)q_out,
                         (const void*)rope->q_norm, (const void*)rope->k_norm})
@@ -141,12 +146,12 @@ w12_status w12_attn_paged(const uint16_t* q, uint64_t q_stride, uint32_t m, uint
   const w12_status st = check_kv(kv, n_heads);
   if (st != W12_OK) return st;
   const uint32_t d = kv->head_dim;
-  if (!slots_ok(max_pages, kv->page_size)) return W12_ERR_SHAPE;
+  if (!length_ok(max_pages, kv->page_size)) return W12_ERR_SHAPE;
   if (!stride_ok(q_stride, n_heads, d) || !stride_ok(out_stride, n_heads, d)) return W12_ERR_SHAPE;
   if (n_req < 1 || n_req > W12_MAX_REQ || m > W12_MAX_KV_ROWS) return W12_ERR_RANGE;
   // Units of at least 32 tokens for tiles of at least 16 query rows, with up to 16 units of
   // overhead each: their number stays below 2^31.
-  const uint64_t tokens = (uint64_t)max_pages * kv->page_size + 1024;   // < 2^31 + 2^10
+  const uint64_t tokens = (uint64_t)max_pages * kv->page_size + 1024;   // <= 2^30 + 2^10
   const uint64_t qrows = (uint64_t)m * n_heads + 64ull * n_req * kv->n_kv_heads;   // < 2^31
   if (qrows * tokens >= (1ull << 40)) return W12_ERR_RANGE;
   // scores in powers of two: exp(scale q.k) = exp2(score_scale q.code)

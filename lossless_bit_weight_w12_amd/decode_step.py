@@ -74,7 +74,9 @@ class DecodeStack:
         if len(at.caches) != len(self.layers) or len(at.ropes) != len(self.layers):
             raise ValueError("DecodeAttention: one cache and one rope per layer")
         for L, c in zip(self.layers, at.caches):
-            _, kv_heads, _, d = c.k.shape
+            n_pages, kv_heads, page_size, d = c.k.shape
+            if page_size != at.pages.page_size or n_pages < at.pages.n_pages:
+                raise ValueError("DecodeAttention: a cache does not hold the pool's pages")
             if (L["q"].n, L["k"].n, L["v"].n, L["o"].k) != (at.n_heads * d, kv_heads * d, kv_heads * d, at.n_heads * d):
                 raise ValueError("DecodeAttention: the heads do not fit q, k, v and o")
         i32 = dict(dtype=torch.int32, device=dev)

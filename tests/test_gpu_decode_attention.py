@@ -133,7 +133,9 @@ def test_decode_attention_refusals():
     stack, at, *_ = build(g, True, False, sum(ROWS))
     with pytest.raises(ValueError, match="req_ndraft"):
         stack.prepare(i32(np.zeros(sum(ROWS))))
-    for change in (dict(caches=at.caches[:1]), dict(ropes=[]), dict(n_heads=8)):
+    other = w12.kv_cache(64, 32, HKV, D, device=DEV)
+    for change in (dict(caches=at.caches[:1]), dict(ropes=[]), dict(n_heads=8), dict(caches=[other] * NL),
+                   dict(caches=[w12.kv_cache(63, PAGE, HKV, D, device=DEV)] * NL)):
         bad = DecodeAttention(**{**at.__dict__, **change})
         with pytest.raises(ValueError):
             DecodeStack(stack.layers, stack.head, sum(ROWS), attention=bad)

@@ -343,6 +343,11 @@ ATTN = [  # lens, rows, hq, hkv, d, page, f8
     ([3000, 900], [5, 5], 14, 2, 64, 32, True),
     ([333], [90], 7, 1, 128, 32, True),
     ([777, 778], [40, 33], 4, 2, 256, 32, False),
+    ([50], [2], 128, 1, 64, 16, False),
+    ([2000], [3], 96, 1, 128, 16, True),
+    ([9000, 5000], [16, 9], 40, 8, 128, 16, False),
+    ([9000, 5000], [16, 9], 40, 8, 128, 16, True),
+    ([6000, 4000], [4, 4], 32, 4, 256, 64, False),
 ]
 
 
@@ -359,6 +364,41 @@ def test_attention_many_requests(d, f8):
     g = np.random.default_rng([22, d])
     rows = g.integers(0, 5, 300)
     Ctx(g, g.integers(0, 400, 300), rows, 4, 2, d, 16, f8).check()
+
+
+def test_attention_most_requests():
+    """4096 requests, most without rows or tokens, a few long ones among them."""
+    g = np.random.default_rng(32)
+    rows = (g.random(4096) < 0.05).astype(int) * g.integers(1, 4, 4096)
+    lens = np.where(g.random(4096) < 0.5, 0, g.integers(0, 40, 4096))
+    lens[[7, 2000, 4095]], rows[[7, 2000, 4095]] = [3000, 1, 1500], [2, 1, 20]
+    Ctx(g, lens, rows, 2, 1, 64, 16, extra=0).check()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_attention_queries_stay_apart(f8):
+    """NaN and infinity in one query row: the others are as they were, bit for bit."""
+    g = np.random.default_rng(33)
+    x = Ctx(g, [200, 70], [5, 2], 10, 2, 128, 16, f8)
+    clean = x.run().clone()
+    x.q[2, 3, 7], x.q[6, 0, 0] = float("nan"), float("inf")
+    got = x.run()
+    keep = torch.ones_like(got, dtype=torch.bool)
+    keep[2, 3], keep[6, 0] = False, False
+    assert torch.equal(got[keep], clean[keep]) and torch.isnan(got[2, 3]).all()
+
+
+def test_attention_longest_table():
+    """A length of 2^24 tokens through a table whose pages repeat: 16 different pages, so the
+    result is that of 256 tokens (every weight 2^16 times)."""
+    g = np.random.default_rng(34)
+    x = Ctx(g, [256], [1], 2, 1, 64, 16, peak=1.0)
+    want, tol = ko.attention(host(x.q), host(x.c.k), host(x.c.v), x.table, x.lens, x.off, 0.125)
+    x.table = np.tile(x.table[:, :16], (1, 1 << 16))
+    x.lens = [1 << 24]
+    # 2^18 units over 1024 waves: a lane adds 16 weights of each of 256 units, then waves and
+    # pieces; below 2^13 roundings of 2^-23 (tol allows 256) of a sum of w |v| <= max |v|
+    assert (np.abs(host(x.run()) - want) <= tol + 2.0 ** -10 * np.abs(host(x.c.v)).max()).all()
 
 
 def test_attention_rows_before_the_first_token():

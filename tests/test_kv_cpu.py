@@ -124,7 +124,7 @@ def test_plan_refusals(L):
         assert plan(L, pages(**{name: None})) == NULL, name
         assert plan(L, pages(**{name: FAKE + 2})) == ALIGN, name
     for kw in (dict(page_size=0), dict(page_size=8), dict(page_size=48), dict(page_size=512),
-               dict(n_pages=0), dict(n_pages=1 << 27), dict(max_pages=0), dict(max_pages=1 << 27),
+               dict(n_pages=0), dict(n_pages=1 << 27), dict(max_pages=0), dict(max_pages=(1 << 26) + 1),
                dict(max_req=0), dict(max_req=4097)):
         assert plan(L, pages(**kw)) == SHAPE, kw
     assert plan(L, n_req=0) == RANGE and plan(L, n_req=9) == RANGE
@@ -184,6 +184,7 @@ def test_qk_rope_refusals(L):
                dict(os_=1 << 40), dict(heads=0), dict(heads=7), dict(heads=1026)):
         assert qk(L, **kw) == SHAPE, kw
     assert qk(L, m=(1 << 20) + 1) == RANGE
+    assert qk(L, kv(n_kv_heads=64), heads=64, qs=8192, ks=8192, vs=8192, os_=8192, m=1 << 20) == RANGE
     for kw in (dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(interleaved=2)):
         assert qk(L, r=rope(**kw)) == FORMAT, kw
     for kw in (dict(q=FAKE + 8), dict(k=FAKE + 2), dict(v=FAKE + 8), dict(out=FAKE + 8), dict(pos=FAKE + 2),
@@ -207,10 +208,11 @@ def test_attn_refusals(L):
         assert attn(L, **kw) == NULL, kw
     for kw, st in BAD_CACHE:
         assert attn(L, kv(**kw)) == st, kw
-    for kw in (dict(max_pages=0), dict(max_pages=1 << 27), dict(qs=1016), dict(qs=1030), dict(os_=0),
+    for kw in (dict(max_pages=0), dict(max_pages=(1 << 26) + 1), dict(qs=1016), dict(qs=1030), dict(os_=0),
                dict(heads=0), dict(heads=9), dict(heads=1026)):
         assert attn(L, **kw) == SHAPE, kw
-    for kw in (dict(n_req=0), dict(n_req=4097), dict(m=(1 << 20) + 1)):
+    for kw in (dict(n_req=0), dict(n_req=4097), dict(m=(1 << 20) + 1), dict(max_pages=1 << 26, m=128),
+               dict(m=1 << 20, max_pages=8192)):
         assert attn(L, **kw) == RANGE, kw
     for s in (float("nan"), float("inf"), 3e38):
         assert attn(L, scale=s) == FORMAT, s
