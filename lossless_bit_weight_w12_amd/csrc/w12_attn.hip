@@ -31,7 +31,13 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-constexpr uint32_t kAttnWG = 256;       // workgroups of a launch, at most (one ticket each)
+// Workgroups of a launch, at most (one ticket each): one per CU; with one tile of query rows, so
+// that the registers allow it, two or four where a unit's K and V (`bytes`) are so small that
+// four waves do not keep enough reads in flight (64 requests of up to 8191 tokens with heads of
+// 64: in BF16 117 -> 109 us with two, in E4M3 90 -> 71 us with two, 67 us with four).
+constexpr uint32_t workgroups(int nt, int bytes) {
+  return nt > 1 || bytes > 16384 ? 256 : (bytes > 8192 ? 512 : 1024);
+}
 constexpr uint32_t kTicketBytes = 4096;
 
 __device__ __forceinline__ int32_t uniform_load(const int32_t* p, uint64_t i) {
@@ -137,6 +143,15 @@ struct Req {
   uint32_t tiles;    // tiles of query rows, per key head
 };
 
+// One item (request, tiles, head) as its output needs it, and its pieces if it is cut.
+struct Item {
+  int32_t row0;          // the request's first row
+  int32_t base;          // tokens that row sees
+  bool broken;
+  uint32_t head, q0, nq; // query rows q0 .. q0 + nq - 1 of the head
+  uint32_t w0, w1, late; // workgroups with a piece; 1: the first one's second partial
+};
+
 template <int D, bool F8, int NT, int NW, int UT>
 struct Attn {
   static constexpr int ES = F8 ? 1 : 2;          // bytes per cached value
@@ -149,6 +164,7 @@ struct Attn {
   static constexpr int VL = F8 ? PS / 2 : PS;    // 16-byte loads of one dimension of V per lane
   static constexpr int ROW = D + 4;              // LDS row of the join, padded
   static constexpr int T = 64 * NW;
+  static constexpr uint32_t kWG = workgroups(NT, 2 * UT * D * ES);
   // What an item costs a workgroup beside its units (its queries' load, the join, the writes:
   // about 15000 cycles under load, the time of 128 KB), in units.
   static constexpr uint32_t kLead = 131072 / (2 * UT * D * ES);
@@ -338,19 +354,20 @@ struct Attn {
 };
 
 template <int D, bool F8, int NT, int NW, int UT>
-__global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) / 256) void k_attn(AttnArgs a) {
   using A = Attn<D, F8, NT, NW, UT>;
   constexpr int QT = A::QT, KS = A::KS, DT = A::DT, TT = A::TT, PS = A::PS, T = A::T;
   // the waves' results, and later the (max, sum) pairs of an item's pieces
   __shared__ __attribute__((aligned(16))) uint8_t s_buf[sizeof(float) * NT * NW * 16 * A::ROW];
   constexpr uint32_t kPairs = sizeof(s_buf) / sizeof(float2);
-  static_assert(kPairs >= kAttnWG, "one row of every piece");
+  static_assert(kPairs >= A::kWG, "one row of every piece");
   auto& s_o = *reinterpret_cast<float (*)[NT][NW][16][A::ROW]>(s_buf);
   float2* const s_ml = reinterpret_cast<float2*>(s_buf);
   __shared__ float s_m[NW][QT], s_l[NW][QT];
   __shared__ uint32_t s_scan[NW], s_line[NW], s_few[NW], s_items[NW], s_bad[NW];
   __shared__ uint32_t s_start[5];
-  __shared__ uint32_t s_flag;
+  __shared__ uint32_t s_last[2];
+  __shared__ Item s_cut[2];   // (in LDS: scalar registers are short)
   const int tid = threadIdx.x, lane = tid & 63;
   const uint32_t wave = uni(tid >> 6);
   const uint32_t hkv = a.n_kv_heads, n_req = a.n_req;
@@ -469,11 +486,23 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
   __syncthreads();
   uint32_t r = uni(s_start[0]), start = uni(s_start[1]);   // a request and its place on the line
 
-  const float c = fabsf(a.score_scale);
+  const float cs = fabsf(a.score_scale);
   const uint32_t flip = a.score_scale < 0.f ? 0x80008000u : 0u;
   const __amdgpu_buffer_rsrc_t rs = ws_rsrc(a.partial);
   constexpr uint32_t kSlot = NW * QT * (D + 2) * 4;   // bytes of one partial: values, then (max, sum)
   auto per_group = [&](uint32_t x) { return div_by(x, a.group, a.group_inv); };
+  auto out_at = [&](const Item& t, uint32_t qi) {   // query row qi of the item
+    const uint32_t row = per_group(t.q0 + qi), gq = t.q0 + qi - row * a.group;
+    return a.out + (uint64_t)(t.row0 + row) * a.out_stride + (uint64_t)(t.head * a.group + gq) * D;
+  };
+  auto scale_of = [&](const Item& t, uint32_t qi, float l) {
+    const int32_t sees = t.base + (int32_t)per_group(t.q0 + qi);
+    return t.broken ? NAN : (sees > 0 ? a.v_scale / l : 0.f);   // (without a token the values are 0)
+  };
+  auto put = [](uint16_t* p, f32x4 v, float f) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{bf_pack(v[0] * f, v[1] * f), bf_pack(v[2] * f, v[3] * f)};
+  };
+  uint32_t n_cut = 0;   // items that the piece's borders cut: two at most
   auto load_req = [&](uint32_t i) {
     return request(uniform_load(a.req_off, i), uniform_load(a.req_off, i + 1), uniform_load(a.kv_len, i));
   };
@@ -597,7 +626,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
         if (ids.bad) A::spoil(ids.bad, lane, s);
         bf16x8_t p[NT][PS];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) A::template weights<false>(c, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
+        for (int nt = 0; nt < NT; ++nt) A::template weights<false>(cs, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
         fence();
         A::product(vf, p, o);
         fence();
@@ -623,7 +652,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
               const int32_t tok = t_lane + (F8 ? 4 * t + i : 32 * (t / 2) + 4 * (t & 1) + i);
               seen |= tok < lim[nt] ? 1u << (4 * t + i) : 0u;
             }
-          A::template weights<true>(c, seen, s[nt], top[nt], sum[nt], o[nt], p[nt]);
+          A::template weights<true>(cs, seen, s[nt], top[nt], sum[nt], o[nt], p[nt]);
         }
         // What lies past a row's last token may be anything: zeros in its place.  Between the
         // first row's last token and the last row's, a value that is not finite would reach
@@ -678,25 +707,15 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
       // (values of the thread's place, hidden from the optimiser: it would compute what the
       // join needs before the loops above and keep it there, in registers they have not got)
       const int tj = opaque(tid), lj = tj & 63;
-      auto out_at = [&](uint32_t qi) {   // query row qi of the tile
-        const uint32_t row = per_group(q0 + qi), gq = q0 + qi - row * a.group;
-        return a.out + (uint64_t)(row0 + row) * a.out_stride + (uint64_t)(head * a.group + gq) * D;
-      };
-      auto scale_of = [&](uint32_t qi, float l) {
-        const int32_t sees = base + (int32_t)per_group(q0 + qi);
-        return broken ? NAN : (sees > 0 ? a.v_scale / l : 0.f);   // (without a token the values are 0)
-      };
-      auto put = [](uint16_t* p, f32x4 v, float f) {
-        *reinterpret_cast<u32x2*>(p) = u32x2{bf_pack(v[0] * f, v[1] * f), bf_pack(v[2] * f, v[3] * f)};
-      };
+      Item it = {row0, base, broken, head, q0, nq, 0, 0, 0};
       if (alone) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float l = group_sum(sum[nt]);
           const uint32_t qi = nt * 16 + (lj & 15);
           if (qi < nq) {
-            uint16_t* const p = out_at(qi) + 4 * (lj >> 4);
-            const float f = scale_of(qi, l);
+            uint16_t* const p = out_at(it, qi) + 4 * (lj >> 4);
+            const float f = scale_of(it, qi, l);
 #pragma unroll
             for (int d = 0; d < DT; ++d) put(p + 16 * d, o[nt][d], f);
           }
@@ -736,7 +755,7 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
 #pragma unroll
         for (int j = 0; j < NW; ++j)
           if (j < (int)stride) {
-            const float f = t[j] == -INFINITY ? 1.f : pow2((t[j] - m) * c);   // (without a maximum: 0, or NaN that stays)
+            const float f = t[j] == -INFINITY ? 1.f : pow2((t[j] - m) * cs);   // (without a maximum: 0, or NaN that stays)
             l += s_l[tile + j * deal][n] * f;
             s_m[tile + j * deal][n] = f;
           }
@@ -753,124 +772,136 @@ __global__ __launch_bounds__(64 * NW) void k_attn(AttnArgs a) {
         for (int j = 0; j < NW; ++j)
           if (j < (int)stride)
             v += *reinterpret_cast<const f32x4*>(&s_o[nt][tile + j * deal][n][d]) * s_m[tile + j * deal][nt * 16 + n];
-        if (whole) put(out_at(row) + d, v, scale_of(row, s_l[tile][nt * 16 + n]));
+        if (whole) put(out_at(it, row) + d, v, scale_of(it, row, s_l[tile][nt * 16 + n]));
         else st_dev4(rs, my_slot + (row * D + d) * 4, v);
       }
-      if (!whole) {
-        // ---- the item's last workgroup joins its pieces in order
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (tj == 0) {
-          const uint32_t old = __hip_atomic_fetch_add(a.tickets + w0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          const bool last = old == w1 - w0;
-          if (last) __hip_atomic_store(a.tickets + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          s_flag = last;
-        }
-        __syncthreads();
-        if (s_flag) {
-          // as many rows at a time as the pieces' maxima and sums leave room for in LDS
-          const uint32_t pieces = w1 - w0 + 1;   // at most kAttnWG
-          const uint32_t most = min(nq, kPairs / pieces);
-          auto slot_of = [&](uint32_t w) { return ((w0 + w) * 2 + (w == 0 ? late : 0u)) * kSlot; };
-          // the values, PU places of a thread and B pieces of each in flight: another
-          // workgroup's write takes about 5000 cycles to read, and only the number of reads at
-          // once helps; the first ones are requested together with the maxima
-          constexpr uint32_t PU = QT * (D / 4) / T < 4 ? 1 : (NT == 1 ? 2 : 4), B = 16 / PU;
-          for (uint32_t n0 = 0; n0 < nq; n0 += most) {
-            const uint32_t rows = min(most, nq - n0), n_places = rows * (D / 4);
-            f32x4 x[PU][B];
-            auto request_values = [&](uint32_t e, uint32_t w) {
+      if (!whole) {   // its values are on their way to the workspace
+        it.w0 = w0;
+        it.w1 = w1;
+        it.late = late;
+        if (tid == 0) s_cut[n_cut] = it;
+        ++n_cut;
+      }
+    }
+  }
+
+  // ---- the items that the piece's borders cut: the workgroup that is through with one last
+  // joins its pieces in order
+  if (n_cut == 0) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid < (int)n_cut) {
+    uint32_t* const ticket = a.tickets + s_cut[tid].w0;
+    const uint32_t old = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last[tid] = old == s_cut[tid].w1 - s_cut[tid].w0;
+    if (s_last[tid]) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  for (uint32_t i = 0; i < n_cut; ++i) {
+    if (!uni(s_last[i])) continue;
+    const Item& t = s_cut[i];
+    const Item c = {(int32_t)uni(t.row0), (int32_t)uni(t.base), uni(t.broken) != 0, uni(t.head), uni(t.q0),
+                    uni(t.nq), uni(t.w0), uni(t.w1), uni(t.late)};
+    // as many rows at a time as the pieces' maxima and sums leave room for in LDS
+    const uint32_t pieces = c.w1 - c.w0 + 1;   // at most A::kWG
+    const uint32_t most = min(c.nq, kPairs / pieces);
+    auto slot_of = [&](uint32_t w) { return ((c.w0 + w) * 2 + (w == 0 ? c.late : 0u)) * kSlot; };
+    // the values, PU places of a thread and B pieces of each in flight: another
+    // workgroup's write takes about 5000 cycles to read, and only the number of reads at
+    // once helps; the first ones are requested together with the maxima
+    constexpr uint32_t PU = QT * (D / 4) / T < 4 ? 1 : (NT == 1 ? 2 : 4), B = 16 / PU;
+    for (uint32_t n0 = 0; n0 < c.nq; n0 += most) {
+      const uint32_t rows = min(most, c.nq - n0), n_places = rows * (D / 4);
+      f32x4 x[PU][B];
+      auto request_values = [&](uint32_t e, uint32_t w) {
+        // (places and pieces past the end: an offset past the buffer, which reads as zero)
 #pragma unroll
-              for (uint32_t i = 0; i < PU; ++i)
-                if (e + i * T < n_places) {
+        for (uint32_t i = 0; i < PU; ++i)
 #pragma unroll
-                  for (uint32_t b = 0; b < B; ++b)
-                    if (w + b < pieces) x[i][b] = ld_dev4(rs, slot_of(w + b) + (n0 * (D / 4) + e + i * T) * 16);
-                }
-            };
-            request_values(tj, 0);
-            // 16 lanes per row: its pieces' maxima and sums, each lane's own kept in LDS, and
-            // turned into factors there; two rows at once
-            for (uint32_t n1 = tj >> 4; n1 < rows; n1 += 2 * T / 16) {
-              float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+          for (uint32_t b = 0; b < B; ++b) {
+            const bool on = e + i * T < n_places && w + b < pieces;
+            x[i][b] = ld_dev4(rs, on ? slot_of(w + b) + (n0 * (D / 4) + e + i * T) * 16 : 0x7ffffff0u);
+          }
+      };
+      request_values(tid, 0);
+      // 16 lanes per row: its pieces' maxima and sums, each lane's own kept in LDS, and
+      // turned into factors there; two rows at once
+      for (uint32_t n1 = tid >> 4; n1 < rows; n1 += 2 * T / 16) {
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll 2
-              for (uint32_t w = tj & 15; w < pieces; w += 16) {
-                u32x2 ml[2];
+        for (uint32_t w = tid & 15; w < pieces; w += 16) {
+          u32x2 ml[2];
 #pragma unroll
-                for (uint32_t k = 0; k < 2; ++k)
-                  if (n1 + k * (T / 16) < rows)
-                    ml[k] = ld_dev2(rs, slot_of(w) + (NW * QT * D + 2 * (n0 + n1 + k * (T / 16))) * 4);
+          for (uint32_t k = 0; k < 2; ++k)
+            if (n1 + k * (T / 16) < rows)
+              ml[k] = ld_dev2(rs, slot_of(w) + (NW * QT * D + 2 * (n0 + n1 + k * (T / 16))) * 4);
 #pragma unroll
-                for (uint32_t k = 0; k < 2; ++k)
-                  if (n1 + k * (T / 16) < rows) {
-                    s_ml[w * rows + n1 + k * (T / 16)] = make_float2(__uint_as_float(ml[k][0]), __uint_as_float(ml[k][1]));
-                    m[k] = fmaxf(m[k], __uint_as_float(ml[k][0]));
-                  }
-              }
-#pragma unroll
-              for (uint32_t k = 0; k < 2; ++k) m[k] = row_max(m[k]);
-              for (uint32_t w = tj & 15; w < pieces; w += 16)
-#pragma unroll
-                for (uint32_t k = 0; k < 2; ++k)
-                  if (n1 + k * (T / 16) < rows) {
-                    const float2 ml = s_ml[w * rows + n1 + k * (T / 16)];
-                    const float f = ml.x == -INFINITY ? 1.f : pow2((ml.x - m[k]) * c);
-                    l[k] += ml.y * f;
-                    s_ml[w * rows + n1 + k * (T / 16)].x = f;
-                  }
-#pragma unroll
-              for (uint32_t k = 0; k < 2; ++k) {
-                const float all = row_sum(l[k]);
-                if ((tj & 15) == 0 && n1 + k * (T / 16) < rows) (&s_l[0][0])[n1 + k * (T / 16)] = all;
-              }
+          for (uint32_t k = 0; k < 2; ++k)
+            if (n1 + k * (T / 16) < rows) {
+              s_ml[w * rows + n1 + k * (T / 16)] = make_float2(__uint_as_float(ml[k][0]), __uint_as_float(ml[k][1]));
+              m[k] = fmaxf(m[k], __uint_as_float(ml[k][0]));
             }
-            __syncthreads();
-            bool there = true;   // the first values were requested above
-            for (uint32_t e = tj; e < n_places; e += PU * T) {
-              f32x4 v[PU];
+        }
 #pragma unroll
-              for (uint32_t i = 0; i < PU; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-              for (uint32_t w = 0; w < pieces; w += B) {
-                if (!there) request_values(e, w);
-                there = false;
+        for (uint32_t k = 0; k < 2; ++k) m[k] = row_max(m[k]);
+        for (uint32_t w = tid & 15; w < pieces; w += 16)
 #pragma unroll
-                for (uint32_t i = 0; i < PU; ++i)
-                  if (e + i * T < n_places) {
-#pragma unroll
-                    for (uint32_t b = 0; b < B; ++b)
-                      if (w + b < pieces) v[i] += x[i][b] * s_ml[(w + b) * rows + (e + i * T) / (D / 4)].x;
-                  }
-              }
-#pragma unroll
-              for (uint32_t i = 0; i < PU; ++i)
-                if (e + i * T < n_places) {
-                  const uint32_t n = (e + i * T) / (D / 4);
-                  put(out_at(n0 + n) + 4 * ((e + i * T) % (D / 4)), v[i], scale_of(n0 + n, (&s_l[0][0])[n]));
-                }
+          for (uint32_t k = 0; k < 2; ++k)
+            if (n1 + k * (T / 16) < rows) {
+              const float2 ml = s_ml[w * rows + n1 + k * (T / 16)];
+              const float f = ml.x == -INFINITY ? 1.f : pow2((ml.x - m[k]) * cs);
+              l[k] += ml.y * f;
+              s_ml[w * rows + n1 + k * (T / 16)].x = f;
             }
-            __syncthreads();
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k) {
+          const float all = row_sum(l[k]);
+          if ((tid & 15) == 0 && n1 + k * (T / 16) < rows) (&s_l[0][0])[n1 + k * (T / 16)] = all;
+        }
+      }
+      __syncthreads();
+      bool there = true;   // the first values were requested above
+      for (uint32_t e = tid; e < n_places; e += PU * T) {
+        f32x4 v[PU];
+#pragma unroll
+        for (uint32_t i = 0; i < PU; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (uint32_t w = 0; w < pieces; w += B) {
+          if (!there) request_values(e, w);
+          there = false;
+#pragma unroll
+          for (uint32_t i = 0; i < PU; ++i) {
+            const uint32_t n = min(e + i * T, n_places - 1) / (D / 4);
+#pragma unroll
+            for (uint32_t b = 0; b < B; ++b) v[i] += x[i][b] * s_ml[min(w + b, pieces - 1) * rows + n].x;
           }
         }
-        __syncthreads();
+#pragma unroll
+        for (uint32_t i = 0; i < PU; ++i)
+          if (e + i * T < n_places) {
+            const uint32_t n = (e + i * T) / (D / 4);
+            put(out_at(c, n0 + n) + 4 * ((e + i * T) % (D / 4)), v[i], scale_of(c, n0 + n, (&s_l[0][0])[n]));
+          }
       }
+      __syncthreads();
     }
   }
 }
 
 template <int D, bool F8, int NT, int NW, int UT>
 hipError_t attn_go(const AttnArgs& a, hipStream_t s) {
+  using A = Attn<D, F8, NT, NW, UT>;
   // no more workgroups than units that the widest table could fill
   const uint64_t tiles = ((uint64_t)a.m * a.group + (uint64_t)a.n_req * (16 * NT - 1)) / (16 * NT) + 1;
   const uint64_t units = (((uint64_t)a.max_pages << a.page_shift) + UT - 1) / UT;
-  uint64_t wg = kAttnWG;
+  uint64_t wg = A::kWG;
   if (units < wg && tiles * a.n_kv_heads * units < wg) wg = tiles * a.n_kv_heads * units;
   // What one more piece costs the join of an item, in units: a read's latency, and the values
   // of its rows at 30 bytes per cycle against a unit's at 10.
   const uint64_t mean = ((uint64_t)a.m + a.n_req - 1) / a.n_req * a.group;
   AttnArgs b = a;
   b.join_cost = 0.3f + (float)(mean < 16 * NT * NW ? mean : 16 * NT * NW) * 4.f / (6.f * UT * (F8 ? 1 : 2));
-  static_assert(kAttnWG * 2ull * NW * 16 * NT * (D + 2) * 4 <= W12_ATTN_WS_BYTES - kTicketBytes, "workspace");
-  static_assert(kAttnWG * 4 <= kTicketBytes, "tickets");
+  static_assert(A::kWG * 2ull * NW * 16 * NT * (D + 2) * 4 <= W12_ATTN_WS_BYTES - kTicketBytes, "workspace");
+  static_assert(A::kWG * 4 <= kTicketBytes, "tickets");
   b.grid = (uint32_t)wg;
   b.grid_inv = wg == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / wg);
   hipLaunchKernelGGL((k_attn<D, F8, NT, NW, UT>), dim3((uint32_t)wg), dim3(64 * NW), 0, s, b);
@@ -878,10 +909,13 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t s) {
 }
 
 // Tile of query rows by the mean number per request: 16 while it holds them, else 32 (what the
-// registers hold; with a head_dim of 256 that is 16).  Units of 64 tokens; of 32 where 64 do
-// not fit or fit only just (two BF16 tiles at 128: 24 requests of 25 query rows over 98k tokens
-// 95 us with 32, 99 us with 64; of 80 query rows, whose waves take a tile each and read the
-// same unit at once, 177 us with 32, 154 us with 64).
+// registers hold; with a head_dim of 256 that is 16).  Units of 64 tokens in E4M3 (16 bytes of
+// V^T).  In BF16 of 32 where 64 do not fit (256), and at 128, where a short request's one unit
+// is half the work (300 requests of up to 100 tokens 23 us with 64, 19 us with 32; one of 17
+// tokens 7.4 and 6.1 us; 98k tokens in 24 requests 84 us either way, 131k in one 102 and 105
+// us; 25 query rows each 95 us with 32, 99 us with 64); 64 for more than two tiles, whose waves
+// take a tile each and read the same unit at once (80 query rows each 177 us with 32, 154 us
+// with 64).
 template <int D, bool F8>
 hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
   const uint64_t rows = ((uint64_t)a.m + a.n_req - 1) / a.n_req * a.group;
@@ -892,7 +926,7 @@ hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
       return attn_go<D, F8, 2, 4, 64>(a, s);
     }
   }
-  return attn_go<D, F8, 1, 4, F8 || D < 256 ? 64 : 32>(a, s);
+  return attn_go<D, F8, 1, 4, F8 || D < 128 ? 64 : 32>(a, s);
 }
 
 template <bool F8>
