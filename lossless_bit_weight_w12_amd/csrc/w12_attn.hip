@@ -19,6 +19,11 @@
 // joins its waves in LDS; an item (request, tile, head) cut by a piece's border is joined by
 // the workgroup that finishes it last, in piece order, so the result does not depend on
 // which that is.
+//
+// Bound by HBM where there is enough to read (24 requests, 98k tokens, 8 key heads of 128 in
+// BF16, 423 MB: 84 us, 5.0 TB/s over the call and 5.9 in the loop; one request of 131k tokens,
+// 537 MB: 105 us, 5.1 TB/s), else by the dependent steps around the loop (one request of 17
+// tokens: 6 us; of 4096: 13 us).
 #include "w12.h"
 #include "w12_kv.h"
 
