@@ -229,8 +229,9 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a, uint32_t row, uint
   constexpr int kSub = D / 8;          // lanes per head
   constexpr int kPar = 64 / kSub;      // heads per wave at a time
   const int lane = threadIdx.x & 63;
+  // (Every read is requested before the first is waited for: 512 rows of 40 heads 6.8 -> 6.4 us,
+  // 8192 rows 50.6 -> 49.4 us.)
   const int32_t pos = a.pos[row];
-  if (pos < 0) return;
   const uint32_t slot = (uint32_t)a.slot[row];
   const uint32_t sub = lane % kSub, heads = a.n_heads + a.n_kv_heads, half = a.rot_dim / 2;
   auto load = [&](uint32_t h) {
@@ -242,15 +243,22 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a, uint32_t row, uint
   };
   const uint32_t h_first = part * kPar + lane / kSub;
   u32x4 next = load(h_first);
+  double freq[(D / 2 + 63) / 64];
+#pragma unroll
+  for (int i = 0; i < (D / 2 + 63) / 64; ++i)
+    freq[i] = lane + 64u * i < half ? a.inv_freq[lane + 64u * i] : 0.0;
   u32x4 wq = {0u, 0u, 0u, 0u}, wk = wq;
   if (a.q_norm) wq = *reinterpret_cast<const u32x4*>(a.q_norm + sub * 8);
   if (a.k_norm) wk = *reinterpret_cast<const u32x4*>(a.k_norm + sub * 8);
-  for (uint32_t f = lane; f < half; f += 64) {
-    const double turns = (double)pos * a.inv_freq[f] * 0.15915494309189535;
-    float sn, cs;
-    sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
-    s_turn[f] = make_float2(cs, sn);
-  }
+  if (pos < 0) return;
+#pragma unroll
+  for (int i = 0; i < (D / 2 + 63) / 64; ++i)
+    if (lane + 64u * i < half) {
+      const double turns = (double)pos * freq[i] * 0.15915494309189535;
+      float sn, cs;
+      sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
+      s_turn[lane + 64u * i] = make_float2(cs, sn);
+    }
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();   // one wave writes and reads: LDS keeps the order
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -346,6 +354,15 @@ __device__ __forceinline__ void rope_values(const RopeArgs& a, uint32_t tile, ui
     const uint32_t s = (uint32_t)a.slot[near];
     if (a.pos[near] >= 0 && s < a.n_slots) slot = s;
   }
+  constexpr int kEach = (kRowsV * kSub + kRopeT - 1) / kRopeT;   // 8 dimensions of a row per thread
+  u32x4 own[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const uint32_t i = t + e * kRopeT;
+    const uint64_t row = (uint64_t)tile * kRowsV + i / kSub;
+    if (i < kRowsV * kSub && row < a.m)
+      own[e] = *reinterpret_cast<const u32x4*>(a.v + row * a.v_stride + (uint64_t)head * D + i % kSub * 8);
+  }
   const uint32_t after = __shfl_down(slot, 1);
   const uint64_t follows = __ballot(slot != ~0u && slot + 1 == after);
   const uint64_t full = __ballot(slot % 8 == 0 && ((follows >> lane) & 0x7f) == 0x7f);   // first rows of whole groups
@@ -354,12 +371,12 @@ __device__ __forceinline__ void rope_values(const RopeArgs& a, uint32_t tile, ui
   };
   auto quot = [&](uint16_t x) { return __uint_as_float((uint32_t)x << 16) / a.v_scale; };
 
-  for (uint32_t i = t; i < kRowsV * kSub; i += kRopeT) {
-    const uint32_t l = i / kSub + 7, d = i % kSub * 8;
-    const uint32_t s = __shfl(slot, l);   // (i / kSub < 16: whole waves take part)
-    if (s == ~0u || (s % 8 <= l && ((full >> (l - s % 8)) & 1))) continue;
-    const u32x4 x = *reinterpret_cast<const u32x4*>(a.v + ((uint64_t)tile * kRowsV + l - 7) * a.v_stride +
-                                                    (uint64_t)head * D + d);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const uint32_t i = t + e * kRopeT, l = i / kSub + 7, d = i % kSub * 8;
+    const uint32_t s = __shfl(slot, l & 63);
+    if (i >= kRowsV * kSub || s == ~0u || (s % 8 <= l && ((full >> (l - s % 8)) & 1))) continue;
+    const u32x4 x = own[e];
     const uint64_t at = dest(s, d);
     if constexpr (F8) {
       const uint32_t lo = pack_e4m3x4(quot(x[0]), quot(x[0] >> 16), quot(x[1]), quot(x[1] >> 16));
