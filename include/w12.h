@@ -525,7 +525,7 @@ w12_status w12_qk_rope(const uint16_t* q, uint64_t q_stride, const uint16_t* k, 
  * that sees a token whose table entry is outside 0 .. n_pages - 1; every row gets NaN when
  * req_off is not 0 <= req_off[0] <= req_off[1] <= ... <= m.
  * q and out device BF16 [m][n_heads][head_dim], rows *_stride elements apart (a multiple of 8,
- * at least the row's length), 16-byte aligned; table device int32 [>= n_req][max_pages],
+ * at least the row's length), 16-byte aligned, apart; table device int32 [>= n_req][max_pages],
  * kv_len [n_req], req_off [n_req + 1].  The sequence is split over workgroups and joined
  * inside the launch in a fixed order: same inputs, same bits.  ws: W12_ATTN_WS_BYTES bytes,
  * 256-byte aligned, beginning with 4096 bytes of tickets that must be zero before its first

@@ -118,7 +118,7 @@ __global__ __launch_bounds__(T) void k_kv_plan(PlanArgs a) {
     if (i < (int)per && r < n) {
       s_need[r + 1] = nsum;
       s_free[r + 1] = fsum;
-      nsum -= need[i];   // (a saturated sum stays above any pool: kPer n_pages < 2^29)
+      nsum -= need[i];   // (a saturated sum stays above any pool: kPer max_pages <= 2^28)
       fsum -= freed[i];
     }
   }
@@ -129,7 +129,9 @@ __global__ __launch_bounds__(T) void k_kv_plan(PlanArgs a) {
   const uint32_t taken = total_need <= avail ? total_need : s_need[segment(s_need, n, avail)];
 
   auto rows_of = [&](uint32_t r) { return s_off[r + 1] - s_off[r]; };
-  auto served = [&](uint32_t r) { return s_held[r] >= 0 && (s_need[r + 1] == s_need[r] || s_need[r + 1] <= avail); };
+  auto served = [&](uint32_t r) {   // (needs nothing, by its own count: saturated sums are equal too)
+    return s_held[r] >= 0 && (s_need[r + 1] <= avail || want_of(s_len[r], rows_of(r)) <= (uint32_t)s_held[r]);
+  };
   auto ring_at = [&](uint32_t j) {   // j <= n_pages
     const uint32_t i = head + j;
     return i >= a.n_pages ? i - a.n_pages : i;

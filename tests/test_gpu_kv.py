@@ -116,6 +116,27 @@ def test_plan_pages_move_within_a_call():
     assert want[0].tolist() == [64, 21]
 
 
+def test_plan_needs_past_2_to_the_30_pages():
+    """Requests of 2^26 pages each: from the 16th on the sums of their needs saturate, and a sum equals
+    the one before it; all the same every request that needs pages is refused."""
+    n = 19
+    p = w12.page_table(64, 16, n, 1 << 26, DEV)
+    p.held[3] = 4      # the one request that needs nothing, behind refused ones
+    p.state[1] = 60
+    length = np.full(n, (1 << 30) - 1)
+    length[3] = 60
+    kv_len, pos, slot = w12.kv_plan(p, i32(length), i32(np.arange(n + 1)), n)
+    want = np.full(n, -1)
+    want[3] = 61
+    assert np.array_equal(kv_len.cpu().numpy(), want)
+    want[3] = 60
+    assert np.array_equal(pos.cpu().numpy(), want)
+    assert (slot == -1).all()      # (its table names no page)
+    assert p.held.tolist() == [0, 0, 0, 4] + [0] * 15 and p.state.tolist() == [0, 60, 0, 0]
+    assert p.ring.tolist() == list(range(64))
+    assert int(p.table.max()) == -1
+
+
 def test_plan_large_tables():
     """64 prompts of up to 4000 tokens at once, then everything back; and a bad page id in the
     table gives no slot."""
