@@ -13,6 +13,10 @@
 // of V^T hold.  Nothing passes through LDS inside the loop, and every load is 16 bytes used
 // as it comes.
 //
+// Where several tiles of query rows read the same keys, their waves can read K and V from LDS
+// instead: a step of 64 KB, in the operands' own order (so the reads have no conflicts), which
+// the waves fetch together while they work on the step before it.
+//
 // Split: the work of all requests, heads and tiles is one line of units of UT tokens, cut into
 // equal pieces, one per workgroup; inside a piece each wave takes every NW-th unit.  Lengths
 // can be as uneven as they like and a single long request still fills the chip.  A workgroup
@@ -157,7 +161,7 @@ struct Item {
   uint32_t w0, w1, late; // workgroups with a piece; 1: the first one's second partial
 };
 
-template <int D, bool F8, int NT, int NW, int UT>
+template <int D, bool F8, int NT, int NW, int UT, bool ST>
 struct Attn {
   static constexpr int ES = F8 ? 1 : 2;          // bytes per cached value
   static constexpr int QT = 16 * NT;             // query rows of a tile
@@ -169,6 +173,11 @@ struct Attn {
   static constexpr int VL = F8 ? PS / 2 : PS;    // 16-byte loads of one dimension of V per lane
   static constexpr int ROW = D + 4;              // LDS row of the join, padded
   static constexpr int T = 64 * NW;
+  // Staged (ST): a step of SU units (64 KB) passes through LDS, CB wave loads of K and of V per
+  // unit; a wave fetches K or V of one unit.
+  static constexpr uint32_t SU = NW / 2;
+  static constexpr uint32_t CB = UT * D * 2 / 1024;
+  static_assert(!ST || (!F8 && UT * D == 8192), "64 KB per step");
   static constexpr uint32_t kWG = workgroups(NT, 2 * UT * D * ES);
   // What an item costs a workgroup beside its units (its queries' load, the join, the writes:
   // about 15000 cycles under load, the time of 128 KB), in units.
@@ -200,8 +209,9 @@ struct Attn {
 
   // K of a unit: lane (row r = l % 16 of each token tile, group g) the 16 bytes g of each
   // 64-byte step of its token's key.
+  template <class P>
   static __device__ __forceinline__ void load_k(const AttnArgs& a, const Ids& x, uint32_t u, uint32_t head,
-                                                int lane, u32x4 (&k)[TT][KL]) {
+                                                int lane, P&& put) {
     const uint32_t r = lane & 15, g = lane >> 4, mask = (1u << a.page_shift) - 1u;
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
@@ -216,14 +226,15 @@ struct Attn {
       const uint32_t place = (u * UT + tok) & mask;
       const uint8_t* p = a.kc + ((((uint64_t)id * a.n_kv_heads + head) << a.page_shift) + place) * (D * ES) + 16 * g;
 #pragma unroll
-      for (int i = 0; i < KL; ++i) k[t][i] = load16(p + 64 * i);
+      for (int i = 0; i < KL; ++i) put(t, i, load16(p + 64 * i));
     }
   }
 
   // V^T of a unit: lane (dimension l % 16 of each dimension tile, group g) 16 bytes of
   // consecutive tokens: 32 s + 8 g .. + 7 (BF16), 16 g .. + 15 (E4M3).
+  template <class P>
   static __device__ __forceinline__ void load_v(const AttnArgs& a, const Ids& x, uint32_t u, uint32_t head,
-                                                int lane, u32x4 (&v)[DT][VL]) {
+                                                int lane, P&& put) {
     const uint32_t g = lane >> 4, mask = (1u << a.page_shift) - 1u;
 #pragma unroll
     for (int s = 0; s < VL; ++s) {
@@ -241,7 +252,7 @@ struct Attn {
       const uint32_t step = (16u * ES) << a.page_shift;
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        v[d][s] = load16(p);
+        put(d, s, load16(p));
         p += step;
       }
     }
@@ -358,12 +369,13 @@ struct Attn {
   }
 };
 
-template <int D, bool F8, int NT, int NW, int UT>
-__global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) / 256) void k_attn(AttnArgs a) {
-  using A = Attn<D, F8, NT, NW, UT>;
+template <int D, bool F8, int NT, int NW, int UT, bool ST>
+__global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) / 256) void k_attn(AttnArgs given) {
+  using A = Attn<D, F8, NT, NW, UT, ST>;
   constexpr int QT = A::QT, KS = A::KS, DT = A::DT, TT = A::TT, PS = A::PS, T = A::T;
   // the waves' results, and later the (max, sum) pairs of an item's pieces
-  __shared__ __attribute__((aligned(16))) uint8_t s_buf[sizeof(float) * NT * NW * 16 * A::ROW];
+  constexpr uint32_t kJoin = sizeof(float) * NT * NW * 16 * A::ROW, kStep = A::SU * 2 * A::CB * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t s_buf[ST && 2 * kStep > kJoin ? 2 * kStep : kJoin];
   constexpr uint32_t kPairs = sizeof(s_buf) / sizeof(float2);
   static_assert(kPairs >= A::kWG, "one row of every piece");
   auto& s_o = *reinterpret_cast<float (*)[NT][NW][16][A::ROW]>(s_buf);
@@ -372,19 +384,20 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
   __shared__ uint32_t s_scan[NW], s_line[NW], s_few[NW], s_items[NW], s_bad[NW];
   __shared__ uint32_t s_start[5];
   __shared__ uint32_t s_last[2];
+  __shared__ uint32_t s_spoil[2][A::SU];   // staged: Ids::bad of the step's units
   __shared__ Item s_cut[2];   // (in LDS: scalar registers are short)
   const int tid = threadIdx.x, lane = tid & 63;
   const uint32_t wave = uni(tid >> 6);
-  const uint32_t hkv = a.n_kv_heads, n_req = a.n_req;
+  const uint32_t hkv = given.n_kv_heads, n_req = given.n_req;
 
   auto request = [&](int32_t row0, int32_t row1, int32_t len) {
     Req q;
     q.row0 = row0;
     q.len = len;
     q.rows = (uint32_t)(row1 - row0);
-    q.broken = len < 0 || (uint64_t)len > ((uint64_t)a.max_pages << a.page_shift);
+    q.broken = len < 0 || (uint64_t)len > ((uint64_t)given.max_pages << given.page_shift);
     q.units = q.broken || len == 0 ? 1u : ((uint32_t)len + UT - 1) / UT;
-    q.tiles = (q.rows * a.group + QT - 1) / QT;
+    q.tiles = (q.rows * given.group + QT - 1) / QT;
     return q;
   };
 
@@ -392,7 +405,7 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
   const uint32_t per_t = (n_req + T - 1) / T;
   auto mine_at = [&](uint32_t i) {   // this thread's i-th request
     const uint32_t r = tid * per_t + i;
-    return r < n_req ? request(a.req_off[r], a.req_off[r + 1], a.kv_len[r]) : Req{0, 0, 0, false, 1, 0};
+    return r < n_req ? request(given.req_off[r], given.req_off[r + 1], given.kv_len[r]) : Req{0, 0, 0, false, 1, 0};
   };
   const Req mine_0 = mine_at(0);   // the only one up to T requests: loaded once
   auto mine = [&](uint32_t i) { return i == 0 ? mine_0 : mine_at(i); };
@@ -401,7 +414,7 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
   bool bad = false;
   for (uint32_t i = 0; i < per_t; ++i) {
     const Req q = mine(i);
-    bad |= q.row0 < 0 || (int32_t)q.rows < 0 || (int64_t)q.row0 + q.rows > (int64_t)a.m;
+    bad |= q.row0 < 0 || (int32_t)q.rows < 0 || (int64_t)q.row0 + q.rows > (int64_t)given.m;
     all_units += q.tiles * hkv * q.units;
     few_units += (q.tiles + NW - 1) / NW * hkv * q.units;
     all_items += q.tiles * hkv;
@@ -426,9 +439,10 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
     bad |= uni(s_bad[w]) != 0;
   }
   if (bad) {   // no request table: NaN everywhere
-    for (uint64_t i = (uint64_t)blockIdx.x * T + tid; i < (uint64_t)a.m * a.n_heads * D; i += (uint64_t)a.grid * T) {
-      const uint64_t row = i / (a.n_heads * D);
-      a.out[row * a.out_stride + i % (a.n_heads * D)] = 0x7fc0u;
+    const uint64_t all = (uint64_t)given.m * given.n_heads * D;
+    for (uint64_t i = (uint64_t)blockIdx.x * T + tid; i < all; i += (uint64_t)given.grid * T) {
+      const uint64_t row = i / (given.n_heads * D);
+      given.out[row * given.out_stride + i % (given.n_heads * D)] = 0x7fc0u;
     }
     return;
   }
@@ -436,15 +450,15 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
   // one head, one for each wave, so that K and V are read once for all of them (16 rows of 5
   // heads each against 98k tokens: 207 us apart, 170 us together; but 8 heads of 1 to 4 rows
   // against 10k tokens, 2 units per workgroup: 26 us apart, 36 us together).
-  auto per_grid = [&](uint32_t x) { return div_by(x, a.grid, a.grid_inv); };
-  const uint32_t span = all_units >= 16 * a.grid ? NW : 1u;   // tiles of a long item, at most
-  const uint32_t mean = min(per_grid((span > 1 ? few_units : all_units) + a.grid - 1), 1u << 20);
+  auto per_grid = [&](uint32_t x) { return div_by(x, given.grid, given.grid_inv); };
+  const uint32_t span = all_units >= 16 * given.grid ? NW : 1u;   // tiles of a long item, at most
+  const uint32_t mean = min(per_grid((span > 1 ? few_units : all_units) + given.grid - 1), 1u << 20);
   auto wide = [&](const Req& q) { return span > 1 ? (q.tiles + NW - 1) / NW : q.tiles; };   // long items per head
   // A long item has a lead of kLead places on the line, then one per unit; its units may fall
   // into several pieces.  A brief one (few enough units that a wave does better with an
   // item of its own than all waves one after the other: with k = mean / units items per
   // piece, (k - 1) kLead >= units) is never cut: it belongs to the piece it begins in.
-  auto brief = [&](const Req& q) { return q.units < 4096 && q.units * (q.units + A::kLead) <= A::kLead * mean; };
+  auto brief = [&](const Req& q) { return !ST && q.units < 4096 && q.units * (q.units + A::kLead) <= A::kLead * mean; };
   auto lead = [&](const Req& q) { return brief(q) ? (A::kLead + NW - 1) / NW : A::kLead; };
   auto places = [&](const Req& q) { return lead(q) + q.units; };   // of one item
   auto items = [&](const Req& q) { return (brief(q) ? q.tiles : wide(q)) * hkv; };
@@ -468,12 +482,32 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
   // of at least 4 units, so that a workgroup's waves share an item before it is cut; but of
   // no more than the mean item.
   const float units = all_items ? (float)all_units / (float)all_items : 1.f;   // of the mean item
-  const uint32_t least = (uint32_t)fminf(units, fmaxf(4.f, __builtin_amdgcn_sqrtf(units * a.join_cost)));
-  const uint32_t per = uni(max(per_grid(total + a.grid - 1), least));
+  const uint32_t least = (uint32_t)fminf(units, fmaxf(4.f, __builtin_amdgcn_sqrtf(units * given.join_cost)));
+  const uint32_t per = uni(max(per_grid(total + given.grid - 1), least));
   const uint32_t here = blockIdx.x * per;   // where the piece begins
   uint32_t pos = here;
   const uint32_t end = min(pos + per, total);
   if (pos >= total) return;
+  // What the line does not need is read from the arguments here: the compiler would load it at
+  // the kernel's entry, have no scalar registers for it, and wait for it three times before the
+  // first request is read (one request of 17 tokens 6.35 us, 6.2 us so).
+  AttnArgs a = given;
+  {
+    auto late = (const __attribute__((address_space(4))) AttnArgs*)(uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(late));
+    a.q = late->q;
+    a.q_stride = late->q_stride;
+    a.out_stride = late->out_stride;
+    a.n_pages = late->n_pages;
+    a.kc = late->kc;
+    a.vc = late->vc;
+    a.table = late->table;
+    a.score_scale = late->score_scale;
+    a.v_scale = late->v_scale;
+    a.out = late->out;
+    a.tickets = late->tickets;
+    a.partial = late->partial;
+  }
   if (pos >= upto - line && pos < upto) {   // one thread: the request it starts in
     uint32_t at = upto - line;
     uint32_t i = 0;
@@ -609,42 +643,12 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
 
       const uint64_t trow = (uint64_t)r_item * a.max_pages;
       u32x4 kf[TT][A::KL], vf[DT][A::VL];
-      uint32_t u = ua + turn;
-      typename A::Ids ids = {{0u, 0u, 0u, 0u}, 0u};
-      if (u < uz) {
-        ids = A::load_ids(a, trow, u, see);
-        A::load_k(a, ids, u, head, lane, kf);
-        A::load_v(a, ids, u, head, lane, vf);
-      }
-      // full units: every row sees every token; the next unit's pages, K and V are requested as
-      // soon as the registers they go to are free
-      const uint32_t full = min(uz, see_min > 0 ? (uint32_t)see_min / UT : 0u);
-      for (; u < full; u += stride) {
-        const bool more = u + stride < uz;
-        typename A::Ids next = ids;
-        if (more) next = A::load_ids(a, trow, u + stride, see);
+      // a unit (kf, vf) in which some row's tokens end
+      auto ends_in = [&](uint32_t u, uint32_t spoilt, auto&& values) {
         f32x4 s[NT][TT];
         A::scores(kf, qf, s);
-        fence();
-        if (more) A::load_k(a, next, u + stride, head, lane, kf);
-        fence();
-        if (ids.bad) A::spoil(ids.bad, lane, s);
-        bf16x8_t p[NT][PS];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) A::template weights<false>(cs, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
-        fence();
-        A::product(vf, p, o);
-        fence();
-        if (more) {
-          A::load_v(a, next, u + stride, head, lane, vf);
-          ids = next;
-        }
-      }
-      // units in which some row's tokens end
-      for (; u < uz; u += stride) {
-        f32x4 s[NT][TT];
-        A::scores(kf, qf, s);
-        if (ids.bad) A::spoil(ids.bad, lane, s);
+        values();
+        if (spoilt) A::spoil(spoilt, lane, s);
         const int32_t t_lane = (int32_t)(u * UT) + (F8 ? 16 : 8) * (lane >> 4);   // the lane's first token
         bf16x8_t p[NT][PS];
 #pragma unroll
@@ -702,10 +706,114 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
             fence();
           }
         }
-        if (u + stride < uz) {
-          ids = A::load_ids(a, trow, u + stride, see);
-          A::load_k(a, ids, u + stride, head, lane, kf);
-          A::load_v(a, ids, u + stride, head, lane, vf);
+      };
+      if constexpr (ST) {
+        // A step ahead: while the waves work on a step in one half of the buffer, the next is on
+        // its way to their registers and goes to the other half.
+        const uint32_t see_all = (uint32_t)max(base + (int32_t)per_group(q0 + nq - 1), 0);
+        const uint32_t uz_all = min(ub, (see_all + UT - 1) / UT);
+        const uint32_t of_step = wave / 2;   // the step's unit that this wave fetches
+        const bool of_v = wave & 1;          // its V, or its K
+        u32x4 st[A::CB];
+        uint32_t spoils = 0;
+        auto fetch = [&](uint32_t u0) {
+          const uint32_t u = u0 + of_step;
+          if (u >= uz_all) return;
+          const typename A::Ids x = A::load_ids(a, trow, u, see_all);
+          spoils = x.bad;
+          if (of_v) A::load_v(a, x, u, head, lane, [&](int d, int i, u32x4 v) { st[d * A::VL + i] = v; });
+          else A::load_k(a, x, u, head, lane, [&](int t, int i, u32x4 v) { st[t * A::KL + i] = v; });
+        };
+        __syncthreads();   // the buffer is free
+        fetch(ua);
+        uint32_t u0 = ua, b = 0;
+        auto step = [&](auto&& unit) {
+          if (u0 + of_step < uz_all) {
+            u32x4* const to = reinterpret_cast<u32x4*>(s_buf + b * kStep) + wave * A::CB * 64 + lane;
+#pragma unroll
+            for (uint32_t c = 0; c < A::CB; ++c) to[c * 64] = st[c];
+            if (lane == 0) s_spoil[b][of_step] = spoils;
+          }
+          fetch(u0 + A::SU);
+          __syncthreads();
+          for (uint32_t k = turn; k < A::SU && u0 + k < uz; k += stride) {
+            const u32x4* const from = reinterpret_cast<const u32x4*>(s_buf + b * kStep) + k * 2 * A::CB * 64 + lane;
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+              for (int i = 0; i < KS; ++i) kf[t][i] = from[(t * KS + i) * 64];
+            unit(u0 + k, uni(s_spoil[b][k]), [&] {   // (not before: the registers of K are free then)
+              fence();
+#pragma unroll
+              for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < PS; ++i) vf[d][i] = from[(A::CB + d * PS + i) * 64];
+              fence();
+            });
+          }
+          u0 += A::SU;
+          b ^= 1;
+        };
+        // (one loop with both forms of a unit would hold the results twice)
+        const int32_t see_first = base + (int32_t)per_group(q0);   // what the item's first row sees
+        const uint32_t full_all = min(uz_all, see_first > 0 ? (uint32_t)see_first / UT : 0u);
+        while (u0 + A::SU <= full_all)
+          step([&](uint32_t, uint32_t spoilt, auto&& values) {
+            f32x4 s[NT][TT];
+            A::scores(kf, qf, s);
+            values();
+            if (spoilt) A::spoil(spoilt, lane, s);
+            bf16x8_t p[NT][PS];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) A::template weights<false>(cs, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
+            A::product(vf, p, o);
+          });
+        while (u0 < uz_all) step(ends_in);
+      } else {
+        auto load_k = [&](const typename A::Ids& x, uint32_t u) {
+          A::load_k(a, x, u, head, lane, [&](int t, int i, u32x4 v) { kf[t][i] = v; });
+        };
+        auto load_v = [&](const typename A::Ids& x, uint32_t u) {
+          A::load_v(a, x, u, head, lane, [&](int d, int i, u32x4 v) { vf[d][i] = v; });
+        };
+        uint32_t u = ua + turn;
+        typename A::Ids ids = {{0u, 0u, 0u, 0u}, 0u};
+        if (u < uz) {
+          ids = A::load_ids(a, trow, u, see);
+          load_k(ids, u);
+          load_v(ids, u);
+        }
+        // full units: every row sees every token; the next unit's pages, K and V are requested as
+        // soon as the registers they go to are free
+        const uint32_t full = min(uz, see_min > 0 ? (uint32_t)see_min / UT : 0u);
+        for (; u < full; u += stride) {
+          const bool more = u + stride < uz;
+          typename A::Ids next = ids;
+          if (more) next = A::load_ids(a, trow, u + stride, see);
+          f32x4 s[NT][TT];
+          A::scores(kf, qf, s);
+          fence();
+          if (more) load_k(next, u + stride);
+          fence();
+          if (ids.bad) A::spoil(ids.bad, lane, s);
+          bf16x8_t p[NT][PS];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) A::template weights<false>(cs, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
+          fence();
+          A::product(vf, p, o);
+          fence();
+          if (more) {
+            load_v(next, u + stride);
+            ids = next;
+          }
+        }
+        for (; u < uz; u += stride) {
+          ends_in(u, ids.bad, [] {});
+          if (u + stride < uz) {
+            ids = A::load_ids(a, trow, u + stride, see);
+            load_k(ids, u + stride);
+            load_v(ids, u + stride);
+          }
         }
       }
 
@@ -892,9 +1000,9 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
   }
 }
 
-template <int D, bool F8, int NT, int NW, int UT>
+template <int D, bool F8, int NT, int NW, int UT, bool ST = false>
 hipError_t attn_go(const AttnArgs& a, hipStream_t s) {
-  using A = Attn<D, F8, NT, NW, UT>;
+  using A = Attn<D, F8, NT, NW, UT, ST>;
   // no more workgroups than units that the widest table could fill
   const uint64_t tiles = ((uint64_t)a.m * a.group + (uint64_t)a.n_req * (16 * NT - 1)) / (16 * NT) + 1;
   const uint64_t units = (((uint64_t)a.max_pages << a.page_shift) + UT - 1) / UT;
@@ -909,7 +1017,7 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t s) {
   static_assert(A::kWG * 4 <= kTicketBytes, "tickets");
   b.grid = (uint32_t)wg;
   b.grid_inv = wg == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / wg);
-  hipLaunchKernelGGL((k_attn<D, F8, NT, NW, UT>), dim3((uint32_t)wg), dim3(64 * NW), 0, s, b);
+  hipLaunchKernelGGL((k_attn<D, F8, NT, NW, UT, ST>), dim3((uint32_t)wg), dim3(64 * NW), 0, s, b);
   return hipGetLastError();
 }
 
@@ -921,16 +1029,37 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t s) {
 // us; 25 query rows each 95 us with 32, 99 us with 64); 64 for more than two tiles, whose waves
 // take a tile each and read the same unit at once (80 query rows each 177 us with 32, 154 us
 // with 64).
+// Staged through LDS (BF16) where several waves read a tile of K and V often enough: with a
+// head_dim of 256, whose waves hold 16 rows, from the second tile on (24 requests of up to 8000
+// tokens, 4 key heads, 32 / 64 / 256 query rows each: 110 -> 100, 164 -> 124 and 585 -> 370 us;
+// prompts of 64 to 300 tokens, 512 query rows each, 38 -> 45 us); with 128 for more than one
+// item's tiles and pages of 64 or more, where a load of V^T touches 16 lines (256 query rows
+// each 216 -> 156 us, four prompts' 1280 244 -> 169 us; with pages of 16 166 -> 154 and 176 ->
+// 165 us; 80 rows, pages of 64, 96 -> 89 us).  Where the work does not suffice for items of
+// several tiles, nothing is shared (one request of 4096 tokens, 64 query rows of 256 22 -> 25
+// us, 256 of 128 29 -> 33 us).  With 64 prompts lose (four of 256 rows and up to 4096 tokens
+// 119 -> 124 us), and in E4M3, whose decoding costs a wave as much as the wait, 80 rows take 129
+// us either way.
 template <int D, bool F8>
 hipError_t attn_rows(const AttnArgs& a, hipStream_t s) {
   const uint64_t rows = ((uint64_t)a.m + a.n_req - 1) / a.n_req * a.group;
+  // Can there be items of several tiles?  With tables as wide as they are, as the kernel decides
+  // it: 16 units for each of 256 workgroups.
+  [[maybe_unused]] auto shared = [&](uint64_t tile, uint64_t unit) {
+    const uint64_t tiles = ((uint64_t)a.m * a.group + a.n_req * (tile - 1)) / tile * a.n_kv_heads;
+    return tiles * ((((uint64_t)a.max_pages << a.page_shift) + unit - 1) / unit) >= 16 * 256;
+  };
   if constexpr (D < 256) {
     if (rows > 16) {
       if constexpr (D == 128 && !F8)
         if (rows <= 32) return attn_go<D, F8, 2, 4, 32>(a, s);
+      if constexpr (D == 128 && !F8)
+        if (rows > 128 && a.page_shift >= 6 && shared(32, 64)) return attn_go<D, F8, 2, 4, 64, true>(a, s);
       return attn_go<D, F8, 2, 4, 64>(a, s);
     }
   }
+  if constexpr (D == 256 && !F8)
+    if (rows > 16 && shared(16, 32)) return attn_go<D, F8, 1, 4, 32, true>(a, s);
   return attn_go<D, F8, 1, 4, F8 || D < 128 ? 64 : 32>(a, s);
 }
 

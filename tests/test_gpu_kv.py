@@ -378,6 +378,56 @@ def test_attention(lens, rows, hq, hkv, d, page, f8):
     Ctx(np.random.default_rng([21, sum(lens), d]), lens, rows, hq, hkv, d, page, f8, start=1, tail=2).check()
 
 
+SHARED = [  # lens, rows, hq, hkv, d, page: several tiles of query rows read a cache together
+    ([9000, 5000], [40, 33], 32, 8, 128, 64),
+    ([9000, 3, 5000, 0, 64, 65], [40, 2, 60, 0, 64, 65], 32, 8, 128, 128),
+    ([1000], [40], 8, 2, 128, 64),
+    ([200, 129], [160, 129], 3, 3, 128, 256),
+    ([20000], [16], 64, 4, 128, 64),
+    ([9000, 8000, 300], [20, 7, 3], 16, 4, 256, 16),
+    ([9000, 0, 1, 6000], [3, 0, 1, 50], 36, 3, 256, 256),
+    ([5000, 4000], [64, 100], 4, 4, 256, 64),
+    ([33, 31, 96], [5, 31, 9], 5, 1, 256, 32),
+]
+
+
+@pytest.mark.parametrize("lens,rows,hq,hkv,d,page", SHARED)
+def test_attention_of_shared_tiles(lens, rows, hq, hkv, d, page):
+    say("attention of shared tiles", lens, rows, hq, hkv, d, page)
+    Ctx(np.random.default_rng([29, lens[0], rows[0], d]), lens, rows, hq, hkv, d, page, start=1, tail=2).check()
+
+
+@pytest.mark.parametrize("lens,rows,hq,hkv,d,page", [
+    ([5000, 4500, 130], [40, 50, 12], 32, 8, 128, 64), ([9000, 8000, 130], [20, 7, 3], 16, 4, 256, 16)])
+def test_attention_of_shared_tiles_ignores_what_lies_behind(lens, rows, hq, hkv, d, page):
+    """NaN in every free place, an infinite value that only the last row sees, a page that is none
+    and a length that is none: each reaches its own rows only."""
+    say("attention of shared tiles, what lies behind", lens, rows, d)
+    x = Ctx(np.random.default_rng([30, d]), lens, rows, hq, hkv, d, page)
+    clean = x.run().clone()
+    k, v = x.c.k.view(torch.int16), x.c.v.view(torch.int16)
+    used = np.zeros((x.n_pages, page), bool)
+    for r, n in enumerate(lens):
+        t = np.arange(n)
+        used[x.table[r, t // page], t % page] = True
+    free = torch.from_numpy(~used).to(DEV)
+    k.copy_(torch.where(free[:, None, :, None], 0x7fc0, k))
+    v.copy_(torch.where(free[:, None, None, :], 0x7fc0, v))
+    assert torch.equal(x.run(), clean)
+    x.check()
+    last = lens[0] - 1
+    v[int(x.table[0, last // page]), :, 3, last % page] = 0x7f80
+    got, keep = x.run().clone(), torch.ones_like(clean, dtype=torch.bool)
+    assert not torch.isfinite(got[rows[0] - 1, :, 3].float()).any()
+    keep[rows[0] - 1, :, 3] = False
+    assert torch.equal(got[keep], clean[keep])
+    x.table[0, 70 // page] = x.n_pages
+    x.lens[2] = -1
+    got = x.check()     # (the pieces of request 1 differ now, and so may its last bits)
+    mine = slice(rows[0], rows[0] + rows[1])
+    assert np.isfinite(got[mine]).all() and np.isnan(got[:rows[0]]).all() and np.isnan(got[mine.stop:]).all()
+
+
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_attention_many_requests(d, f8):
