@@ -10,8 +10,8 @@
 // 4g + 3 of each 16-token tile and wants 8 consecutive summed indices of it, and since the
 // order in which tokens are dealt to tile rows is free, tile row 4a + i takes the token that
 // makes a lane's scores 8 (BF16) or 16 (E4M3) consecutive tokens: the ones its 16-byte loads
-// of V^T hold.  Nothing passes through LDS inside the loop, and every load is 16 bytes used
-// as it comes.
+// of V^T hold.  Nothing has to pass through LDS inside the loop, and every load is 16 bytes
+// used as it comes.
 //
 // Where several tiles of query rows read the same keys, their waves can read K and V from LDS
 // instead: a step of 64 KB, in the operands' own order (so the reads have no conflicts), which
