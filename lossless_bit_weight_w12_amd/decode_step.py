@@ -18,7 +18,8 @@ decoding speed, and the 10.87x needs context", section "The mechanisms it found"
 With a DecodeAttention the step is a decoder's own: q and k are normed and turned per head and
 appended with v to the layer's paged cache (w12_qk_rope), the rows of every request attend over
 its cache (w12_attn_paged), and o reads that (o = attention W_o^T) in place of rms(q); the block
-tables are brought in line with the requests' lengths once per step (w12_kv_plan).
+tables are brought in line with the requests' lengths once per step (w12_kv_plan).  The accepted
+lengths of requests that the pool refused become -1 in an elementwise minimum of torch's.
 """
 from __future__ import annotations
 
@@ -34,7 +35,9 @@ class DecodeAttention:
     """The attention of a DecodeStack: request r keeps length[r] tokens in the cache and its
     new rows are req_off[r] .. req_off[r+1]-1 of the batch (int32 device tensors, read anew by
     every step: after a verification add the accepted tokens and the one that follows them,
-    length += accepted + 1; the tokens rejected are overwritten by the next step)."""
+    length += accepted + 1; the tokens rejected are overwritten by the next step).  A request
+    that the pool had too few pages for, or whose length is none, has accepted -1: it keeps its
+    length and comes again, with the same rows, once pages are free."""
     n_heads: int
     pages: object      # w12.PageTable, shared by the layers
     caches: list       # w12.KvCache per layer
@@ -132,7 +135,7 @@ class DecodeStack:
         """Marshal every call of the step once (on the current stream): the layers read
         and write the stack's own buffers; the step starts from self.h.  With attention the
         verification is of its requests: draft int32 [m], req_ndraft int32 [n_req] (see
-        w12.lmhead_verify_batched), accepted [n_req]."""
+        w12.lmhead_verify_batched), accepted [n_req], -1 also for a request without pages."""
         self.calls = [self._layer_calls(L, li == 0, li) for li, L in enumerate(self.layers)]
         if self.fused_rms:   # the final h, rescaled on its own for the LM head
             self.calls[-1].append(w12.prepare_rms(self.out["down"], self.h))
@@ -147,6 +150,15 @@ class DecodeStack:
         self.verify_call = w12.prepare_verify_batched(self.h, self.head, at.req_off, req_ndraft, draft,
                                                       self.argmax, self.accepted)
 
+    def _verify(self):
+        import torch
+        self.verify_call()
+        if self.attention is not None:
+            # The verification knows nothing of the cache: a refused request's rows are NaN and
+            # mismatch at once, accepted 0.  Its kv_len is -1, a served one's at least its rows
+            # and so at least what it accepts: the smaller of the two says both.
+            torch.minimum(self.accepted, self.kv_len, out=self.accepted)
+
     def run(self):
         """One step from the current contents of self.h (after prepare)."""
         if self.attention is not None:
@@ -154,7 +166,7 @@ class DecodeStack:
         for calls in self.calls:
             for c in calls:
                 c()
-        self.verify_call()
+        self._verify()
 
     def step(self, h0, draft, capture=(), req_ndraft=None):
         """Run every layer from h0 [m, hidden] and verify `draft` on the final h.
@@ -188,7 +200,7 @@ class DecodeStack:
                 caps[li] = {"in": ins, **{k: v.clone() for k, v in o.items()}}
                 if self.attention is not None:
                     caps[li]["turned"] = self.turned.clone()
-        self.verify_call()
+        self._verify()
         return self.h, self.argmax, self.accepted, caps
 
     def weight_bytes(self) -> int:
