@@ -85,7 +85,9 @@ class DecodeStack:
         i32 = dict(dtype=torch.int32, device=dev)
         self.kv_len = torch.empty_like(at.length)
         self.pos, self.slot = torch.empty(self.m, **i32), torch.empty(self.m, **i32)
-        # rows of no request are left as they are by the attention: zeros, so that o stays finite
+        # Rows of no request are left as they are by the attention: zeros here (so o is 0 and, with
+        # rms(0) = 0 / 0, the rest of the row NaN), later what they held when they were a
+        # request's.  What a step gives for them means nothing; no other row depends on it.
         self.turned, self.a = torch.zeros_like(self.out["q"]), torch.zeros_like(self.a)
         self.accepted = torch.empty(at.length.numel(), **i32)
         self.attn_ws = w12.attn_workspace(dev)
