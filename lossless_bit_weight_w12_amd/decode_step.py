@@ -91,6 +91,9 @@ class DecodeStack:
         self.turned, self.a = torch.zeros_like(self.out["q"]), torch.zeros_like(self.a)
         self.accepted = torch.empty(at.length.numel(), **i32)
         self.attn_ws = w12.attn_workspace(dev)
+        # The fills above are through before the stack is handed out: its steps may run on any
+        # stream, and a ticket that is cleared while a join is under way would end it early.
+        torch.cuda.current_stream(dev).synchronize()
 
     def _attention_calls(self, li: int):
         """Norm, rotation and append of the layer's heads, then the attention into self.a."""

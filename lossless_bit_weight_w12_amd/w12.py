@@ -932,7 +932,8 @@ _ATTN_WS = {}
 
 def attn_workspace(device="cuda"):
     """A workspace for attn_paged (zero tickets), for callers that keep their own: one for each
-    stream or captured graph that may run at the same time as others."""
+    stream or captured graph that may run at the same time as others.  It is zeroed on the current
+    stream: a call on another one has to wait for that."""
     torch = _torch()
     return torch.zeros(ATTN_WS_BYTES, dtype=torch.uint8, device=device)
 
