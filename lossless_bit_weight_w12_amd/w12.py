@@ -846,12 +846,45 @@ def _heads(name: str, t, m: int, n: int, d: int, device) -> int:
     return t.stride(0) if m > 1 else n * d
 
 
-def _apart(name: str, out, *ins):
-    for t in ins:
-        a, b = out.data_ptr(), t.data_ptr()
-        if out.numel() and t.numel() and a < b + t.numel() * t.element_size() \
-                and b < a + out.numel() * out.element_size():
-            raise ValueError(f"{name} overlaps another argument")
+def _rows(t):
+    """(address, bytes of a row, bytes between rows, rows) of a tensor [m, heads, d], or of any
+    contiguous one as a single row."""
+    shape, es = t.shape, t.element_size()
+    if len(shape) == 3 and shape[0] > 1:
+        return t.data_ptr(), shape[1] * shape[2] * es, t.stride(0) * es, shape[0]
+    nbytes = t.numel() * es
+    return t.data_ptr(), nbytes, nbytes, 1 if nbytes else 0
+
+
+def _meet(a, b) -> bool:
+    """Do two sets of rows (as _rows has them) share a byte?  Columns of one buffer do not."""
+    (p, la, sa, ma), (q, lb, sb, mb) = a, b
+    if not (ma and mb and la and lb) or p >= q + sb * (mb - 1) + lb or q >= p + sa * (ma - 1) + la:
+        return False
+    if ma == 1:
+        sa = sb
+    if mb == 1:
+        sb = sa
+    if sa != sb:
+        return any(_meet((p + i * sa, la, sb, 1), b) for i in range(ma))
+    # rows i and j meet where -lb < q - p + (j - i) sa < la: the smallest j - i past the left end
+    k = max((p - q - lb) // sa + 1, 1 - ma)
+    return k < mb and q - p + k * sa < la
+
+
+def _disjoint(what: str, outs, ins):
+    """Every tensor in outs {name: tensor} apart from the others and from those in ins."""
+    spans = []
+    for i, (name, t) in enumerate((*outs.items(), *ins.items())):
+        if t is None:
+            continue
+        rows = p, length, stride, n = _rows(t)
+        end = p + stride * (n - 1) + length
+        for other, q, q_end, of in spans:
+            if p < q_end and q < end and _meet(rows, of):
+                raise ValueError(f"{what}: {other} overlaps {name}")
+        if i < len(outs):
+            spans.append((name, p, end, rows))
 
 
 def _issue(name: str, args, device):
@@ -868,11 +901,9 @@ def _plan_args(pt: PageTable, length, req_off, kv_len, pos, slot):
     for name, t, size in (("length", length, n_req), ("req_off", req_off, n_req + 1),
                           ("kv_len", kv_len, n_req), ("pos", pos, m), ("slot", slot, m)):
         _int32(f"kv_plan: {name}", t, size, dev)
-    state = (pt.table, pt.held, pt.ring, pt.state)
-    for name, t, others in (("kv_len", kv_len, (length, req_off, pos, slot)),
-                            ("pos", pos, (length, req_off, slot)), ("slot", slot, (length, req_off))):
-        _apart(f"kv_plan: {name}", t, *others, *state)
     d = pt.desc()
+    _disjoint("kv_plan", {"kv_len": kv_len, "pos": pos, "slot": slot, "table": pt.table, "held": pt.held,
+                          "ring": pt.ring, "state": pt.state}, {"length": length, "req_off": req_off})
     args = (ctypes.byref(d), _ptr(length), _ptr(req_off), n_req, m, _ptr(kv_len),
             _ptr(pos) if m else None, _ptr(slot) if m else None, _stream(dev))
     return args, (pt, length, req_off, kv_len, pos, slot, d)
@@ -908,6 +939,11 @@ def _rope_args(q, k, v, cache: KvCache, rope: Rope, pos, slot, q_out):
     if q_out.data_ptr() == q.data_ptr() and strides[3] != strides[0]:
         raise ValueError("qk_rope: q_out may be q itself, with the same strides")
     r = rope.desc(d, dev)
+    ins = {"k": k, "v": v, "pos": pos, "slot": slot, "inv_freq": rope.inv_freq, "q_norm": rope.q_norm,
+           "k_norm": rope.k_norm}
+    if q_out.data_ptr() != q.data_ptr():
+        ins["q"] = q
+    _disjoint("qk_rope", {"q_out": q_out, "the cache's k": cache.k, "the cache's v": cache.v}, ins)
     args = (_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], m, n, ctypes.byref(c),
             ctypes.byref(r), _ptr(pos), _ptr(slot), _ptr(q_out), strides[3], _stream(dev))
     return args, (q, k, v, cache, rope, pos, slot, q_out, c, r)
@@ -962,14 +998,15 @@ def _attn_args(q, cache: KvCache, table, kv_len, req_off, out, scale, ws):
     c = cache.desc()
     dev, m, n, d, n_req = cache.device, q.shape[0], q.shape[1], c.head_dim, int(kv_len.numel())
     qs, os_ = _heads("attn_paged: q", q, m, n, d, dev), _heads("attn_paged: out", out, m, n, d, dev)
-    if out.data_ptr() == q.data_ptr() and m:
-        raise ValueError("attn_paged: out overlaps q")
     if table.dim() != 2 or table.shape[0] < n_req:
         raise ValueError("attn_paged: table must be [>= n_req, max_pages]")
     _int32("attn_paged: table", table, table.shape[0] * table.shape[1], dev)
     _int32("attn_paged: kv_len", kv_len, n_req, dev)
     _int32("attn_paged: req_off", req_off, n_req + 1, dev)
     ws = _attn_ws(dev, ws)
+    _disjoint("attn_paged", {"out": out, "ws": ws},
+              {"q": q, "the cache's k": cache.k, "the cache's v": cache.v, "table": table,
+               "kv_len": kv_len, "req_off": req_off})
     scale = d ** -0.5 if scale is None else float(scale)
     args = (_ptr(q), qs, m, n, ctypes.byref(c), _ptr(table), table.shape[1], _ptr(kv_len), _ptr(req_off),
             n_req, scale, _ptr(out), os_, _ptr(ws), ws.numel(), _stream(dev))
