@@ -448,7 +448,7 @@ typedef struct w12_pages {
   int32_t* table;         /* device [max_req][max_pages] page ids */
   int32_t* held;          /* device [max_req] pages each request holds */
   int32_t* ring;          /* device [n_pages] free page ids */
-  int32_t* state;         /* device [4]: head, count, 0, 0 */
+  int32_t* state;         /* device [4]: head, count, 0 (a ticket inside a call), 0 */
 } w12_pages;
 
 /* Brings the block tables in line with the requests' lengths and maps the new rows.
@@ -461,7 +461,8 @@ typedef struct w12_pages {
  * later one that needs any, is refused: its pages stay as they are.  Refused too is a request
  * with len[r] < 0, len[r] + rows_r > max_pages * page_size or held[r] outside
  * 0..max_pages; and every request, with nothing changed, when req_off is not
- * 0 <= req_off[0] <= req_off[1] <= ... <= m or state is not a ring's.
+ * 0 <= req_off[0] <= req_off[1] <= ... <= m or state is not a ring's (head, count, or a third
+ * value that is not zero).
  * Written: kv_len [n_req] = len[r] + rows_r, -1 if refused; pos [m] = the row's position in
  * its request; slot [m] = its place in the cache; both -1 for rows of a refused request or of
  * none; table, held, ring, state.  Table entries past want_r keep their old values.

@@ -12,6 +12,16 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kPlanCap = 1u << 30;   // sums of pages saturate here, above any pool
 
+// The ticket of a launch goes in steps of kTicket, so that the values a launch of G workgroups
+// can leave it at, i kTicket with i < G, are told from what a state that is none may hold.
+constexpr uint32_t kTicket = 0x9e3779b1u;
+__host__ __device__ constexpr uint32_t inverse(uint32_t a) {   // modulo 2^32, of an odd a: five Newton steps
+  uint32_t x = a;
+  for (int i = 0; i < 5; ++i) x *= 2 - a * x;
+  return x;
+}
+static_assert(inverse(kTicket) * kTicket == 1u, "kTicket's inverse");
+
 // Smallest i in 1..n with a[i] > v, minus one: the segment of v in the ascending offsets
 // a[0..n], for a[0] <= v < a[n] (segments may be empty).
 __device__ __forceinline__ uint32_t segment(const uint32_t* a, uint32_t n, uint32_t v) {
@@ -49,6 +59,9 @@ __global__ __launch_bounds__(T) void k_kv_plan(PlanArgs a) {
   const uint32_t shift = a.page_shift;
   const int32_t head0 = a.state[0], count0 = a.state[1];
   bool bad = head0 < 0 || (uint32_t)head0 >= a.n_pages || count0 < 0 || (uint32_t)count0 > a.n_pages;
+  // A ticket that did not begin at zero would leave the counts as they were beside new tables.
+  // (Workgroups that are through may have taken theirs already: any value a launch passes will do.)
+  bad |= (uint32_t)a.state[2] * inverse(kTicket) >= gridDim.x;
   auto want_of = [&](int32_t len, uint32_t rows) { return (uint32_t)(((uint64_t)len + rows + (1u << shift) - 1) >> shift); };
 
   // page counts, and their running sums: missing ones and those given back
@@ -184,7 +197,8 @@ __global__ __launch_bounds__(T) void k_kv_plan(PlanArgs a) {
   if (gridDim.x > 1) {
     if (t == 0) {
       uint32_t* const ticket = reinterpret_cast<uint32_t*>(a.state + 2);
-      s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+      s_last = __hip_atomic_fetch_add(ticket, kTicket, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               (gridDim.x - 1) * kTicket;
       if (s_last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
