@@ -132,3 +132,34 @@ def test_attention_counts_longest(d, f8):
 def test_attention_counts_items_of_several_tiles(rows, hq, hkv, d, page, f8):
     """Work enough that tiles of a head form one item (16 units for each of 256 workgroups)."""
     run_counts([20011, 5000, 70, 3], [rows, rows, min(rows, 70), 2], hq, hkv, d, page, f8, 16)
+
+
+@gpu
+@pytest.mark.parametrize("rows,hq,hkv,d,page,f8", FORMS)
+@pytest.mark.parametrize("lens", [[64, 3, 2, 300], [3000, 1, 777, 4096]])
+def test_attention_of_equal_values(lens, rows, hq, hkv, d, page, f8):
+    """Values that depend on head and dimension alone are what every row gets, exactly: the weights add
+    up to their divisor.  (Both sums have at most t + 3 units + 64 additions and fadings of 2^-24 each,
+    for t <= 4096 below 2^-10 together, and a BF16 value's neighbour begins 2^-9 away.)  Scores: one
+    token's 0, all others such that their weight lies just below the middle of two BF16 values."""
+    from tests.test_gpu_kv import Ctx
+    say("attention of equal values", lens, rows, hq, hkv, d, page, f8)
+    g = np.random.default_rng([93, lens[0], d])
+    x = Ctx(g, lens, [rows] * len(lens), hq, hkv, d, page, f8)
+    x.q.zero_()
+    x.q[..., 5] = 1
+    k = np.zeros((x.n_pages, hkv, page, d), np.float32)
+    k[..., 5] = -1
+    for r in range(len(lens)):
+        k[x.table[r, 0], :, 1 % min(lens[r], page), 5] = 0
+    x.c.k.copy_(torch.from_numpy(k).to(x.c.k.dtype).to(DEV))
+    value = torch.from_numpy(g.standard_normal((hkv, d)).astype(np.float32)).to(x.c.v.dtype).to(DEV)
+    x.c.v.copy_(value[None, :, :, None].expand(x.n_pages, hkv, d, page))
+    weight = 0.5 * (1 + 0.98 * 2.0 ** -8)
+    got = x.run(scale=-float(np.log(weight)) / x.c.k_scale)
+    want = (value.float() * x.c.v_scale).bfloat16().repeat_interleave(hq // hkv, 0)
+    a = 0
+    for n in lens:
+        for i in range(rows):
+            assert torch.equal(got[a + i], want if n - rows + i >= 0 else torch.zeros_like(want)), (n, i)
+        a += rows
