@@ -34,10 +34,12 @@ MATS = ("q", "k", "v", "o", "gate", "up", "down")
 class DecodeAttention:
     """The attention of a DecodeStack: request r keeps length[r] tokens in the cache and its
     new rows are req_off[r] .. req_off[r+1]-1 of the batch (int32 device tensors, read anew by
-    every step: after a verification add the accepted tokens and the one that follows them,
-    length += accepted + 1; the tokens rejected are overwritten by the next step).  A request
-    that the pool had too few pages for, or whose length is none, has accepted -1: it keeps its
-    length and comes again, with the same rows, once pages are free."""
+    every step).  After a verification length += min(accepted + 1, the request's rows): its first
+    row's token and the accepted ones stay, the rejected ones are overwritten by the next step,
+    a request without rows stays as it is, and of a request whose last row had a draft too, that
+    one is no row yet.  A request that the pool had too few pages for, or whose length is none,
+    has accepted -1: it keeps its length and comes again, with the same rows, once pages are
+    free."""
     n_heads: int
     pages: object      # w12.PageTable, shared by the layers
     caches: list       # w12.KvCache per layer

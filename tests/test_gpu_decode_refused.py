@@ -105,3 +105,33 @@ def test_refused_request_in_a_graph():
             stack.run()
             torch.cuda.synchronize()
             assert stack.accepted.cpu().numpy().tolist() == got.tolist()
+
+
+def test_lengths_never_pass_what_was_appended():
+    """length += min(accepted + 1, rows) with a request without rows, one without drafts, and one whose
+    last row has a draft too, when every draft is right and when none is."""
+    say("lengths after a step")
+    g = np.random.default_rng(75)
+    m = sum(ROWS)
+    stack, at = stack_of(g, True, m, 40)
+    rows = np.array([3, 0, 5, 2])
+    nd = i32([2, 0, 5, 0])
+    off = np.concatenate([[0], np.cumsum(rows)])
+    at.req_off.copy_(i32(off))
+    start = [20, 7, 33, 0]
+    x0 = to_dev(wi.gaussian_bf16((m, HID), 1.0, g), torch).view(torch.bfloat16)
+    at.length.copy_(i32(start))
+    am = stack.step(x0, i32(np.zeros(m)), req_ndraft=nd)[1].clone()
+    for draft, want in ((am, [2, 0, 5, 0]), ((am + 1) % VOCAB, [0, 0, 0, 0])):
+        at.length.copy_(i32(start))
+        acc = stack.step(x0, draft, req_ndraft=nd)[2]      # (the same tokens to the same places)
+        assert acc.cpu().tolist() == want
+        at.length += torch.minimum(acc + 1, i32(rows))
+        got = at.length.cpu().numpy()
+        assert got.tolist() == [s + min(a + 1, r) for s, a, r in zip(start, want, rows)]
+        assert (got <= stack.kv_len.cpu().numpy()).all()
+    # a pool that holds nothing for request 3: refused and idle requests keep their lengths
+    at.length.copy_(i32([20, 7, 33, 12 * PAGE]))
+    acc = stack.step(x0, am, req_ndraft=nd)[2]
+    at.length += torch.minimum(acc + 1, i32(rows))
+    assert at.length.cpu().tolist() == [23, 7, 38, 12 * PAGE] and acc.cpu().tolist() == [2, 0, 5, -1]
