@@ -222,7 +222,8 @@ class DecodeStack:
                 t = L[name]
                 total += 2 * m * (t.k + t.n)
             if not self.fused_rms:
-                for name in ("q", "o", "up", "down"):     # rescales: read + write
+                # rescales: read + write (with attention q has none)
+                for name in ("q", "o", "up", "down")[self.attention is not None:]:
                     total += 2 * 2 * m * L[name].n
         if self.fused_rms:                                # the final h: read + write
             total += 2 * 2 * m * self.layers[-1]["down"].n

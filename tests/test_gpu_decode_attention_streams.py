@@ -1,4 +1,4 @@
-"""A stack with attention built on one stream and run on another."""
+"""A stack with attention built on one stream and run on another; and its byte count."""
 import numpy as np
 import pytest
 
@@ -6,7 +6,7 @@ torch = pytest.importorskip("torch")
 import w12_inputs as wi  # noqa: E402
 from lossless_bit_weight_w12_amd.decode_step import DecodeStack  # noqa: E402
 from tests.gpu_util import say, to_dev  # noqa: E402
-from tests.test_gpu_decode_attention import HID, ROWS, VOCAB, build, i32  # noqa: E402
+from tests.test_gpu_decode_attention import D, HID, HQ, NL, ROWS, VOCAB, build, i32  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,14 @@ def test_stack_built_on_a_busy_stream():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_bytes_of_a_step_with_attention():
+    """Without fused rescales a step with attention has one rescale less per layer, that of q: the
+    attention reads its heads."""
+    m = sum(ROWS)
+    plain, at, *_ = build(np.random.default_rng(76), False, False, m)
+    chain = DecodeStack(plain.layers, plain.head, m, fused_rms=False)
+    assert chain.io_bytes() - plain.io_bytes() == NL * 2 * 2 * m * HQ * D
+    fused = DecodeStack(plain.layers, plain.head, m)
+    assert DecodeStack(plain.layers, plain.head, m, attention=at).io_bytes() == fused.io_bytes()
