@@ -519,8 +519,9 @@ w12_status w12_qk_rope(const uint16_t* q, uint64_t q_stride, const uint16_t* k, 
 /* out[row][h] = sum_t softmax_t(scale * q[row][h] . K[t]) V[t], K and V of head h / (n_heads /
  * n_kv_heads): row i of the rows_r rows of request r sees the tokens t <= kv_len[r] - rows_r
  * + i (the last row sees all kv_len[r] tokens, so the draft block is causal).  FP32 scores,
- * maxima and sums; the weights, relative to the largest, are rounded to BF16 in the second product
- * and in the sum that it is divided by.  A row that sees no token gets zeros.  What lies in the cache behind a row's last token never reaches it, NaN
+ * maxima and sums; the weights, relative to the largest, are rounded in the second product: to BF16
+ * (as in the sum that it is divided by), over an E4M3 cache to FP16.  A row that sees no token gets
+ * zeros.  What lies in the cache behind a row's last token never reaches it, NaN
  * included.  Rows of no request are left as they were.  A request whose kv_len is outside
  * 0 .. max_pages * page_size (kv_len -1: refused by w12_kv_plan) gets NaN, and so does a row
  * that sees a token whose table entry is outside 0 .. n_pages - 1; every row gets NaN when

@@ -39,6 +39,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
 // Workgroups of a launch, at most (one ticket each): one per CU; with one tile of query rows, so
 // that the registers allow it, two or four where a unit's K and V (`bytes`) are so small that
@@ -57,6 +58,11 @@ __device__ __forceinline__ uint32_t uni(uint32_t v) { return __builtin_amdgcn_re
 
 __device__ __forceinline__ uint32_t bf_pack(float a, float b) {
   const __bf16 x = (__bf16)a, y = (__bf16)b;   // round to nearest even
+  return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+}
+
+__device__ __forceinline__ uint32_t f16_pack(float a, float b) {
+  const _Float16 x = (_Float16)a, y = (_Float16)b;   // round to nearest even
   return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
 }
 
@@ -182,6 +188,10 @@ struct Attn {
   // What an item costs a workgroup beside its units (its queries' load, the join, the writes:
   // about 15000 cycles under load, the time of 128 KB), in units.
   static constexpr uint32_t kLead = 131072 / (2 * UT * D * ES);
+  // Weights of E4M3 values are times 2^15 (and so are their sums and products: the quotient is the
+  // same), 32768 at most: FP16 keeps 11 bits of them down to 2^-29 of the largest, and a part of
+  // them down to 2^-39.
+  static constexpr float kUp = F8 ? 15.f : 0.f;
   static_assert(!F8 || UT == 64, "an E4M3 lane load holds 16 tokens of a 64-token unit");
 
   // Page ids of a unit's 16-token groups; groups past `end` read page 0 (masked).
@@ -258,7 +268,8 @@ struct Attn {
     }
   }
 
-  // The A operand of step s (32 dimensions or tokens) from the lane's loads.
+  // Operands of step s (32 dimensions or tokens) from the lane's loads: of the first product in
+  // BF16, the type of q, of the second in BF16, or in FP16 for E4M3.
   template <int L>
   static __device__ __forceinline__ bf16x8_t operand(const u32x4 (&x)[L], int s) {
     if constexpr (F8) {
@@ -273,6 +284,28 @@ struct Attn {
     } else {
       return __builtin_bit_cast(bf16x8_t, x[s]);
     }
+  }
+
+  template <int L>
+  static __device__ __forceinline__ u32x4 operand_v(const u32x4 (&x)[L], int s) {
+    if constexpr (F8) {
+      u32x4 o;   // every E4M3 value is an FP16 value
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = x[s / 2][2 * (s & 1) + h];
+        o[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+        o[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
+      }
+      return o;
+    } else {
+      return x[s];
+    }
+  }
+  static __device__ __forceinline__ f32x4 mfma_v(u32x4 v, u32x4 p, f32x4 o) {
+    if constexpr (F8)
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, v), __builtin_bit_cast(f16x8_t, p), o, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, p), o, 0, 0, 0);
   }
 
   // S^T of a unit.
@@ -294,16 +327,16 @@ struct Attn {
   }
 
   // O^T += V^T P^T.
-  static __device__ __forceinline__ void product(const u32x4 (&vf)[DT][VL], const bf16x8_t (&p)[NT][PS],
+  static __device__ __forceinline__ void product(const u32x4 (&vf)[DT][VL], const u32x4 (&p)[NT][PS],
                                                  f32x4 (&o)[NT][DT]) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
 #pragma unroll
       for (int i = 0; i < PS; ++i) {
-        const bf16x8_t vv = operand(vf[d], i);
+        const u32x4 vv = operand_v(vf[d], i);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, p[nt][i], o[nt][d], 0, 0, 0);
+          o[nt][d] = mfma_v(vv, p[nt][i], o[nt][d]);
       }
       fence();
     }
@@ -321,19 +354,21 @@ struct Attn {
     }
   }
 
-  // One step of the running softmax of a query row: raw scores s to weights exp2(c (s - top)),
-  // rounded to BF16 for the second product (the type of V, 2^-8 of each weight at most), their
-  // FP32 sum, and the old results faded where the maximum rose.  The sum is that of the rounded
-  // weights, so that they add up to the divisor: the result is a mean of the values seen,
-  // whatever the rounding, and what remains of it is their spread times 2^-8 at most (with the
-  // unrounded sum 64 equal values came back 2^-8 too small; no case's time differs).  Weights in
-  // two BF16 parts would leave the rounding of the result alone, 0.0016 of the norm in place of
-  // 0.0017, in E4M3 draft blocks of 0.0020, and cost a third product: those 58 -> 62 us, 80 query
-  // rows 146 -> 154 us and in E4M3 130 -> 152 us.  top is the same in the four lanes of a row, sum
-  // is each lane's own part.  A NaN score leaves the maximum alone and makes the sum NaN.
+  // One step of the running softmax of a query row: raw scores s to weights exp2(c (s - top)) for
+  // the second product, their FP32 sum, and the old results faded where the maximum rose.
+  // A weight enters the product in the type of V's operand.  BF16, 2^-8 of it at most: the sum is
+  // that of the rounded weights, so that they add up to the divisor and the result is a mean of
+  // the values seen (with the unrounded sum 64 equal values came back 2^-8 too small; no case's
+  // time differs).  E4M3 values go in FP16, with 2^-11 of each weight, and their sum is taken as
+  // it comes: 24 draft blocks 0.0017 of the norm from 64 bits, the rounding of the result alone, in
+  // place of 0.0020, and 80 query rows 133 -> 130 us for the shorter sum.  BF16 weights in two parts
+  // and a third product would bring the rest there too, 0.0016 in place of 0.0017, for 80 query
+  // rows 146 -> 154 us and for prompts 169 -> 189 us: not taken.
+  // top is the same in the four lanes of a row, sum is each lane's own part.  A NaN score leaves
+  // the maximum alone and makes the sum NaN.
   template <bool EDGE>
   static __device__ __forceinline__ void weights(float c, uint32_t seen, f32x4 (&s)[TT], float& top, float& sum,
-                                                 f32x4 (&o)[DT], bf16x8_t (&p)[PS]) {
+                                                 f32x4 (&o)[DT], u32x4 (&p)[PS]) {
     float mx = top;
 #pragma unroll
     for (int t = 0; t < TT; ++t)
@@ -348,26 +383,32 @@ struct Attn {
       top = mx;
     }
     // (the distance from the maximum first, then its scaling: with c s - c top in one step and c top
-    // rounded, scores past 2^22 gave weights that differed between units, past 2^31 NaN; heads of 64
-    // 108.4 -> 110.2 us, 24 requests with heads of 128 83.6 -> 84.4 us, others as before)
+    // rounded, scores past 2^22 gave weights that differed between units, past 2^31 NaN; it costs 1 %
+    // at most: 24 requests with heads of 128 83.9 -> 84.9 us)
     const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = pow2((s[t][i] - base) * c);
+        const float e = pow2(F8 ? fmaf(s[t][i] - base, c, kUp) : (s[t][i] - base) * c);
         s[t][i] = !EDGE || ((seen >> (4 * t + i)) & 1u) ? e : 0.f;
       }
 #pragma unroll
     for (int i = 0; i < PS; ++i) {
       const f32x4 x = s[2 * i], y = s[2 * i + 1];
-      const u32x4 w = {bf_pack(x[0], x[1]), bf_pack(x[2], x[3]), bf_pack(y[0], y[1]), bf_pack(y[2], y[3])};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sum += __uint_as_float(w[j] << 16);
-        sum += __uint_as_float(w[j] & 0xffff0000u);
+        const float u = (j < 2 ? x : y)[2 * (j & 1)], v = (j < 2 ? x : y)[2 * (j & 1) + 1];
+        if constexpr (F8) {
+          p[i][j] = f16_pack(u, v);
+          sum += u;
+          sum += v;
+        } else {
+          p[i][j] = bf_pack(u, v);
+          sum += __uint_as_float(p[i][j] << 16);
+          sum += __uint_as_float(p[i][j] & 0xffff0000u);
+        }
       }
-      p[i] = __builtin_bit_cast(bf16x8_t, w);
     }
     fence();
   }
@@ -662,7 +703,7 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
         values();
         if (spoilt) A::spoil(spoilt, lane, s);
         const int32_t t_lane = (int32_t)(u * UT) + (F8 ? 16 : 8) * (lane >> 4);   // the lane's first token
-        bf16x8_t p[NT][PS];
+        u32x4 p[NT][PS];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           uint32_t seen = 0;   // bit 4t + i: the row sees the token
@@ -712,7 +753,7 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
               f32x4 sum_d = o[nt][d];
 #pragma unroll
               for (int i = 0; i < PS; ++i)
-                sum_d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A::operand(x, i), p[nt][i], sum_d, 0, 0, 0);
+                sum_d = A::mfma_v(A::operand_v(x, i), p[nt][i], sum_d);
               if (!apart || lim[nt] == row) o[nt][d] = sum_d;   // a lane holds one row's sums
             }
             fence();
@@ -775,7 +816,7 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
             A::scores(kf, qf, s);
             values();
             if (spoilt) A::spoil(spoilt, lane, s);
-            bf16x8_t p[NT][PS];
+            u32x4 p[NT][PS];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) A::template weights<false>(cs, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
             A::product(vf, p, o);
@@ -808,7 +849,7 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
           if (more) load_k(next, u + stride);
           fence();
           if (ids.bad) A::spoil(ids.bad, lane, s);
-          bf16x8_t p[NT][PS];
+          u32x4 p[NT][PS];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) A::template weights<false>(cs, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
           fence();

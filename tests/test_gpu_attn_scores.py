@@ -89,3 +89,42 @@ def test_attention_equal_large_scores(rows, hq, hkv, d, page, f8):
                 want = 1 + (e // 2) / e if e else 0.0
                 assert (np.abs(got[a + i] - want) <= 2.0 ** -8 * (1 + 2.0 ** -8) * want).all(), (n, i)
             a += rows
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d,page", [f[:5] for f in FORMS if f[5]])
+def test_attention_e4m3_weights(rows, hq, hkv, d, page):
+    """Weights over an E4M3 cache keep 11 bits: n tokens of weight 0.502 and value 1 stand against one of
+    weight 1 and value -n / 2, so that what is left of their sum is the weight's last bits."""
+    say("E4M3 weights", rows, hq, hkv, d, page)
+    g = np.random.default_rng([97, d])
+    lens, weight = [33, 65, 257], 0.5 * (1 + 0.98 * 2.0 ** -8)
+    value = lambda r, t: np.where(t == 0, -(lens[r] // 2.0), 1.0)
+    x = filled(g, lens, rows, hq, hkv, d, page, True, lambda r, t: {5: np.where(t == 0, 0.0, -1.0)}, value, {5: 1.0})
+    got = x.run(scale=-float(np.log(weight))).double().cpu().numpy()
+    a = 0
+    for r, n in enumerate(lens):
+        for i in range(rows):
+            t = np.arange(n - rows + i + 1)
+            w, v = np.where(t == 0, 1.0, weight), value(r, t)
+            want, size = (w * v).sum() / w.sum(), (w * np.abs(v)).sum() / w.sum()
+            # weights: half a step of FP16, 2^-11; exp2, scale and FP32 sums below 2^-18; the result: 2^-8
+            tol = 2.0 ** -8 * abs(want) + (2.0 ** -11 + 2.0 ** -18) * (1 + 2.0 ** -7) * size
+            assert (np.abs(got[a + i] - want) <= tol).all(), (n, i, got[a + i].ravel()[0], want)
+        a += rows
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d,page", [f[:5] for f in FORMS if f[5]])
+def test_attention_e4m3_small_weights(rows, hq, hkv, d, page):
+    """One token of weight 1 with value 0 and thousands of weight 2^-18 with value 256: none is lost."""
+    say("E4M3 small weights", rows, hq, hkv, d, page)
+    g = np.random.default_rng([98, d])
+    x = filled(g, LENS, rows, hq, hkv, d, page, True, lambda r, t: {5: np.where(t == 0, 0.0, -18.0)},
+               lambda r, t: np.where(t == 0, 0.0, 256.0), {5: 1.0})
+    got = x.run(scale=float(np.log(2))).double().cpu().numpy()
+    a = 0
+    for n in LENS:
+        for i in range(rows):
+            e = max(n - rows + i + 1, 0)
+            want = 256 * (e - 1) * 2.0 ** -18 / (1 + (e - 1) * 2.0 ** -18) if e else 0.0
+            assert (np.abs(got[a + i] - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12) * want).all(), (n, i)
+        a += rows
