@@ -44,7 +44,7 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 // Workgroups of a launch, at most (one ticket each): one per CU; with one tile of query rows, so
 // that the registers allow it, two or four where a unit's K and V (`bytes`) are so small that
 // four waves do not keep enough reads in flight (64 requests of up to 8191 tokens with heads of
-// 64: in BF16 117 -> 109 us with two, in E4M3 90 -> 71 us with two, 67 us with four).
+// 64: in BF16 117 -> 109 us with two, in E4M3 90 -> 71 us with two, 68 us with four).
 constexpr uint32_t workgroups(int nt, int bytes) {
   return nt > 1 || bytes > 16384 ? 256 : (bytes > 8192 ? 512 : 1024);
 }
@@ -501,8 +501,8 @@ __global__ __launch_bounds__(64 * NW, workgroups(NT, 2 * UT * D * (F8 ? 1 : 2)) 
   }
   // A long item is a tile, or, where there is work for every workgroup anyway, up to NW tiles of
   // one head, one for each wave, so that K and V are read once for all of them (16 rows of 5
-  // heads each against 98k tokens: 207 us apart, 170 us together; but 8 heads of 1 to 4 rows
-  // against 10k tokens, 2 units per workgroup: 26 us apart, 36 us together).
+  // heads each against 98k tokens: 202 us apart, 146 us together; but 8 heads of 1 to 4 rows
+  // against 10k tokens, 2 units per workgroup: 22 us apart, 29 us together).
   auto per_grid = [&](uint32_t x) { return div_by(x, given.grid, given.grid_inv); };
   const uint32_t span = all_units >= 16 * given.grid ? NW : 1u;   // tiles of a long item, at most
   const uint32_t mean = min(per_grid((span > 1 ? few_units : all_units) + given.grid - 1), 1u << 20);
@@ -1077,20 +1077,24 @@ hipError_t attn_go(const AttnArgs& a, hipStream_t s) {
 // Tile of query rows by the mean number per request: 16 while it holds them, else 32 (what the
 // registers hold; with a head_dim of 256 that is 16).  Units of 64 tokens in E4M3 (16 bytes of
 // V^T).  In BF16 of 32 where 64 do not fit (256), and at 128, where a short request's one unit
-// is half the work (300 requests of up to 100 tokens 23 us with 64, 19 us with 32; one of 17
-// tokens 7.4 and 6.1 us; 98k tokens in 24 requests 84 us either way, 131k in one 102 and 105
-// us; 25 query rows each 95 us with 32, 99 us with 64); 64 for more than two tiles, whose waves
-// take a tile each and read the same unit at once (80 query rows each 177 us with 32, 154 us
-// with 64).
-// Staged through LDS (BF16) where several waves read a tile of K and V often enough: with a
-// head_dim of 256, whose waves hold 16 rows, from the second tile on (24 requests of up to 8000
-// tokens, 4 key heads, 32 / 64 / 256 query rows each: 110 -> 100, 164 -> 124 and 585 -> 370 us;
-// prompts of 64 to 300 tokens, 512 query rows each, 38 -> 45 us); with 128 for more than one
-// item's tiles and pages of 64 or more, where a load of V^T touches 16 lines (256 query rows
-// each 216 -> 156 us, four prompts' 1280 244 -> 169 us; with pages of 16 166 -> 154 and 176 ->
-// 165 us; 80 rows, pages of 64, 96 -> 89 us).  Where the work does not suffice for items of
-// several tiles, nothing is shared (one request of 4096 tokens, 64 query rows of 256 22 -> 25
-// us, 256 of 128 29 -> 33 us).  With 64 prompts lose (four of 256 rows and up to 4096 tokens
+// is half the work (300 requests of up to 100 tokens 24 us with 64, 19 us with 32; one of 17
+// tokens 7.7 and 6.2 us; 98k tokens in 24 requests 83 and 84 us, 131k in one 103 and 105 us; 25
+// query rows each 94 us with 64, 91 us with 32); 64 for more than two tiles, whose waves take a
+// tile each and read the same unit at once (80 query rows each 165 us with 32, 146 us with 64).
+// Staged through LDS (BF16) where several waves read a tile of K and V often enough.  How long the
+// requests are is not known here, only how wide the table is, and on short ones staging loses
+// (the step's barriers, no items of a wave's own, and where the work does not suffice for items of
+// several tiles nothing is shared): so it is taken where long ones gain more than that.
+// With a head_dim of 256, whose waves hold 16 rows, from the second tile on (24 requests of up to
+// 8000 tokens, 4 key heads, 32 / 48 / 64 / 128 / 256 query rows each: 110 -> 98, 139 -> 111, 163 ->
+// 123, 303 -> 207 and 583 -> 364 us; 8 of up to 500, 32 / 64 / 128 rows 16.4 -> 16.8, 24 -> 26, 29 ->
+// 31 us; one of 4096, 64 / 128 rows 22.5 -> 25, 52 -> 44 us; prompts of 64 to 300 tokens, 512 rows
+// each, 38 -> 45 us).  With 128 for more than one item's tiles and pages of 64 or more, where a load
+// of V^T touches 16 lines (24 requests of up to 8000 tokens, 256 rows each 215 -> 157 us, four prompts
+// 244 -> 169 us; one of 4096 30 -> 32 us, 8 of up to 500 28 -> 31 us); below, the long ones gain less
+// (128 rows, pages of 64, 121 -> 101 us, 80 rows 95 -> 87 us; 256 rows, pages of 32, 174 -> 154 us, of
+// 16, 166 -> 154 us) and the short ones lose as much (256 rows, pages of 16, one of 4096 tokens 29 ->
+// 32 us, 8 of up to 500 26 -> 30 us).  With 64 prompts lose (four of 256 rows and up to 4096 tokens
 // 119 -> 124 us), and in E4M3, whose decoding costs a wave as much as the wait, 80 rows take 129
 // us either way.
 template <int D, bool F8>

@@ -1155,7 +1155,8 @@ def prepare_qk_rope(q, k, v, cache: KvCache, rope: Rope, pos, slot, q_out) -> Pr
 
 
 def prepare_attn_paged(q, cache: KvCache, table, kv_len, req_off, out, scale=None, ws=None) -> Prepared:
-    """attn_paged into out.  A captured prepared call keeps its workspace: graphs that may run
-    at the same time are prepared with a ws of their own (attn_workspace)."""
+    """attn_paged into out.  A captured prepared call keeps its workspace, by default that of the
+    stream it was prepared on: graphs that may run at the same time, or beside calls on that
+    stream, are prepared with a ws of their own (attn_workspace)."""
     args, keep = _attn_args(q, cache, table, kv_len, req_off, out, scale, ws)
     return _prepared("w12_attn_paged", args, keep, cache.device)

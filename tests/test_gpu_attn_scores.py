@@ -114,17 +114,19 @@ def test_attention_e4m3_weights(rows, hq, hkv, d, page):
 
 
 @pytest.mark.parametrize("rows,hq,hkv,d,page", [f[:5] for f in FORMS if f[5]])
-def test_attention_e4m3_small_weights(rows, hq, hkv, d, page):
-    """One token of weight 1 with value 0 and thousands of weight 2^-18 with value 256: none is lost."""
-    say("E4M3 small weights", rows, hq, hkv, d, page)
+@pytest.mark.parametrize("power", [18, 33])
+def test_attention_e4m3_small_weights(power, rows, hq, hkv, d, page):
+    """One token of weight 1 with value 0 and thousands of weight 2^-power with value 256: none is lost."""
+    say("E4M3 small weights", power, rows, hq, hkv, d, page)
     g = np.random.default_rng([98, d])
-    x = filled(g, LENS, rows, hq, hkv, d, page, True, lambda r, t: {5: np.where(t == 0, 0.0, -18.0)},
-               lambda r, t: np.where(t == 0, 0.0, 256.0), {5: 1.0})
+    x = filled(g, LENS, rows, hq, hkv, d, page, True,
+               lambda r, t: {5: np.where(t == 0, 0.0, -float(power // 2)), 6: np.where(t == 0, 0.0, -float(power % 2))},
+               lambda r, t: np.where(t == 0, 0.0, 256.0), {5: 2.0, 6: 1.0})
     got = x.run(scale=float(np.log(2))).double().cpu().numpy()
-    a = 0
+    a, w = 0, 2.0 ** -power
     for n in LENS:
         for i in range(rows):
             e = max(n - rows + i + 1, 0)
-            want = 256 * (e - 1) * 2.0 ** -18 / (1 + (e - 1) * 2.0 ** -18) if e else 0.0
+            want = 256 * (e - 1) * w / (1 + (e - 1) * w) if e else 0.0
             assert (np.abs(got[a + i] - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12) * want).all(), (n, i)
         a += rows
