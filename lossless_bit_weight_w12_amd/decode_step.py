@@ -164,7 +164,7 @@ class DecodeStack:
             # The verification knows nothing of the cache: a refused request's rows are NaN and
             # mismatch at once, accepted 0.  Its kv_len is -1, a served one's at least its rows
             # and so at least what it accepts: the smaller of the two says both.
-            torch.minimum(self.accepted, self.kv_len, out=self.accepted)
+            torch.minimum(self.accepted, self.kv_len.view(-1), out=self.accepted)
 
     def run(self):
         """One step from the current contents of self.h (after prepare)."""

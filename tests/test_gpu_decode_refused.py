@@ -135,3 +135,17 @@ def test_lengths_never_pass_what_was_appended():
     acc = stack.step(x0, am, req_ndraft=nd)[2]
     at.length += torch.minimum(acc + 1, i32(rows))
     assert at.length.cpu().tolist() == [23, 7, 38, 12 * PAGE] and acc.cpu().tolist() == [2, 0, 5, -1]
+
+
+def test_lengths_as_a_column():
+    """Lengths of shape [n, 1] are taken as those of shape [n]."""
+    g = np.random.default_rng(77)
+    m = sum(ROWS)
+    stack, at = stack_of(g, True, m, 4)
+    nd, draft = i32([r - 1 for r in ROWS]), i32(g.integers(0, VOCAB, m))
+    x0 = to_dev(wi.gaussian_bf16((m, HID), 1.0, g), torch).view(torch.bfloat16)
+    at.length.copy_(i32([2, 2, 12, 2]))
+    want = stack.step(x0, draft, req_ndraft=nd)[2].cpu().tolist()
+    column = DecodeAttention(**{**at.__dict__, "length": at.length.view(-1, 1)})
+    other = DecodeStack(stack.layers, stack.head, m, attention=column)
+    assert other.step(x0, draft, req_ndraft=nd)[2].cpu().tolist() == want
