@@ -153,6 +153,8 @@ class DecodeStack:
             return
         if req_ndraft is None:
             raise ValueError("a step with attention verifies its requests: req_ndraft is missing")
+        import torch
+        self.stream = torch.cuda.current_stream(self.head.device)
         self.plan_call = w12.prepare_kv_plan(at.pages, at.length, at.req_off, self.kv_len, self.pos, self.slot)
         self.verify_call = w12.prepare_verify_batched(self.h, self.head, at.req_off, req_ndraft, draft,
                                                       self.argmax, self.accepted)
@@ -164,7 +166,8 @@ class DecodeStack:
             # The verification knows nothing of the cache: a refused request's rows are NaN and
             # mismatch at once, accepted 0.  Its kv_len is -1, a served one's at least its rows
             # and so at least what it accepts: the smaller of the two says both.
-            torch.minimum(self.accepted, self.kv_len.view(-1), out=self.accepted)
+            with torch.cuda.stream(self.stream):   # that of the prepared calls
+                torch.minimum(self.accepted, self.kv_len.view(-1), out=self.accepted)
 
     def run(self):
         """One step from the current contents of self.h (after prepare)."""

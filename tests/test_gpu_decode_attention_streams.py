@@ -44,3 +44,29 @@ def test_bytes_of_a_step_with_attention():
     assert chain.io_bytes() - plain.io_bytes() == NL * 2 * 2 * m * HQ * D
     fused = DecodeStack(plain.layers, plain.head, m)
     assert DecodeStack(plain.layers, plain.head, m, attention=at).io_bytes() == fused.io_bytes()
+
+
+def test_run_from_another_stream():
+    """A step prepared on one stream, which is busy (a bounded spin), and run while another is current:
+    all of it, the accepted lengths of refused requests too, happens on the first."""
+    say("run from another stream")
+    g = np.random.default_rng(78)
+    m = sum(ROWS)
+    stack, at, *_ = build(g, True, False, m)
+    nd, draft = i32([r - 1 for r in ROWS]), i32(g.integers(0, VOCAB, m))
+    x0 = to_dev(wi.gaussian_bf16((m, HID), 1.0, g), torch).view(torch.bfloat16)
+    at.length.copy_(i32([20, -1, 7, 300]))      # no length, and one past the table
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        stack.prepare(draft, nd)
+    for _ in range(3):
+        stack.accepted.fill_(100)
+        stack.h.copy_(x0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        stack.run()
+        torch.cuda.synchronize()
+        got = stack.accepted.cpu().tolist()
+        assert got[1] == got[3] == -1 and 0 <= got[0] <= 2 and 0 <= got[2] <= 4
