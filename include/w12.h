@@ -5,7 +5,8 @@
  * rows for several requests verified together), the greedy verification epilogue
  * (exact-logit argmax per row, accepted-prefix length per request), the same GEMM
  * for the FP8 weights of FP8 targets (E4M3 codes with 128 x 128 block scales), and the
- * attention side of the decode step (paged cache, block tables, attention of the new rows).
+ * attention side of the decode step (paged cache, block tables, attention of the new rows,
+ * several continuations of one prompt).
  *
  * Sources (pages cited by title and section):
  *  - "StargazerX0/SpecPilot" (hotrepo.ai), "What it is": W12 is a 12-bit weight
@@ -543,6 +544,77 @@ w12_status w12_attn_paged(const uint16_t* q, uint64_t q_stride, uint32_t m, uint
                           const int32_t* kv_len, const int32_t* req_off, uint32_t n_req,
                           float scale, uint16_t* out, uint64_t out_stride, void* ws,
                           size_t ws_bytes, void* stream);
+
+/* ---- Several continuations of one prompt: pages that requests share, the attention of requests
+ * with the same first tokens, and the choice of the beams that go on.
+ *
+ * Pages that requests share are counted: refs, W12_REFS_WORDS(n_pages) int32 words of device
+ * memory, begins with the number of table entries that hold each page (entries table[r][c] with c
+ * < held[r]); the words behind are the calls' own and zero at first.  Zeroed refs fit an empty
+ * pool.  The holders of a page hold it in the same column.  A pool with refs is changed by the
+ * calls of this section alone (w12_kv_plan knows nothing of other holders). */
+#define W12_REFS_WORDS(n_pages) (5ull * (n_pages) + 1024)
+
+/* Brings the block tables in line with the requests' lengths where requests continue others, and
+ * maps the new rows: request r (r < n_req <= max_req) becomes the first len[r] tokens of request
+ * parent[r] as it was before the call, and rows_r = req_off[r+1] - req_off[r] new rows.  parent[r]
+ * may be r itself (parent NULL: every request), any other row of the table below max_req, used by
+ * several, or -1 for none (len[r] = 0: a new request, or without rows one that is released).  So
+ * one call forks a prompt, reorders beams, trims rejected rows, admits and releases.
+ *
+ * It takes the parent's ceil(len[r] / page_size) pages, shared, and new pages for what the rows
+ * need beyond them.  A request with rows whose last taken page is not full will write into it:
+ * it keeps that page if after the call nobody else holds it (of several that will write into one
+ * page the lowest request keeps it if no other one holds it), else it gets a new page in its place,
+ * to be filled by w12_kv_copy before the rows are appended: copies[r] = {page, new page, len[r]
+ * modulo page_size, 0}; {page, page, 0, 0} where it keeps it, {-1, -1, 0, 0} where there is none.
+ * New pages come from the start of the ring as it was before the call, in request order, a
+ * copy before the pages behind it.  Pages that nobody holds any longer go to the ring's end, by column, in
+ * a column by the lowest request that held it, and serve from the next call on.
+ *
+ * The call is served whole or not at all: if the ring has too few pages, or req_off is not 0 <=
+ * req_off[0] <= ... <= m, or state is not a ring's (see w12_kv_plan), nothing changes, and kv_len,
+ * pos, slot are -1 and copies {-1, -1, 0, 0} throughout.  A single request is refused, and stays as
+ * it was, with len[r] < 0, len[r] + rows_r > max_pages * page_size, parent[r] no row of the table
+ * and not -1, more tokens than the parent holds pages for, or counts outside 0..max_pages in held.
+ * Written: kv_len [n_req] = len[r] + rows_r, pos [m] and slot [m] as w12_kv_plan has them, copies
+ * [n_req][4], table, held, ring, state, refs.  Table entries past a request's pages keep their values.
+ * Rows of the table from n_req on stay as they are.  No result depends on the order of threads.
+ * All arrays device int32; pos and slot may be NULL when m = 0.  Calls on one pool must be ordered.
+ * Errors: W12_ERR_NULL; W12_ERR_SHAPE, W12_ERR_RANGE as w12_kv_plan; W12_ERR_ALIGN (4 bytes, copies
+ * 16). */
+w12_status w12_kv_fork(const w12_pages* p, int32_t* refs, const int32_t* parent, const int32_t* len,
+                       const int32_t* req_off, uint32_t n_req, uint32_t m, int32_t* kv_len,
+                       int32_t* pos, int32_t* slot, int32_t* copies, void* stream);
+
+/* Copies pages in every layer's cache: for each entry {from, to, tokens, -} of copies (device int32
+ * [n_copies][4], 16-byte aligned) the first tokens places of page `from`, rounded up to a multiple
+ * of 16, to the same places of page `to`, K and V of all heads; other places stay as they are.  An
+ * entry with tokens < 1, from = to, or a page outside 0 .. n_pages - 1 does nothing; tokens past the
+ * page are the whole page.  No entry's `to` may be another entry's page.  layers: n_layers
+ * descriptors of one geometry and type (their scales are not read).  n_copies = 0 does nothing.
+ * Errors: W12_ERR_NULL; W12_ERR_SHAPE, W12_ERR_FORMAT, W12_ERR_ALIGN (as w12_attn_paged's cache; layers
+ * that differ: W12_ERR_SHAPE); W12_ERR_RANGE (n_layers outside 1..W12_MAX_LAYERS, n_copies >
+ * W12_MAX_COPIES). */
+#define W12_MAX_LAYERS 1024
+#define W12_MAX_COPIES (1u << 22)
+w12_status w12_kv_copy(const w12_kv* layers, uint32_t n_layers, const int32_t* copies,
+                       uint32_t n_copies, void* stream);
+
+/* Clears the pages first .. first + n_clear - 1 of the pool: the i-th of them that is held (by its
+ * count in refs) moves to the i-th page outside that nobody holds, both in ascending order, and
+ * every table entry that names it follows.  moves (device int32 [n_clear][4], 16-byte aligned): entry i
+ * is {page, new page, page_size, 0} for page first + i, {-1, -1, 0, 0} if nobody holds it; w12_kv_copy
+ * then moves the contents.  Afterwards the ring starts at 0 and holds the free pages outside the
+ * range, ascending, then the whole range: so with the range at the pool's end a ring without its
+ * last n_clear entries, and a count that is less by n_clear, is the ring of the smaller pool.
+ * moved (device int32 [1]): the number of pages that moved, -1 if there are too few outside: then
+ * nothing changes and no entry of moves names a page.  The ring is made anew from refs (entries
+ * past its count keep their values).  Calls on one pool must be ordered.
+ * Errors: W12_ERR_NULL; W12_ERR_SHAPE as w12_kv_plan; W12_ERR_RANGE (n_clear < 1, a range that
+ * leaves the pool); W12_ERR_ALIGN. */
+w12_status w12_kv_compact(const w12_pages* p, int32_t* refs, uint32_t first, uint32_t n_clear,
+                          int32_t* moves, int32_t* moved, void* stream);
 
 /* Measurement helper, not part of the W12 method: streams `bytes` (a multiple of 16,
  * below 2^32) of device memory at `buf` (16-byte aligned) with the nontemporal 16-byte

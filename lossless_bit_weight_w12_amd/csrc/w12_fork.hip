@@ -1,0 +1,616 @@
+// Pages that requests share: block tables brought in line where a request continues another
+// one (w12_kv_fork), the copies and moves of pages in the caches (w12_kv_copy), and a range of
+// the pool cleared of pages (w12_kv_compact).
+//
+// The counts of holders lie in refs [n_pages]; behind them the calls' own words: per page the
+// change of its count and the mark of a call under way (both zero between calls), per page a
+// rank and a target of w12_kv_compact, and the workgroups' counts.
+#include "w12.h"
+#include "w12_fork.h"
+#include "w12_plan.h"
+
+namespace w12 {
+
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kForkWG = 256;        // workgroups of a launch, at most (one count each)
+constexpr uint32_t kEntries = 8192;      // table entries of a workgroup in LDS at a time
+constexpr uint32_t kWriter = 0x10000u;   // a mark of a request that writes
+
+__device__ __forceinline__ int32_t load_dev(const int32_t* p) {   // past this XCD's L2, as the atomics are
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void store_dev(int32_t* p, int32_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void add_dev(int32_t* p, int32_t v) {
+  __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Sum over the workgroup's threads, the same in all of them.
+template <int T>
+__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t* s_w) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = v;
+  __syncthreads();
+  uint32_t all = 0;
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) all += s_w[w];
+  return all;
+}
+
+// Number of set flags in threads before this one, and in all of them.
+template <int T>
+__device__ __forceinline__ uint32_t block_rank(bool flag, uint32_t* s_w, uint32_t& all) {
+  const uint64_t b = __ballot(flag);
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __syncthreads();
+  if (lane == 0) s_w[wave] = (uint32_t)__popcll(b);
+  __syncthreads();
+  uint32_t before = (uint32_t)__popcll(b & ((1ull << lane) - 1ull));
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) {
+    if (w < (int)wave) before += s_w[w];
+    all += s_w[w];
+  }
+  return before;
+}
+
+// One request of w12_kv_fork: what it shall hold.
+struct Fork {
+  int32_t src;           // row that it continues, -1: none
+  uint32_t held, keep;   // pages of its row now, pages of src that it takes
+  uint32_t want;         // pages afterwards
+  int32_t len;
+  uint32_t off, rows;
+  bool writes;           // it adds rows to the last page it takes
+  bool served;
+};
+
+__device__ __forceinline__ Fork fork_req(const ForkArgs& a, uint32_t r, bool& bad) {
+  Fork f;
+  const int32_t lo = a.req_off[r], hi = a.req_off[r + 1], len = a.len[r], own = a.held[r];
+  const int32_t src = a.parent ? a.parent[r] : (int32_t)r;
+  bad |= lo < 0 || hi < lo || hi > (int32_t)a.m;
+  const bool whole = own >= 0 && (uint32_t)own <= a.max_pages;
+  const bool known = src >= 0 && (uint32_t)src < a.max_req;
+  const int32_t have = known ? a.held[src] : 0;
+  const uint32_t page = 1u << a.page_shift, rows = (uint32_t)(hi - lo);
+  f.off = (uint32_t)lo;
+  f.rows = rows;
+  f.len = len;
+  f.held = whole ? (uint32_t)own : 0u;
+  f.served = whole && len >= 0 && (known ? have >= 0 && (uint32_t)have <= a.max_pages : src == -1) &&
+             (int64_t)len + rows <= (int64_t)a.max_pages << a.page_shift &&
+             ((uint64_t)(uint32_t)len + page - 1) >> a.page_shift <= (uint64_t)(uint32_t)have;
+  if (f.served) {
+    f.src = src;
+    f.keep = ((uint32_t)len + page - 1) >> a.page_shift;
+    f.want = (uint32_t)(((uint64_t)len + rows + page - 1) >> a.page_shift);
+    f.writes = ((uint32_t)len & (page - 1)) != 0 && rows > 0;
+  } else {   // it keeps what it holds
+    f.src = (int32_t)r;
+    f.keep = f.want = f.held;
+    f.writes = false;
+  }
+  return f;
+}
+
+// The requests in LDS.  flags: bit 31 of keep: writes.
+template <int N>
+struct ForkTable {
+  int32_t src[N];
+  uint32_t held[N], keep[N];
+};
+constexpr uint32_t kWrites = 1u << 31;
+
+// What request r's place in column c holds (x) and will hold of src's pages (y), -1: nothing.
+template <int N>
+__device__ __forceinline__ void entry(const ForkArgs& a, const ForkTable<N>& q, const int32_t* s_old, uint32_t n,
+                                      uint32_t r, uint32_t j, uint32_t c, int32_t& x, int32_t& y, bool& tail) {
+  const uint32_t keep = q.keep[r] & ~kWrites;
+  x = s_old[j * n + r];
+  y = -1;
+  tail = false;
+  if (c < keep) {
+    const int32_t src = q.src[r];
+    y = (uint32_t)src < n ? s_old[j * n + (uint32_t)src] : a.table[(uint64_t)(uint32_t)src * a.max_pages + c];
+    tail = c + 1 == keep && (q.keep[r] & kWrites);
+  }
+}
+
+// Both kernels of w12_kv_fork deal the columns that somebody holds to the workgroups: the holders
+// of a page hold it in the same column (a request that continues another one has its first
+// tokens in the same places), so one workgroup sees everything about a page.  A column's old
+// entries are in LDS, so that the rows can change places.  The first kernel counts: the change of
+// each page's holders, the requests that write into their last page (the lowest may keep it if
+// nobody else holds it), and the pages nobody holds any longer; the second knows from the sums
+// where the pages it gives back go and whether there are enough, and writes.  Entries that stay are
+// passed over before any atomic, so a prompt's shared pages cost nothing.
+//
+// Bound by latency (dependent reads behind two launches).
+template <int T, int N>
+__global__ __launch_bounds__(T) void k_fork_look(ForkArgs a) {
+  __shared__ ForkTable<N> q;
+  __shared__ int32_t s_old[kEntries];
+  __shared__ uint32_t s_w[T / 64], s_cols, s_bad;
+  const uint32_t t = threadIdx.x, n = a.n_req, b = blockIdx.x;
+  int32_t* const delta = a.refs + a.n_pages;
+  int32_t* const mark = delta + a.n_pages;
+  uint32_t* const counts = reinterpret_cast<uint32_t*>(a.refs) + 5ull * a.n_pages;
+  if (t == 0) s_cols = s_bad = 0;
+  __syncthreads();
+  const int32_t head = a.state[0], count = a.state[1];
+  bool bad = head < 0 || (uint32_t)head >= a.n_pages || count < 0 || (uint32_t)count > a.n_pages || a.state[2] != 0;
+  uint32_t cols = 0;
+  for (uint32_t r = t; r < n; r += T) {
+    const Fork f = fork_req(a, r, bad);
+    q.src[r] = f.src;
+    q.held[r] = f.held;
+    q.keep[r] = f.keep | (f.writes ? kWrites : 0u);
+    cols = max(cols, max(f.held, f.keep));
+    if (b == 0 && !f.writes) {
+      int32_t* const e = a.copies + 4ull * r;
+      e[0] = e[1] = -1;
+      e[2] = e[3] = 0;
+    }
+  }
+  atomicMax(&s_cols, cols);
+  if (bad) s_bad = 1;
+  __syncthreads();
+  if (b == 0 && t == 0) counts[kForkWG] = s_bad;
+  if (s_bad) return;
+  cols = s_cols;
+  const uint32_t per = (cols + gridDim.x - 1) / gridDim.x, c_end = min(cols, (b + 1) * per);
+  const uint32_t width = max(1u, min(per, kEntries / n));
+  uint32_t freed = 0;
+  auto valid = [&](int32_t p) { return (uint32_t)p < a.n_pages; };
+  for (uint32_t c0 = b * per; c0 < c_end; c0 += width) {
+    const uint32_t w = min(width, c_end - c0), all = w * n;
+    __syncthreads();
+    for (uint32_t e = t; e < all; e += T) {
+      const uint32_t r = e / w, j = e - r * w;
+      s_old[j * n + r] = c0 + j < q.held[r] ? a.table[(uint64_t)r * a.max_pages + c0 + j] : -1;
+    }
+    __syncthreads();
+    bool any = false;
+    for (uint32_t e = t; e < all; e += T) {
+      const uint32_t j = e / n, r = e - j * n;
+      int32_t x, y;
+      bool tail;
+      entry(a, q, s_old, n, r, j, c0 + j, x, y, tail);
+      if (x == y && !tail) continue;
+      any = true;
+      if (valid(x)) {
+        add_dev(delta + x, -1);
+        __hip_atomic_fetch_max(mark + x, (int32_t)(n - r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      if (valid(y)) {
+        if (tail) __hip_atomic_fetch_max(mark + y, (int32_t)(kWriter + n - r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        else add_dev(delta + y, 1);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (!__syncthreads_or(any)) continue;
+    for (uint32_t e = t; e < all; e += T) {
+      const uint32_t j = e / n, r = e - j * n;
+      int32_t x, y;
+      bool tail;
+      entry(a, q, s_old, n, r, j, c0 + j, x, y, tail);
+      if (x == y && !tail) continue;
+      if (valid(x)) freed += load_dev(mark + x) == (int32_t)(n - r) && a.refs[x] + load_dev(delta + x) == 0;
+      if (tail) {   // the lowest of those that write keeps a page that nobody else holds
+        const bool stays = !valid(y) || (load_dev(mark + y) == (int32_t)(kWriter + n - r) && a.refs[y] + load_dev(delta + y) == 0);
+        int32_t* const c = a.copies + 4ull * r;
+        c[0] = y;
+        c[1] = y;
+        c[2] = stays ? 0 : a.len[r] & ((1 << a.page_shift) - 1);
+        c[3] = 0;
+      }
+    }
+  }
+  freed = block_sum<T>(freed, s_w);
+  if (t == 0) counts[b] = freed;
+}
+
+template <int T, int N>
+__global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
+  constexpr uint32_t kPer = N / T;
+  __shared__ ForkTable<N> q;
+  __shared__ uint32_t s_need[N + 1], s_off[N + 1];
+  __shared__ int32_t s_len[N];   // -1: not served
+  __shared__ int32_t s_old[kEntries];
+  __shared__ uint32_t s_w[T / 64], s_cols, s_last, s_sum[2];
+  const uint32_t t = threadIdx.x, n = a.n_req, b = blockIdx.x, lane = t & 63, wave = t >> 6;
+  const uint32_t first = b * T + t, step = gridDim.x * T;   // of the flat lists
+  int32_t* const delta = a.refs + a.n_pages;
+  int32_t* const mark = delta + a.n_pages;
+  const uint32_t* const counts = reinterpret_cast<const uint32_t*>(a.refs) + 5ull * a.n_pages;
+  const uint32_t shift = a.page_shift, in_page = (1u << shift) - 1u;
+  if (t == 0) s_cols = s_sum[0] = s_sum[1] = 0;
+  __syncthreads();
+  const uint32_t head = (uint32_t)a.state[0], count = (uint32_t)a.state[1];
+  const bool none = counts[kForkWG] != 0;   // the first kernel has left everything as it was
+  bool bad = false;   // (known)
+  uint32_t cols = 0, need[kPer], sum = 0;
+  const uint32_t per_t = (n + T - 1) / T;
+#pragma unroll
+  for (uint32_t i = 0; i < kPer; ++i) {
+    const uint32_t r = t * per_t + i;
+    need[i] = 0;
+    if (i < per_t && r < n) {
+      const Fork f = fork_req(a, r, bad);
+      q.src[r] = f.src;
+      q.held[r] = f.held;
+      q.keep[r] = f.keep | (f.writes ? kWrites : 0u);
+      need[i] = f.want - f.keep + (f.writes && a.copies[4ull * r + 2] > 0 ? 1u : 0u);
+      s_len[r] = f.served ? f.len : -1;
+      s_off[r] = f.off;
+      if (r + 1 == n) s_off[n] = f.off + f.rows;
+      cols = max(cols, max(f.held, f.keep));
+    }
+    sum = sat_add(sum, need[i]);
+  }
+  atomicMax(&s_cols, cols);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t u = __shfl_up(sum, o);
+    if (lane >= (uint32_t)o) sum = sat_add(sum, u);
+  }
+  if (lane == 63) s_w[wave] = sum;
+  if (t < gridDim.x && T >= kForkWG) {   // pages given back, by the workgroups before and by all
+    const uint32_t v = counts[t];
+    atomicAdd(&s_sum[0], t < b ? v : 0u);
+    atomicAdd(&s_sum[1], v);
+  }
+  __syncthreads();
+  uint32_t total = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < T / 64; ++w) {
+    if (w < wave) sum = sat_add(sum, s_w[w]);
+    total = sat_add(total, s_w[w]);
+  }
+#pragma unroll
+  for (int i = (int)kPer - 1; i >= 0; --i) {
+    const uint32_t r = t * per_t + i;
+    if (i < (int)per_t && r < n) {
+      s_need[r + 1] = sum;
+      sum -= need[i];
+    }
+  }
+  if (t == 0) s_need[0] = 0u;
+  const uint32_t freed = s_sum[1];
+  const bool enough = !none && total <= count && (uint64_t)count + freed <= a.n_pages;
+  cols = s_cols;
+  __syncthreads();
+
+  auto ring_at = [&](uint32_t j) {   // j <= n_pages
+    const uint32_t i = head + j;
+    return i >= a.n_pages ? i - a.n_pages : i;
+  };
+  auto valid = [&](int32_t p) { return (uint32_t)p < a.n_pages; };
+  auto copied = [&](uint32_t r) {   // a page of its own for the last one it takes
+    return (q.keep[r] & kWrites) && a.copies[4ull * r + 2] > 0;
+  };
+  // the page that request r gets for its column c >= keep, or (c = keep - 1) for the copy
+  auto fresh = [&](uint32_t r, uint32_t c, bool copy) {
+    const uint32_t at = s_need[r] + (c + (copy ? 1u : 0u) - (q.keep[r] & ~kWrites));
+    const int32_t p = at < s_need[r + 1] ? a.ring[ring_at(at)] : -1;
+    return valid(p) ? p : -1;
+  };
+
+  // ---- the columns
+  const uint32_t per = (cols + gridDim.x - 1) / gridDim.x, c_end = none ? 0u : min(cols, (b + 1) * per);
+  const uint32_t width = max(1u, min(per, kEntries / n));
+  uint32_t back = s_sum[0];   // where this workgroup's pages go in the ring
+  for (uint32_t c0 = b * per; c0 < c_end; c0 += width) {
+    const uint32_t w = min(width, c_end - c0), all = w * n;
+    __syncthreads();
+    for (uint32_t e = t; e < all; e += T) {
+      const uint32_t r = e / w, j = e - r * w;
+      s_old[j * n + r] = c0 + j < q.held[r] ? a.table[(uint64_t)r * a.max_pages + c0 + j] : -1;
+    }
+    __syncthreads();
+    bool any = false;
+    for (uint32_t e0 = 0; e0 < all; e0 += T) {
+      const uint32_t e = e0 + t;
+      int32_t x = -1, y = -1;
+      bool tail = false;
+      uint32_t r = 0;
+      if (e < all) {
+        const uint32_t j = e / n;
+        r = e - j * n;
+        entry(a, q, s_old, n, r, j, c0 + j, x, y, tail);
+      }
+      const bool moves = e < all && (x != y || tail);
+      const bool gone = moves && valid(x) && load_dev(mark + x) == (int32_t)(n - r) && a.refs[x] + load_dev(delta + x) == 0;
+      any |= moves;
+      if (__syncthreads_or(gone)) {
+        uint32_t some;
+        const uint32_t rank = block_rank<T>(gone, s_w, some);
+        if (gone && enough) a.ring[ring_at(count + back + rank)] = x;
+        back += some;
+      }
+    }
+    any = __syncthreads_or(any);
+    // the counts, and the call's own words back to zero
+    if (any)
+      for (uint32_t e = t; e < all; e += T) {
+        const uint32_t j = e / n, r = e - j * n;
+        int32_t x, y;
+        bool tail;
+        entry(a, q, s_old, n, r, j, c0 + j, x, y, tail);
+        if (x == y && !tail) continue;
+        const bool to = valid(y) && !(tail && copied(r));
+        if (enough) {
+          if (valid(x)) add_dev(a.refs + x, -1);
+          if (to) add_dev(a.refs + y, 1);
+        }
+        if (valid(x)) {
+          store_dev(delta + x, 0);
+          store_dev(mark + x, 0);
+        }
+        if (valid(y)) {
+          store_dev(delta + y, 0);
+          store_dev(mark + y, 0);
+        }
+      }
+    if (enough)
+      for (uint32_t e = t; e < all; e += T) {
+        const uint32_t r = e / w, j = e - r * w, c = c0 + j;
+        int32_t x, y;
+        bool tail;
+        entry(a, q, s_old, n, r, j, c, x, y, tail);
+        const uint32_t keep = q.keep[r] & ~kWrites, news = s_need[r + 1] - s_need[r];
+        if (tail && copied(r)) {
+          y = fresh(r, c, true);
+          if (valid(y)) store_dev(a.refs + y, 1);
+          a.copies[4ull * r + 1] = y;
+        } else if (c >= keep) {
+          const bool more = c - keep < news - (copied(r) ? 1u : 0u);
+          y = more ? fresh(r, c, copied(r)) : x;   // (entries past the pages keep their values)
+          if (more && valid(y)) store_dev(a.refs + y, 1);
+          if (!more) continue;
+        }
+        if (y != x) a.table[(uint64_t)r * a.max_pages + c] = y;
+      }
+  }
+  if (enough)   // pages in columns that nobody held
+    for (uint32_t e = first; e < total; e += step) {
+      const uint32_t r = segment(s_need, n, e), own = copied(r) ? 1u : 0u, i = e - s_need[r];
+      const uint32_t c = (q.keep[r] & ~kWrites) + i - own;
+      if (i < own || c < cols) continue;
+      const int32_t p = fresh(r, c, own != 0);
+      if (valid(p)) store_dev(a.refs + p, 1);
+      a.table[(uint64_t)r * a.max_pages + c] = p;
+    }
+  // ---- the rows, and the requests
+  for (uint32_t i = first; i < a.m; i += step) {
+    int32_t p = -1, s = -1;
+    if (enough && i >= s_off[0] && i < s_off[n]) {
+      const uint32_t r = segment(s_off, n, i);
+      if (s_len[r] >= 0) {
+        p = s_len[r] + (int32_t)(i - s_off[r]);
+        const uint32_t c = (uint32_t)p >> shift;
+        const bool copy = copied(r);
+        const int32_t page = c < (q.keep[r] & ~kWrites) && !copy ? a.copies[4ull * r] : fresh(r, c, copy);
+        if (valid(page)) s = (page << shift) | (p & (int32_t)in_page);
+      }
+    }
+    a.pos[i] = p;
+    a.slot[i] = s;
+  }
+  for (uint32_t r = first; r < n; r += step)
+    a.kv_len[r] = enough && s_len[r] >= 0 ? s_len[r] + (int32_t)(s_off[r + 1] - s_off[r]) : -1;
+  // what others read last: every workgroup is through with the old values
+  if (none) {
+    for (uint32_t r = first; r < n; r += step) *reinterpret_cast<i32x4*>(a.copies + 4ull * r) = i32x4{-1, -1, 0, 0};
+    return;
+  }
+  __syncthreads();
+  if (gridDim.x > 1) {
+    if (t == 0) {
+      uint32_t* const ticket = reinterpret_cast<uint32_t*>(a.state + 2);
+      s_last = __hip_atomic_fetch_add(ticket, kTicket, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               (gridDim.x - 1) * kTicket;
+      if (s_last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!s_last) return;
+  }
+  if (!enough) {   // nothing has changed
+    for (uint32_t r = t; r < n; r += T) *reinterpret_cast<i32x4*>(a.copies + 4ull * r) = i32x4{-1, -1, 0, 0};
+    return;
+  }
+  for (uint32_t r = t; r < n; r += T)
+    if (s_len[r] >= 0) a.held[r] = (int32_t)((q.keep[r] & ~kWrites) + s_need[r + 1] - s_need[r] - (copied(r) ? 1u : 0u));
+  if (t == 0) {
+    a.state[0] = (int32_t)ring_at(total);
+    a.state[1] = (int32_t)(count - total + freed);
+  }
+}
+
+// ------------------------------------------------------------------------------- the copies
+// A workgroup takes kCopyBytes of one page of K or V of one layer, 16 bytes a thread at a time
+// and all reads before the first write.  Bound by HBM.
+constexpr uint32_t kCopyT = 256, kCopyBytes = 32768, kCopyV = kCopyBytes / 16 / kCopyT;
+
+__global__ __launch_bounds__(kCopyT) void k_kv_copy(CopyArgs a) {
+  const int32_t* const c = a.copies + 4ull * blockIdx.x;
+  const int32_t src = c[0], dst = c[1], tokens = c[2];
+  if (tokens <= 0 || src == dst || (uint32_t)src >= a.n_pages || (uint32_t)dst >= a.n_pages) return;
+  const bool of_v = blockIdx.z & 1;
+  const uint32_t part = blockIdx.z >> 1, page = 1u << a.page_shift;
+  const uint32_t here = min(((uint32_t)tokens + 15u) & ~15u, page);
+  uint8_t* const base = (uint8_t*)(of_v ? a.v[blockIdx.y] : a.k[blockIdx.y]);
+  const u32x4* const from = reinterpret_cast<const u32x4*>(base + (uint64_t)src * a.page_bytes);
+  u32x4* const to = reinterpret_cast<u32x4*>(base + (uint64_t)dst * a.page_bytes);
+  auto e_of = [&](uint32_t i) { return part * (kCopyBytes / 16) + i * kCopyT + threadIdx.x; };
+  u32x4 x[kCopyV];
+  bool on[kCopyV];
+#pragma unroll
+  for (uint32_t i = 0; i < kCopyV; ++i) {
+    const uint32_t e = e_of(i), place = of_v ? e << a.vec_shift : e >> a.key_shift;
+    on[i] = e < a.page_bytes / 16 && (place & (page - 1u)) < here;
+    if (on[i]) x[i] = from[e];
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < kCopyV; ++i)
+    if (on[i]) to[e_of(i)] = x[i];
+}
+
+// ---------------------------------------------------------------------- clearing a range
+// Three launches: the workgroups' counts; ranks of the pages that move and of the free pages
+// outside, the new ring; then the moves, the counts and the tables' names.  Bound by latency.
+struct Clear {   // of all pages, and of those before the workgroup's
+  uint32_t out, in, out_before, in_before;
+};
+
+template <int T>
+__device__ __forceinline__ Clear clear_counts(const ClearArgs& a, uint32_t* s_sum) {
+  const uint32_t* const counts = reinterpret_cast<const uint32_t*>(a.refs) + 5ull * a.n_pages;
+  const uint32_t t = threadIdx.x;
+  if (t < 4) s_sum[t] = 0;
+  __syncthreads();
+  if (t < a.blocks) {
+    const uint32_t o = counts[2 * t], i = counts[2 * t + 1];
+    atomicAdd(&s_sum[0], o);
+    atomicAdd(&s_sum[1], i);
+    if (t < blockIdx.x) {
+      atomicAdd(&s_sum[2], o);
+      atomicAdd(&s_sum[3], i);
+    }
+  }
+  __syncthreads();
+  return Clear{s_sum[0], s_sum[1], s_sum[2], s_sum[3]};
+}
+
+__global__ __launch_bounds__(256) void k_clear_count(ClearArgs a) {
+  __shared__ uint32_t s_w[4];
+  uint32_t* const counts = reinterpret_cast<uint32_t*>(a.refs) + 5ull * a.n_pages;
+  const uint32_t x0 = blockIdx.x * a.per, x1 = min(a.n_pages, x0 + a.per);
+  uint32_t out = 0, in = 0;
+  for (uint32_t x = x0 + threadIdx.x; x < x1; x += 256) {
+    const bool inside = x - a.first < a.n_clear, live = a.refs[x] > 0;
+    out += !inside && !live;
+    in += inside && live;
+  }
+  out = block_sum<256>(out, s_w);
+  in = block_sum<256>(in, s_w);
+  if (threadIdx.x == 0) {
+    counts[2 * blockIdx.x] = out;
+    counts[2 * blockIdx.x + 1] = in;
+  }
+}
+
+__global__ __launch_bounds__(256) void k_clear_rank(ClearArgs a) {
+  __shared__ uint32_t s_w[4], s_sum[4];
+  const Clear n = clear_counts<256>(a, s_sum);
+  if (n.in > n.out) return;
+  int32_t* const rank = a.refs + 3ull * a.n_pages;
+  int32_t* const target = rank + a.n_pages;
+  const uint32_t x0 = blockIdx.x * a.per, x1 = min(a.n_pages, x0 + a.per);
+  uint32_t out = n.out_before, in = n.in_before;
+  for (uint32_t x = x0; x < x1; x += 256) {
+    const uint32_t p = x + threadIdx.x;
+    const bool inside = p - a.first < a.n_clear, live = p < x1 && a.refs[p] > 0;
+    uint32_t some, k = block_rank<256>(p < x1 && !inside && !live, s_w, some);
+    if (p < x1 && !inside && !live) {
+      if (out + k < n.in) target[out + k] = (int32_t)p;
+      else a.ring[out + k - n.in] = (int32_t)p;
+    }
+    out += some;
+    k = block_rank<256>(inside && live, s_w, some);
+    if (p < x1 && inside) {
+      rank[p] = live ? (int32_t)(in + k) : -1;
+      a.ring[n.out - n.in + (p - a.first)] = (int32_t)p;
+    }
+    in += some;
+  }
+}
+
+__global__ __launch_bounds__(256) void k_clear_move(ClearArgs a) {
+  __shared__ uint32_t s_sum[4];
+  const Clear n = clear_counts<256>(a, s_sum);
+  const bool enough = n.in <= n.out;
+  const int32_t* const rank = a.refs + 3ull * a.n_pages;
+  const int32_t* const target = rank + a.n_pages;
+  const uint32_t t = threadIdx.x;
+  auto moved = [&](uint32_t p) {   // where page p of the range went
+    const int32_t k = rank[p];
+    return (uint32_t)k < n.in ? target[k] : -1;
+  };
+  const uint64_t wg = (uint64_t)blockIdx.y * gridDim.x + blockIdx.x, all = (uint64_t)gridDim.x * gridDim.y;
+  for (uint64_t i = wg * 256 + t; i < a.n_clear; i += all * 256) {
+    const uint32_t p = a.first + (uint32_t)i;
+    const int32_t to = enough ? moved(p) : -1;
+    if (to >= 0) {
+      a.refs[to] = a.refs[p];
+      a.refs[p] = 0;
+    }
+    *reinterpret_cast<i32x4*>(a.moves + 4 * i) =
+        to >= 0 ? i32x4{(int32_t)p, to, (int32_t)a.page_size, 0} : i32x4{-1, -1, 0, 0};
+  }
+  if (enough)
+    for (uint32_t r = blockIdx.x; r < a.max_req; r += gridDim.x) {
+      const int32_t held = a.held[r];
+      if (held < 0 || (uint32_t)held > a.max_pages) continue;
+      int32_t* const row = a.table + (uint64_t)r * a.max_pages;
+      for (uint32_t c = blockIdx.y * 256 + t; c < (uint32_t)held; c += gridDim.y * 256) {
+        const int32_t p = row[c];
+        if ((uint32_t)p >= a.n_pages || (uint32_t)p - a.first >= a.n_clear) continue;
+        const int32_t to = moved((uint32_t)p);
+        if (to >= 0) row[c] = to;
+      }
+    }
+  if (wg == 0 && t == 0) {
+    *a.moved = enough ? (int32_t)n.in : -1;
+    if (enough) {
+      a.state[0] = 0;
+      a.state[1] = (int32_t)(n.out - n.in + a.n_clear);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
+  // a workgroup for every 1024 places of the tables, or rows
+  const uint64_t work = (uint64_t)a.n_req * a.max_pages;
+  uint64_t wg = ((work > a.m ? work : a.m) + 1023) / 1024;
+  wg = wg < 1 ? 1 : (wg > kForkWG ? kForkWG : wg);
+  if (a.n_req <= 256) {
+    hipLaunchKernelGGL((k_fork_look<256, 256>), dim3((uint32_t)wg), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_fork_apply<256, 256>), dim3((uint32_t)wg), dim3(256), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_fork_look<1024, 4096>), dim3((uint32_t)wg), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((k_fork_apply<1024, 4096>), dim3((uint32_t)wg), dim3(1024), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_copy(const CopyArgs& a, uint32_t n_copies, uint32_t n_layers, hipStream_t s) {
+  const uint32_t parts = (a.page_bytes + kCopyBytes - 1) / kCopyBytes;
+  hipLaunchKernelGGL(k_kv_copy, dim3(n_copies, n_layers, 2 * parts), dim3(kCopyT), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_compact(const ClearArgs& given, hipStream_t s) {
+  ClearArgs a = given;
+  a.per = (a.n_pages + 255) / 256;
+  a.per = a.per < 256 ? 256 : a.per;
+  a.blocks = (a.n_pages + a.per - 1) / a.per;
+  hipLaunchKernelGGL(k_clear_count, dim3(a.blocks), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_clear_rank, dim3(a.blocks), dim3(256), 0, s, a);
+  const uint32_t x = a.max_req < 256 ? a.max_req : 256, most = (a.max_pages + 255) / 256, y = 1024 / x;
+  hipLaunchKernelGGL(k_clear_move, dim3(x, y < most ? y : most), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace w12

@@ -1,0 +1,121 @@
+// C-ABI host layer of the pages that requests share: argument validation (before any HIP call)
+// and launch.
+#include "w12.h"
+#include "w12_check.h"
+#include "w12_fork.h"
+
+using namespace w12;
+
+namespace {
+
+w12_status check_pages(const w12_pages* p) {
+  if (!p->table || !p->held || !p->ring || !p->state) return W12_ERR_NULL;
+  if (!page_size_ok(p->page_size) || !slots_ok(p->n_pages, p->page_size) ||
+      !length_ok(p->max_pages, p->page_size) || p->max_req < 1 || p->max_req > W12_MAX_REQ)
+    return W12_ERR_SHAPE;
+  return W12_OK;
+}
+
+bool aligned4(std::initializer_list<const void*> all) {
+  for (const void* a : all)
+    if (!aligned(a, 4)) return false;
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+w12_status w12_kv_fork(const w12_pages* p, int32_t* refs, const int32_t* parent, const int32_t* len,
+                       const int32_t* req_off, uint32_t n_req, uint32_t m, int32_t* kv_len,
+                       int32_t* pos, int32_t* slot, int32_t* copies, void* stream) {
+  if (!p || !refs || !len || !req_off || !kv_len || !copies) return W12_ERR_NULL;
+  if (m > 0 && (!pos || !slot)) return W12_ERR_NULL;
+  const w12_status st = check_pages(p);
+  if (st != W12_OK) return st;
+  if (n_req < 1 || n_req > p->max_req || m > W12_MAX_KV_ROWS) return W12_ERR_RANGE;
+  if (!aligned4({p->table, p->held, p->ring, p->state, refs, parent, len, req_off, kv_len, pos, slot}) ||
+      !aligned(copies, 16))
+    return W12_ERR_ALIGN;
+  ForkArgs a{};
+  a.n_pages = p->n_pages;
+  a.page_shift = log2u(p->page_size);
+  a.max_pages = p->max_pages;
+  a.max_req = p->max_req;
+  a.table = p->table;
+  a.held = p->held;
+  a.ring = p->ring;
+  a.state = p->state;
+  a.refs = refs;
+  a.parent = parent;
+  a.len = len;
+  a.req_off = req_off;
+  a.n_req = n_req;
+  a.m = m;
+  a.kv_len = kv_len;
+  a.pos = pos;
+  a.slot = slot;
+  a.copies = copies;
+  return hip_status(launch_kv_fork(a, (hipStream_t)stream));
+}
+
+w12_status w12_kv_copy(const w12_kv* layers, uint32_t n_layers, const int32_t* copies,
+                       uint32_t n_copies, void* stream) {
+  if (!layers || (n_copies > 0 && !copies)) return W12_ERR_NULL;
+  if (n_layers < 1 || n_layers > W12_MAX_LAYERS || n_copies > W12_MAX_COPIES) return W12_ERR_RANGE;
+  for (uint32_t i = 0; i < n_layers; ++i) {
+    const w12_status st = check_kv(layers + i, layers[i].n_kv_heads);
+    if (st != W12_OK) return st;
+    const w12_kv &a = layers[0], &b = layers[i];
+    if (b.n_pages != a.n_pages || b.page_size != a.page_size || b.n_kv_heads != a.n_kv_heads ||
+        b.head_dim != a.head_dim || b.dtype != a.dtype)
+      return W12_ERR_SHAPE;
+  }
+  if (!aligned(copies, 16)) return W12_ERR_ALIGN;
+  if (n_copies == 0) return W12_OK;
+  const uint32_t es = layers[0].dtype == W12_KV_BF16 ? 2 : 1;
+  CopyArgs a{};
+  a.n_pages = layers[0].n_pages;
+  a.page_shift = log2u(layers[0].page_size);
+  a.page_bytes = layers[0].n_kv_heads * layers[0].page_size * layers[0].head_dim * es;
+  a.key_shift = log2u(layers[0].head_dim * es / 16);
+  a.vec_shift = log2u(16 / es);
+  a.copies = copies;
+  for (uint32_t i = 0; i < n_layers; i += kCopyLayers) {
+    const uint32_t here = n_layers - i < kCopyLayers ? n_layers - i : kCopyLayers;
+    for (uint32_t j = 0; j < here; ++j) {
+      a.k[j] = layers[i + j].k;
+      a.v[j] = layers[i + j].v;
+    }
+    const w12_status st = hip_status(launch_kv_copy(a, n_copies, here, (hipStream_t)stream));
+    if (st != W12_OK) return st;
+  }
+  return W12_OK;
+}
+
+w12_status w12_kv_compact(const w12_pages* p, int32_t* refs, uint32_t first, uint32_t n_clear,
+                          int32_t* moves, int32_t* moved, void* stream) {
+  if (!p || !refs || !moves || !moved) return W12_ERR_NULL;
+  const w12_status st = check_pages(p);
+  if (st != W12_OK) return st;
+  if (n_clear < 1 || n_clear > p->n_pages || first > p->n_pages - n_clear) return W12_ERR_RANGE;
+  if (!aligned4({p->table, p->held, p->ring, p->state, refs, moved}) || !aligned(moves, 16))
+    return W12_ERR_ALIGN;
+  ClearArgs a{};
+  a.n_pages = p->n_pages;
+  a.page_size = p->page_size;
+  a.max_pages = p->max_pages;
+  a.max_req = p->max_req;
+  a.first = first;
+  a.n_clear = n_clear;
+  a.table = p->table;
+  a.held = p->held;
+  a.ring = p->ring;
+  a.state = p->state;
+  a.refs = refs;
+  a.moves = moves;
+  a.moved = moved;
+  return hip_status(launch_kv_compact(a, (hipStream_t)stream));
+}
+
+}  // extern "C"

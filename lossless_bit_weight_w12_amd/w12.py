@@ -22,6 +22,8 @@ KV_BF16, KV_E4M3 = 0, 1
 MAX_REQ = 4096                 # W12_MAX_REQ: requests of one cache call
 MAX_KV_ROWS = 1 << 20          # W12_MAX_KV_ROWS: rows of one cache call
 MAX_HEADS = 1024               # W12_MAX_HEADS
+MAX_LAYERS = 1024              # W12_MAX_LAYERS: caches of one kv_copy
+MAX_COPIES = 1 << 22           # W12_MAX_COPIES
 ATTN_WS_BYTES = 36 << 20       # W12_ATTN_WS_BYTES
 STATUS = {0: "W12_OK", -1: "W12_ERR_NULL", -2: "W12_ERR_SHAPE", -3: "W12_ERR_RANGE",
           -4: "W12_ERR_FORMAT", -5: "W12_ERR_WORKSPACE", -6: "W12_ERR_HIP", -7: "W12_ERR_ALIGN"}
@@ -34,7 +36,7 @@ EXPORTS = ("w12_tiles_bytes", "w12_workspace_bytes", "w12_workspace_init", "w12_
            "w12_screen_bytes", "w12_screen_encode", "w12_lmhead_verify2", "w12_lmhead_verify2_batched",
            "w12_screen_logits_f32", "w12_f8_tile", "w12_gemm_f8", "w12_gemm_f8_group",
            "w12_gemm_f8_rms", "w12_gemm_f8_group_rms", "w12_kv_plan", "w12_qk_rope",
-           "w12_attn_paged")
+           "w12_attn_paged", "w12_kv_fork", "w12_kv_copy", "w12_kv_compact")
 NOALLOC_SCRATCH_BYTES = 32 << 20   # W12_NOALLOC_SCRATCH_BYTES
 ENCODE_TOTAL_OFFSET = 2112   # W12_ENCODE_TOTAL_OFFSET: true escape count in an encode workspace
 
@@ -170,6 +172,14 @@ def lib():
         L.w12_attn_paged.argtypes = [c_void_p, c_uint64, c_uint32, c_uint32, ctypes.POINTER(W12Kv),
                                      c_void_p, c_uint32, c_void_p, c_void_p, c_uint32, c_float,
                                      c_void_p, c_uint64, c_void_p, c_size_t, c_void_p]
+        L.w12_kv_fork.restype = c_int32
+        L.w12_kv_fork.argtypes = [ctypes.POINTER(W12Pages), c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_uint32, c_uint32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]
+        L.w12_kv_copy.restype = c_int32
+        L.w12_kv_copy.argtypes = [ctypes.POINTER(W12Kv), c_uint32, c_void_p, c_uint32, c_void_p]
+        L.w12_kv_compact.restype = c_int32
+        L.w12_kv_compact.argtypes = [ctypes.POINTER(W12Pages), c_void_p, c_uint32, c_uint32, c_void_p,
+                                     c_void_p, c_void_p]
         L.w12_status_str.restype = ctypes.c_char_p
         L.w12_status_str.argtypes = [c_int32]
         L.w12_version.restype = c_uint32
@@ -717,12 +727,14 @@ def rms_rescale(x, out=None):
 class PageTable:
     """Block tables of up to max_req requests over one pool of pages (page_table makes an
     empty one).  Request r's token t lies in page table[r, t // page_size].  The free pages are
-    ring[state[0]], ring[state[0] + 1], ... (state[1] of them, indices modulo n_pages)."""
+    ring[state[0]], ring[state[0] + 1], ... (state[1] of them, indices modulo n_pages).  With refs
+    (page_refs) requests may share pages: kv_fork in place of kv_plan."""
     page_size: int
     table: object      # torch.int32 [max_req, max_pages]
     held: object       # torch.int32 [max_req]: pages each request holds
     ring: object       # torch.int32 [n_pages]
     state: object      # torch.int32 [4]: head, count, 0, 0
+    refs: object = None    # torch.int32 [5 n_pages + 1024]: holders of each page, then words of the calls
 
     @property
     def n_pages(self) -> int:
@@ -746,14 +758,22 @@ class PageTable:
         return p
 
 
-def page_table(n_pages: int, page_size: int, max_req: int, max_pages: int, device="cuda") -> PageTable:
+def page_refs(n_pages: int, device="cuda"):
+    """Zero counts for an empty pool (W12_REFS_WORDS).  For tables that hold pages already, the first
+    n_pages entries are the number of entries table[r, c], c < held[r], that name each page."""
+    torch = _torch()
+    return torch.zeros(5 * n_pages + 1024, dtype=torch.int32, device=device)
+
+
+def page_table(n_pages: int, page_size: int, max_req: int, max_pages: int, device="cuda",
+               shared: bool = False) -> PageTable:
     """A pool of n_pages free pages and empty tables for max_req requests of at most
-    max_pages pages each."""
+    max_pages pages each; shared: with counts, for requests that share pages (kv_fork)."""
     torch = _torch()
     i32 = dict(dtype=torch.int32, device=device)
     return PageTable(page_size, torch.full((max_req, max_pages), -1, **i32),
                      torch.zeros(max_req, **i32), torch.arange(n_pages, **i32),
-                     torch.tensor([0, n_pages, 0, 0], **i32))
+                     torch.tensor([0, n_pages, 0, 0], **i32), page_refs(n_pages, device) if shared else None)
 
 
 @dataclass
@@ -897,6 +917,8 @@ def _issue(name: str, args, device):
 
 
 def _plan_args(pt: PageTable, length, req_off, kv_len, pos, slot):
+    if pt.refs is not None:
+        raise ValueError("kv_plan: the pool's pages are shared (refs): kv_fork")
     dev, n_req, m = pt.device, int(length.numel()), int(pos.numel())
     for name, t, size in (("length", length, n_req), ("req_off", req_off, n_req + 1),
                           ("kv_len", kv_len, n_req), ("pos", pos, m), ("slot", slot, m)):
@@ -1026,6 +1048,111 @@ def attn_paged(q, cache: KvCache, table, kv_len, req_off, out=None, scale=None, 
     args, _keep = _attn_args(q, cache, table, kv_len, req_off, out, scale, ws)
     _issue("w12_attn_paged", args, cache.device)
     return out
+
+
+# ----------------------------------------------------------------------------- shared pages
+def _refs(what: str, pt: PageTable):
+    if pt.refs is None:
+        raise ValueError(f"{what}: the pool has no counts of its pages' holders (refs: page_refs)")
+    _int32(f"{what}: refs", pt.refs, 5 * pt.n_pages + 1024, pt.device)
+    return pt.refs
+
+
+def _quads(name: str, t, n: int, device):
+    if t.dim() != 2 or t.shape[1] != 4:
+        raise ValueError(f"{name} must be [n, 4]")
+    _int32(name, t, 4 * n, device)
+
+
+def _fork_args(pt: PageTable, parent, length, req_off, kv_len, pos, slot, copies):
+    dev, n_req, m = pt.device, int(length.numel()), int(pos.numel())
+    for name, t, size in (("parent", parent, n_req), ("length", length, n_req), ("req_off", req_off, n_req + 1),
+                          ("kv_len", kv_len, n_req), ("pos", pos, m), ("slot", slot, m)):
+        if t is not None or name != "parent":
+            _int32(f"kv_fork: {name}", t, size, dev)
+    _quads("kv_fork: copies", copies, n_req, dev)
+    d, refs = pt.desc(), _refs("kv_fork", pt)
+    _disjoint("kv_fork", {"kv_len": kv_len, "pos": pos, "slot": slot, "copies": copies, "table": pt.table,
+                          "held": pt.held, "ring": pt.ring, "state": pt.state, "refs": refs},
+              {"parent": parent, "length": length, "req_off": req_off})
+    args = (ctypes.byref(d), _ptr(refs), _ptr(parent) if parent is not None else None, _ptr(length), _ptr(req_off),
+            n_req, m, _ptr(kv_len), _ptr(pos) if m else None, _ptr(slot) if m else None, _ptr(copies), _stream(dev))
+    return args, (pt, parent, length, req_off, kv_len, pos, slot, copies, d)
+
+
+def kv_fork(pt: PageTable, parent, length, req_off, m: int, kv_len=None, pos=None, slot=None, copies=None):
+    """kv_plan for requests that share pages (w12_kv_fork): request r becomes the first length[r]
+    tokens of request parent[r] as it was (parent None: its own; -1: none) and rows req_off[r] ..
+    req_off[r+1]-1.  Full pages are shared; where a request will write into a page that another
+    one holds, copies[r] = (page, new page, tokens, 0) says what kv_copy has to copy before the rows are
+    appended.  Served whole or, if the pool has too few pages, not at all (everything -1).
+    Returns int32 (kv_len [n_req], pos [m], slot [m], copies [n_req, 4])."""
+    torch = _torch()
+    new = lambda *n: torch.empty(n, dtype=torch.int32, device=pt.device)
+    kv_len = new(length.numel()) if kv_len is None else kv_len
+    pos = new(m) if pos is None else pos
+    slot = new(m) if slot is None else slot
+    copies = new(length.numel(), 4) if copies is None else copies
+    if pos.numel() != m:
+        raise ValueError(f"kv_fork: pos must have m = {m} entries")
+    args, _keep = _fork_args(pt, parent, length, req_off, kv_len, pos, slot, copies)
+    _issue("w12_kv_fork", args, pt.device)
+    return kv_len, pos, slot, copies
+
+
+def _copy_args(caches, copies):
+    caches = list(caches)
+    if not caches:
+        raise ValueError("kv_copy: no caches")
+    dev = caches[0].device
+    if any(c.device != dev for c in caches):
+        raise ValueError("kv_copy: the caches must be on one device")
+    _quads("kv_copy: copies", copies, copies.shape[0], dev)
+    d = (W12Kv * len(caches))(*(c.desc() for c in caches))
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                   for t in (copies, *(x for c in caches for x in (c.k, c.v))) if t.numel())
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("kv_copy: the caches, or a cache and copies, overlap")
+    args = (d, len(caches), _ptr(copies) if copies.shape[0] else None, copies.shape[0], _stream(dev))
+    return args, (caches, copies, d), dev
+
+
+def kv_copy(caches, copies):
+    """Copy pages in the caches of all layers (w12_kv_copy): copies int32 [n, 4] as kv_fork or
+    kv_compact give them."""
+    args, _keep, dev = _copy_args(caches, copies)
+    _issue("w12_kv_copy", args, dev)
+
+
+def _compact_args(pt: PageTable, first: int, moves, moved):
+    dev = pt.device
+    _quads("kv_compact: moves", moves, moves.shape[0], dev)
+    _int32("kv_compact: moved", moved, 1, dev)
+    d, refs = pt.desc(), _refs("kv_compact", pt)
+    if first < 0 or not 1 <= moves.shape[0] <= pt.n_pages - first:
+        raise ValueError("kv_compact: the range leaves the pool")
+    _disjoint("kv_compact", {"moves": moves, "moved": moved, "table": pt.table, "ring": pt.ring, "state": pt.state,
+                             "refs": refs}, {"held": pt.held})
+    args = (ctypes.byref(d), _ptr(refs), first, moves.shape[0], _ptr(moves), _ptr(moved), _stream(dev))
+    return args, (pt, moves, moved, d)
+
+
+def kv_compact(pt: PageTable, first: int, n_clear: int, moves=None, moved=None):
+    """Clear the pages first .. first + n_clear - 1 of the pool (w12_kv_compact): those in use move to
+    free pages outside, and the tables follow; kv_copy with the returned moves [n_clear, 4] moves
+    the contents.  moved [1] is their number, -1 (and nothing changed) if there are too few
+    outside.  Afterwards the range is the end of the free ring."""
+    torch = _torch()
+    new = lambda *n: torch.empty(n, dtype=torch.int32, device=pt.device)
+    if n_clear < 1:
+        raise ValueError("kv_compact: an empty range")
+    moves = new(n_clear, 4) if moves is None else moves
+    moved = new(1) if moved is None else moved
+    if moves.shape[0] != n_clear:
+        raise ValueError(f"kv_compact: moves must be [{n_clear}, 4]")
+    args, _keep = _compact_args(pt, first, moves, moved)
+    _issue("w12_kv_compact", args, pt.device)
+    return moves, moved
 
 
 # ----------------------------------------------------------------------------- prepared calls
@@ -1160,3 +1287,20 @@ def prepare_attn_paged(q, cache: KvCache, table, kv_len, req_off, out, scale=Non
     stream, are prepared with a ws of their own (attn_workspace)."""
     args, keep = _attn_args(q, cache, table, kv_len, req_off, out, scale, ws)
     return _prepared("w12_attn_paged", args, keep, cache.device)
+
+
+def prepare_kv_fork(pt: PageTable, parent, length, req_off, kv_len, pos, slot, copies) -> Prepared:
+    """kv_fork of m = pos.numel() rows into kv_len, pos, slot and copies."""
+    args, keep = _fork_args(pt, parent, length, req_off, kv_len, pos, slot, copies)
+    return _prepared("w12_kv_fork", args, keep, pt.device)
+
+
+def prepare_kv_copy(caches, copies) -> Prepared:
+    args, keep, dev = _copy_args(caches, copies)
+    return _prepared("w12_kv_copy", args, keep, dev)
+
+
+def prepare_kv_compact(pt: PageTable, first: int, moves, moved) -> Prepared:
+    """kv_compact of moves.shape[0] pages from page first on."""
+    args, keep = _compact_args(pt, first, moves, moved)
+    return _prepared("w12_kv_compact", args, keep, pt.device)
