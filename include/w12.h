@@ -616,6 +616,30 @@ w12_status w12_kv_copy(const w12_kv* layers, uint32_t n_layers, const int32_t* c
 w12_status w12_kv_compact(const w12_pages* p, int32_t* refs, uint32_t first, uint32_t n_clear,
                           int32_t* moves, int32_t* moved, void* stream);
 
+/* w12_attn_paged where requests share their first tokens, which are read once for all of them: group
+ * g is requests grp_off[g] .. grp_off[g+1]-1, and the first grp_len[g] tokens of each lie in the same
+ * pages (those in the table row of its first request that has rows and a length are read; below 1:
+ * nothing is shared).  Requests in no company are groups of one.  Results are those of w12_attn_paged up to the
+ * order of the FP32 sums, with the same rules for rows that see no token, for what lies behind a
+ * row's last token, for rows of no request, and for requests and pages that are none (a shared
+ * page that is none makes the rows of its whole group NaN).  Every row gets NaN when grp_off is not
+ * 0 = grp_off[0] <= grp_off[1] <= ... <= grp_off[n_grp] = n_req.  (Of grp_len what every row of the
+ * group sees is shared, in whole units of 64 tokens; the rest is read per request.)
+ * grp_off [n_grp + 1] and grp_len [n_grp] device int32; everything else as w12_attn_paged, but for
+ * the workspace: w12_attn_shared_ws_bytes(m, n_heads, head_dim) bytes (0 for arguments that are
+ * none), 256-byte aligned, in any state; calls sharing one must be ordered.  Same inputs, same bits.
+ * Errors as w12_attn_paged, and W12_ERR_RANGE (n_grp outside 1..W12_MAX_REQ, m * n_heads >
+ * W12_MAX_SHARED_ROWS, (m * n_heads + 64 * n_req * n_kv_heads) * (max_pages * page_size + 1024) >=
+ * 2^38). */
+#define W12_MAX_SHARED_ROWS (1u << 17)
+size_t w12_attn_shared_ws_bytes(uint32_t m, uint32_t n_heads, uint32_t head_dim);
+w12_status w12_attn_shared(const uint16_t* q, uint64_t q_stride, uint32_t m, uint32_t n_heads,
+                           const w12_kv* kv, const int32_t* table, uint32_t max_pages,
+                           const int32_t* kv_len, const int32_t* req_off, uint32_t n_req,
+                           const int32_t* grp_off, const int32_t* grp_len, uint32_t n_grp,
+                           float scale, uint16_t* out, uint64_t out_stride, void* ws,
+                           size_t ws_bytes, void* stream);
+
 /* Measurement helper, not part of the W12 method: streams `bytes` (a multiple of 16,
  * below 2^32) of device memory at `buf` (16-byte aligned) with the nontemporal 16-byte
  * buffer loads the GEMM kernels use for W12 tiles, grid-stride over `workgroups`

@@ -1,6 +1,7 @@
-// C-ABI host layer of the pages that requests share: argument validation (before any HIP call)
-// and launch.
+// C-ABI host layer of several continuations of one prompt (shared pages, the attention over them):
+// argument validation (before any HIP call) and launch.
 #include "w12.h"
+#include "w12_attn_shared.h"
 #include "w12_check.h"
 #include "w12_fork.h"
 
@@ -116,6 +117,66 @@ w12_status w12_kv_compact(const w12_pages* p, int32_t* refs, uint32_t first, uin
   a.moves = moves;
   a.moved = moved;
   return hip_status(launch_kv_compact(a, (hipStream_t)stream));
+}
+
+size_t w12_attn_shared_ws_bytes(uint32_t m, uint32_t n_heads, uint32_t head_dim) {
+  if (n_heads < 1 || n_heads > W12_MAX_HEADS || (uint64_t)m * n_heads > W12_MAX_SHARED_ROWS) return 0;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  return (size_t)shared_bytes(m, n_heads, head_dim);
+}
+
+w12_status w12_attn_shared(const uint16_t* q, uint64_t q_stride, uint32_t m, uint32_t n_heads,
+                           const w12_kv* kv, const int32_t* table, uint32_t max_pages,
+                           const int32_t* kv_len, const int32_t* req_off, uint32_t n_req,
+                           const int32_t* grp_off, const int32_t* grp_len, uint32_t n_grp,
+                           float scale, uint16_t* out, uint64_t out_stride, void* ws,
+                           size_t ws_bytes, void* stream) {
+  if (!kv || !table || !kv_len || !req_off || !grp_off || !grp_len || !ws) return W12_ERR_NULL;
+  if (m > 0 && (!q || !out)) return W12_ERR_NULL;
+  const w12_status st = check_kv(kv, n_heads);
+  if (st != W12_OK) return st;
+  const uint32_t d = kv->head_dim;
+  if (!length_ok(max_pages, kv->page_size)) return W12_ERR_SHAPE;
+  if (!stride_ok(q_stride, n_heads, d) || !stride_ok(out_stride, n_heads, d)) return W12_ERR_SHAPE;
+  if (n_req < 1 || n_req > W12_MAX_REQ || n_grp < 1 || n_grp > W12_MAX_REQ) return W12_ERR_RANGE;
+  if ((uint64_t)m * n_heads > W12_MAX_SHARED_ROWS) return W12_ERR_RANGE;
+  // Units of at least 32 tokens by tiles of at least 16 query rows, a place each on the lines, with
+  // the items' own places: their number stays below 2^31.
+  const uint64_t tokens = (uint64_t)max_pages * kv->page_size + 1024;   // <= 2^30 + 2^10
+  const uint64_t qrows = (uint64_t)m * n_heads + 64ull * n_req * kv->n_kv_heads;   // < 2^30
+  if (qrows * tokens >= (1ull << 38)) return W12_ERR_RANGE;
+  const float score_scale = (float)((double)scale * (double)kv->k_scale * 1.4426950408889634);
+  if (!isfinite(score_scale)) return W12_ERR_FORMAT;
+  if (ws_bytes < shared_bytes(m, n_heads, d)) return W12_ERR_WORKSPACE;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return W12_ERR_ALIGN;
+  if (!aligned4({table, kv_len, req_off, grp_off, grp_len})) return W12_ERR_ALIGN;
+  if (m == 0) return W12_OK;
+  SharedArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.m = m;
+  a.n_heads = n_heads;
+  a.n_kv_heads = kv->n_kv_heads;
+  a.group = n_heads / kv->n_kv_heads;
+  a.group_inv = a.group == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / a.group);
+  a.n_pages = kv->n_pages;
+  a.page_shift = log2u(kv->page_size);
+  a.kc = (const uint8_t*)kv->k;
+  a.vc = (const uint8_t*)kv->v;
+  a.table = table;
+  a.max_pages = max_pages;
+  a.kv_len = kv_len;
+  a.req_off = req_off;
+  a.grp_off = grp_off;
+  a.grp_len = grp_len;
+  a.n_req = n_req;
+  a.n_grp = n_grp;
+  a.score_scale = score_scale;
+  a.v_scale = kv->v_scale;
+  a.out = out;
+  a.ws = (uint8_t*)ws;
+  return hip_status(launch_attn_shared(a, d, kv->dtype, (hipStream_t)stream));
 }
 
 }  // extern "C"

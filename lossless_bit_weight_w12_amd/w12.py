@@ -24,6 +24,7 @@ MAX_KV_ROWS = 1 << 20          # W12_MAX_KV_ROWS: rows of one cache call
 MAX_HEADS = 1024               # W12_MAX_HEADS
 MAX_LAYERS = 1024              # W12_MAX_LAYERS: caches of one kv_copy
 MAX_COPIES = 1 << 22           # W12_MAX_COPIES
+MAX_SHARED_ROWS = 1 << 17      # W12_MAX_SHARED_ROWS: query rows (m * n_heads) of one attn_shared
 ATTN_WS_BYTES = 36 << 20       # W12_ATTN_WS_BYTES
 STATUS = {0: "W12_OK", -1: "W12_ERR_NULL", -2: "W12_ERR_SHAPE", -3: "W12_ERR_RANGE",
           -4: "W12_ERR_FORMAT", -5: "W12_ERR_WORKSPACE", -6: "W12_ERR_HIP", -7: "W12_ERR_ALIGN"}
@@ -36,7 +37,8 @@ EXPORTS = ("w12_tiles_bytes", "w12_workspace_bytes", "w12_workspace_init", "w12_
            "w12_screen_bytes", "w12_screen_encode", "w12_lmhead_verify2", "w12_lmhead_verify2_batched",
            "w12_screen_logits_f32", "w12_f8_tile", "w12_gemm_f8", "w12_gemm_f8_group",
            "w12_gemm_f8_rms", "w12_gemm_f8_group_rms", "w12_kv_plan", "w12_qk_rope",
-           "w12_attn_paged", "w12_kv_fork", "w12_kv_copy", "w12_kv_compact")
+           "w12_attn_paged", "w12_kv_fork", "w12_kv_copy", "w12_kv_compact",
+           "w12_attn_shared_ws_bytes", "w12_attn_shared")
 NOALLOC_SCRATCH_BYTES = 32 << 20   # W12_NOALLOC_SCRATCH_BYTES
 ENCODE_TOTAL_OFFSET = 2112   # W12_ENCODE_TOTAL_OFFSET: true escape count in an encode workspace
 
@@ -180,6 +182,13 @@ def lib():
         L.w12_kv_compact.restype = c_int32
         L.w12_kv_compact.argtypes = [ctypes.POINTER(W12Pages), c_void_p, c_uint32, c_uint32, c_void_p,
                                      c_void_p, c_void_p]
+        L.w12_attn_shared_ws_bytes.restype = c_size_t
+        L.w12_attn_shared_ws_bytes.argtypes = [c_uint32, c_uint32, c_uint32]
+        L.w12_attn_shared.restype = c_int32
+        L.w12_attn_shared.argtypes = [c_void_p, c_uint64, c_uint32, c_uint32, ctypes.POINTER(W12Kv),
+                                      c_void_p, c_uint32, c_void_p, c_void_p, c_uint32, c_void_p,
+                                      c_void_p, c_uint32, c_float, c_void_p, c_uint64, c_void_p,
+                                      c_size_t, c_void_p]
         L.w12_status_str.restype = ctypes.c_char_p
         L.w12_status_str.argtypes = [c_int32]
         L.w12_version.restype = c_uint32
@@ -1155,6 +1164,72 @@ def kv_compact(pt: PageTable, first: int, n_clear: int, moves=None, moved=None):
     return moves, moved
 
 
+_SHARED_WS = {}
+
+
+def attn_shared_workspace(m: int, n_heads: int, head_dim: int, device="cuda"):
+    """A workspace for attn_shared, in no particular state, for callers that keep their own: one for
+    each stream or captured graph that may run at the same time as others."""
+    n = int(lib().w12_attn_shared_ws_bytes(m, n_heads, head_dim))
+    if n == 0:
+        raise ValueError("attn_shared_workspace: no such call")
+    return _torch().empty(n, dtype=_torch().uint8, device=device)
+
+
+def _shared_ws(dev, ws, m, n_heads, d):
+    """The caller's workspace, or one per device and stream; under graph capture memory of the graph."""
+    torch = _torch()
+    if ws is not None:
+        if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"attn_shared: ws must be a contiguous uint8 tensor on {dev}")
+        return ws
+    with torch.cuda.device(dev):
+        if torch.cuda.is_current_stream_capturing():
+            return attn_shared_workspace(m, n_heads, d, dev)
+        key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+        have = _SHARED_WS.get(key)
+        if have is None or have.numel() < lib().w12_attn_shared_ws_bytes(m, n_heads, d):
+            have = _SHARED_WS[key] = attn_shared_workspace(m, n_heads, d, dev)
+        return have
+
+
+def _shared_args(q, cache: KvCache, table, kv_len, req_off, grp_off, grp_len, out, scale, ws):
+    c = cache.desc()
+    dev, m, n, d, n_req = cache.device, q.shape[0], q.shape[1], c.head_dim, int(kv_len.numel())
+    n_grp = int(grp_len.numel())
+    qs, os_ = _heads("attn_shared: q", q, m, n, d, dev), _heads("attn_shared: out", out, m, n, d, dev)
+    if table.dim() != 2 or table.shape[0] < n_req:
+        raise ValueError("attn_shared: table must be [>= n_req, max_pages]")
+    _int32("attn_shared: table", table, table.shape[0] * table.shape[1], dev)
+    for name, t, size in (("kv_len", kv_len, n_req), ("req_off", req_off, n_req + 1),
+                          ("grp_off", grp_off, n_grp + 1), ("grp_len", grp_len, n_grp)):
+        _int32(f"attn_shared: {name}", t, size, dev)
+    if m * n > MAX_SHARED_ROWS:
+        raise ValueError(f"attn_shared: at most {MAX_SHARED_ROWS} query rows (m * n_heads)")
+    ws = _shared_ws(dev, ws, m, n, d)
+    _disjoint("attn_shared", {"out": out, "ws": ws},
+              {"q": q, "the cache's k": cache.k, "the cache's v": cache.v, "table": table,
+               "kv_len": kv_len, "req_off": req_off, "grp_off": grp_off, "grp_len": grp_len})
+    scale = d ** -0.5 if scale is None else float(scale)
+    args = (_ptr(q), qs, m, n, ctypes.byref(c), _ptr(table), table.shape[1], _ptr(kv_len), _ptr(req_off),
+            n_req, _ptr(grp_off), _ptr(grp_len), n_grp, scale, _ptr(out), os_, _ptr(ws), ws.numel(), _stream(dev))
+    return args, (q, cache, table, kv_len, req_off, grp_off, grp_len, out, ws, c)
+
+
+def attn_shared(q, cache: KvCache, table, kv_len, req_off, grp_off, grp_len, out=None, scale=None, ws=None):
+    """attn_paged for requests that share their first tokens (w12_attn_shared): the first grp_len[g]
+    tokens of requests grp_off[g] .. grp_off[g+1]-1 lie in the same pages and are read once for all of
+    them.  grp_off int32 [n_grp + 1] from 0 to n_req, grp_len int32 [n_grp].  Returns out (BF16; rows
+    of no request are left as they were)."""
+    if q.dim() != 3:
+        raise ValueError("attn_shared: q must be [m, n_heads, head_dim]")
+    if out is None:
+        out = _torch().zeros(tuple(q.shape), dtype=q.dtype, device=q.device)
+    args, _keep = _shared_args(q, cache, table, kv_len, req_off, grp_off, grp_len, out, scale, ws)
+    _issue("w12_attn_shared", args, cache.device)
+    return out
+
+
 # ----------------------------------------------------------------------------- prepared calls
 class Prepared:
     """One library call with its arguments marshalled once (device pointers, descriptor,
@@ -1304,3 +1379,11 @@ def prepare_kv_compact(pt: PageTable, first: int, moves, moved) -> Prepared:
     """kv_compact of moves.shape[0] pages from page first on."""
     args, keep = _compact_args(pt, first, moves, moved)
     return _prepared("w12_kv_compact", args, keep, pt.device)
+
+
+def prepare_attn_shared(q, cache: KvCache, table, kv_len, req_off, grp_off, grp_len, out, scale=None,
+                        ws=None) -> Prepared:
+    """attn_shared into out.  As with prepare_attn_paged, graphs and streams that may run at the same
+    time are prepared with a ws of their own (attn_shared_workspace)."""
+    args, keep = _shared_args(q, cache, table, kv_len, req_off, grp_off, grp_len, out, scale, ws)
+    return _prepared("w12_attn_shared", args, keep, cache.device)

@@ -160,3 +160,28 @@ def test_compact_refuses(L, change, status):
     a = dict(p=pages(), refs=FAKE, first=90, n=10, moves=FAKE, moved=FAKE)
     a.update(change)
     assert L.w12_kv_compact(*a.values(), None) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(kv=None), NULL), (dict(table=None), NULL), (dict(kv_len=None), NULL), (dict(off=None), NULL),
+    (dict(grp_off=None), NULL), (dict(grp_len=None), NULL), (dict(ws=None), NULL), (dict(q=None), NULL),
+    (dict(out=None), NULL), (dict(kv=kv(k=None)), NULL), (dict(kv=kv(head_dim=96)), SHAPE),
+    (dict(heads=41), SHAPE), (dict(q_stride=5112), SHAPE), (dict(out_stride=5121), SHAPE), (dict(max_pages=0), SHAPE),
+    (dict(n_req=0), RANGE), (dict(n_req=4097), RANGE), (dict(n_grp=0), RANGE), (dict(n_grp=4097), RANGE),
+    (dict(m=3277), RANGE), (dict(max_pages=1 << 25), RANGE), (dict(scale=float("inf")), FORMAT), (dict(scale=float("nan")), FORMAT),
+    (dict(kv=kv(dtype=1, k_scale=0.0)), FORMAT), (dict(ws_bytes=-1), WS), (dict(q=FAKE + 8), ALIGN),
+    (dict(ws=FAKE + 16), ALIGN), (dict(grp_off=FAKE + 2), ALIGN), (dict(m=0, q=None, out=None), 0)])
+def test_attn_shared_refuses(L, change, status):
+    a = dict(q=FAKE, q_stride=5120, m=24, heads=40, kv=kv(), table=FAKE, max_pages=600, kv_len=FAKE, off=FAKE, n_req=24,
+             grp_off=FAKE, grp_len=FAKE, n_grp=6, scale=0.1, out=FAKE, out_stride=5120, ws=FAKE, ws_bytes=0)
+    a["ws_bytes"] = L.w12_attn_shared_ws_bytes(24, 40, 128) + change.pop("ws_bytes", 0)
+    a.update(change)
+    a["kv"] = ctypes.byref(a["kv"]) if a["kv"] is not None else None
+    assert L.w12_attn_shared(*a.values(), None) == status
+
+
+def test_attn_shared_workspace_bytes(L):
+    """None for calls that are none; more for more rows and wider heads."""
+    f = L.w12_attn_shared_ws_bytes
+    assert f(1, 0, 128) == f(1, 1025, 128) == f(1, 40, 96) == f(3277, 40, 128) == 0
+    assert 0 < f(1, 1, 64) < f(2, 1, 64) < f(2, 1, 128) and f(1 << 17, 1, 256) > 0
