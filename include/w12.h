@@ -640,6 +640,35 @@ w12_status w12_attn_shared(const uint16_t* q, uint64_t q_stride, uint32_t m, uin
                            float scale, uint16_t* out, uint64_t out_stride, void* ws,
                            size_t ws_bytes, void* stream);
 
+/* The beams that go on: for each group g of rows grp_off[g] .. grp_off[g+1]-1 of logits (at most
+ * W12_MAX_BEAMS of them) the k best pairs of a row and a token, by score = scores[row] + log
+ * softmax(logits[row])[token] in FP64 (a score that is no number counts as -inf), the larger first.
+ * Within a row the order is the logits' own (NaN as -inf), equal ones with the lower token first;
+ * between rows with equal scores the lower row comes first.  Written for j < k at [g][j]: parent (the row,
+ * as w12_kv_fork takes it where beams are requests), token, and score_out (the score in FP32).  A
+ * group without rows gets -1, -1, -inf.  Everything is -1, -1, NaN when grp_off is not 0 <=
+ * grp_off[0] <= grp_off[1] <= ... <= n or a group has more than W12_MAX_BEAMS rows.
+ * (A row's log-sum-exp is within about 1e-8 of exact: scores of different rows that are closer than that
+ * may change places, those of rows with the same logits do not.)
+ * logits device BF16 or FP32 [n][vocab], rows `stride` >= vocab elements apart, of any alignment;
+ * scores device FP32 [n]; grp_off device int32 [n_grp + 1]; parent, token int32, score_out FP32
+ * [n_grp][k].  ws: w12_beam_ws_bytes(n, vocab, k) bytes (0 for arguments that are none), 256-byte aligned,
+ * beginning with 16384 bytes of tickets that must be zero before its first use
+ * (w12_workspace_init) and that every call leaves zero; calls sharing one must be ordered.  Same inputs,
+ * same bits.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (vocab outside 1..W12_MAX_VOCAB, k outside
+ * 1..W12_MAX_BEAM_K or above vocab, stride); W12_ERR_RANGE (n > W12_MAX_REQ, n_grp outside
+ * 1..W12_MAX_REQ); W12_ERR_FORMAT (dtype); W12_ERR_WORKSPACE; W12_ERR_ALIGN. */
+#define W12_LOGITS_BF16 0
+#define W12_LOGITS_F32 1
+#define W12_MAX_VOCAB (1u << 21)
+#define W12_MAX_BEAMS 64       /* rows of a group, at most */
+#define W12_MAX_BEAM_K 64
+size_t w12_beam_ws_bytes(uint32_t n, uint32_t vocab, uint32_t k);
+w12_status w12_beam_select(const void* logits, uint32_t dtype, uint64_t stride, uint32_t n,
+                           uint32_t vocab, const float* scores, const int32_t* grp_off,
+                           uint32_t n_grp, uint32_t k, int32_t* parent, int32_t* token,
+                           float* score_out, void* ws, size_t ws_bytes, void* stream);
+
 /* Measurement helper, not part of the W12 method: streams `bytes` (a multiple of 16,
  * below 2^32) of device memory at `buf` (16-byte aligned) with the nontemporal 16-byte
  * buffer loads the GEMM kernels use for W12 tiles, grid-stride over `workgroups`

@@ -1,7 +1,9 @@
-// C-ABI host layer of several continuations of one prompt (shared pages, the attention over them):
+// C-ABI host layer of several continuations of one prompt (shared pages, the attention over
+// them, the choice of beams):
 // argument validation (before any HIP call) and launch.
 #include "w12.h"
 #include "w12_attn_shared.h"
+#include "w12_beam.h"
 #include "w12_check.h"
 #include "w12_fork.h"
 
@@ -177,6 +179,40 @@ w12_status w12_attn_shared(const uint16_t* q, uint64_t q_stride, uint32_t m, uin
   a.out = out;
   a.ws = (uint8_t*)ws;
   return hip_status(launch_attn_shared(a, d, kv->dtype, (hipStream_t)stream));
+}
+
+size_t w12_beam_ws_bytes(uint32_t n, uint32_t vocab, uint32_t k) {
+  if (n > W12_MAX_REQ || vocab < 1 || vocab > W12_MAX_VOCAB || k < 1 || k > W12_MAX_BEAM_K) return 0;
+  return (size_t)beam_bytes(n, vocab, k);
+}
+
+w12_status w12_beam_select(const void* logits, uint32_t dtype, uint64_t stride, uint32_t n,
+                           uint32_t vocab, const float* scores, const int32_t* grp_off,
+                           uint32_t n_grp, uint32_t k, int32_t* parent, int32_t* token,
+                           float* score_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!grp_off || !parent || !token || !score_out || !ws) return W12_ERR_NULL;
+  if (n > 0 && (!logits || !scores)) return W12_ERR_NULL;
+  if (vocab < 1 || vocab > W12_MAX_VOCAB || k < 1 || k > W12_MAX_BEAM_K || k > vocab) return W12_ERR_SHAPE;
+  if (stride < vocab || stride >= (1ull << 40)) return W12_ERR_SHAPE;
+  if (n > W12_MAX_REQ || n_grp < 1 || n_grp > W12_MAX_REQ) return W12_ERR_RANGE;
+  if (dtype != W12_LOGITS_BF16 && dtype != W12_LOGITS_F32) return W12_ERR_FORMAT;
+  if (ws_bytes < beam_bytes(n, vocab, k)) return W12_ERR_WORKSPACE;
+  if (!aligned(logits, dtype == W12_LOGITS_F32 ? 4 : 2) || !aligned(ws, 256)) return W12_ERR_ALIGN;
+  if (!aligned4({scores, grp_off, parent, token, score_out})) return W12_ERR_ALIGN;
+  BeamArgs a{};
+  a.logits = logits;
+  a.stride = stride;
+  a.n = n;
+  a.vocab = vocab;
+  a.n_grp = n_grp;
+  a.k = k;
+  a.scores = scores;
+  a.grp_off = grp_off;
+  a.parent = parent;
+  a.token = token;
+  a.out = score_out;
+  a.ws = (uint8_t*)ws;
+  return hip_status(launch_beam_select(a, dtype == W12_LOGITS_F32, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -24,6 +24,9 @@ MAX_KV_ROWS = 1 << 20          # W12_MAX_KV_ROWS: rows of one cache call
 MAX_HEADS = 1024               # W12_MAX_HEADS
 MAX_LAYERS = 1024              # W12_MAX_LAYERS: caches of one kv_copy
 MAX_COPIES = 1 << 22           # W12_MAX_COPIES
+MAX_VOCAB = 1 << 21            # W12_MAX_VOCAB
+MAX_BEAMS, MAX_BEAM_K = 64, 64  # W12_MAX_BEAMS: rows of a group, W12_MAX_BEAM_K: pairs chosen
+LOGITS_BF16, LOGITS_F32 = 0, 1
 MAX_SHARED_ROWS = 1 << 17      # W12_MAX_SHARED_ROWS: query rows (m * n_heads) of one attn_shared
 ATTN_WS_BYTES = 36 << 20       # W12_ATTN_WS_BYTES
 STATUS = {0: "W12_OK", -1: "W12_ERR_NULL", -2: "W12_ERR_SHAPE", -3: "W12_ERR_RANGE",
@@ -38,7 +41,7 @@ EXPORTS = ("w12_tiles_bytes", "w12_workspace_bytes", "w12_workspace_init", "w12_
            "w12_screen_logits_f32", "w12_f8_tile", "w12_gemm_f8", "w12_gemm_f8_group",
            "w12_gemm_f8_rms", "w12_gemm_f8_group_rms", "w12_kv_plan", "w12_qk_rope",
            "w12_attn_paged", "w12_kv_fork", "w12_kv_copy", "w12_kv_compact",
-           "w12_attn_shared_ws_bytes", "w12_attn_shared")
+           "w12_attn_shared_ws_bytes", "w12_attn_shared", "w12_beam_ws_bytes", "w12_beam_select")
 NOALLOC_SCRATCH_BYTES = 32 << 20   # W12_NOALLOC_SCRATCH_BYTES
 ENCODE_TOTAL_OFFSET = 2112   # W12_ENCODE_TOTAL_OFFSET: true escape count in an encode workspace
 
@@ -189,6 +192,12 @@ def lib():
                                       c_void_p, c_uint32, c_void_p, c_void_p, c_uint32, c_void_p,
                                       c_void_p, c_uint32, c_float, c_void_p, c_uint64, c_void_p,
                                       c_size_t, c_void_p]
+        L.w12_beam_ws_bytes.restype = c_size_t
+        L.w12_beam_ws_bytes.argtypes = [c_uint32, c_uint32, c_uint32]
+        L.w12_beam_select.restype = c_int32
+        L.w12_beam_select.argtypes = [c_void_p, c_uint32, c_uint64, c_uint32, c_uint32, c_void_p,
+                                      c_void_p, c_uint32, c_uint32, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_size_t, c_void_p]
         L.w12_status_str.restype = ctypes.c_char_p
         L.w12_status_str.argtypes = [c_int32]
         L.w12_version.restype = c_uint32
@@ -1230,6 +1239,86 @@ def attn_shared(q, cache: KvCache, table, kv_len, req_off, grp_off, grp_len, out
     return out
 
 
+# ----------------------------------------------------------------------------- beams
+_BEAM_WS = {}
+
+
+def beam_workspace(n: int, vocab: int, k: int, device="cuda"):
+    """A workspace for beam_select (zero tickets), for callers that keep their own: one for each stream
+    or captured graph that may run at the same time as others.  It is zeroed on the current stream."""
+    size = int(lib().w12_beam_ws_bytes(n, vocab, k))
+    if size == 0:
+        raise ValueError("beam_workspace: no such call")
+    return _torch().zeros(size, dtype=_torch().uint8, device=device)
+
+
+def _beam_ws(dev, ws, n, vocab, k):
+    """The caller's workspace, or one per device and stream; under graph capture memory of the
+    graph, its tickets zeroed inside the graph."""
+    torch = _torch()
+    if ws is not None:
+        if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"beam_select: ws must be a contiguous uint8 tensor on {dev}")
+        return ws
+    size = int(lib().w12_beam_ws_bytes(n, vocab, k))
+    with torch.cuda.device(dev):
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(max(size, 16384), dtype=torch.uint8, device=dev)
+            _check("w12_workspace_init", lib().w12_workspace_init(_ptr(ws), 16384, _stream(dev)))
+            return ws
+        key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+        if key not in _BEAM_WS or _BEAM_WS[key].numel() < size:
+            _BEAM_WS[key] = torch.zeros(max(size, 16384), dtype=torch.uint8, device=dev)
+        return _BEAM_WS[key]
+
+
+def _beam_args(logits, scores, grp_off, parent, token, score_out, ws):
+    torch = _torch()
+    if not logits.is_cuda:
+        raise ValueError("W12 calls need CUDA (HIP) tensors")
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("beam_select: logits must be [n, vocab], bfloat16 or float32")
+    dev, (n, vocab) = logits.device, logits.shape
+    if n and vocab > 1 and logits.stride(1) != 1 or n > 1 and logits.stride(0) < vocab:
+        raise ValueError("beam_select: a row's logits must be contiguous, and rows apart")
+    stride = logits.stride(0) if n > 1 else vocab
+    if parent.dim() != 2:
+        raise ValueError("beam_select: parent must be [n_grp, k]")
+    n_grp, k = parent.shape
+    _int32("beam_select: grp_off", grp_off, n_grp + 1, dev)
+    for name, t in (("parent", parent), ("token", token)):
+        _int32(f"beam_select: {name}", t, n_grp * k, dev)
+    for name, t, size in (("scores", scores, n), ("score_out", score_out, n_grp * k)):
+        if t.dtype != torch.float32 or t.numel() != size or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"beam_select: {name} must be a contiguous float32 tensor of {size} on {dev}")
+    ws = _beam_ws(dev, ws, n, vocab, k)
+    _disjoint("beam_select", {"parent": parent, "token": token, "score_out": score_out, "ws": ws},
+              {"logits": logits.unsqueeze(1), "scores": scores, "grp_off": grp_off})
+    args = (_ptr(logits) if n else None, LOGITS_F32 if logits.dtype == torch.float32 else LOGITS_BF16, stride, n, vocab,
+            _ptr(scores) if n else None, _ptr(grp_off), n_grp, k, _ptr(parent), _ptr(token), _ptr(score_out), _ptr(ws),
+            ws.numel(), _stream(dev))
+    return args, (logits, scores, grp_off, parent, token, score_out, ws), dev
+
+
+def beam_select(logits, scores, grp_off, k: int, parent=None, token=None, score_out=None, ws=None):
+    """The k best pairs of a row and a token of each group of rows grp_off[g] .. grp_off[g+1]-1, by
+    scores[row] + log softmax(logits[row])[token] (w12_beam_select).  logits [n, vocab] bfloat16 or
+    float32 (rows may be strided), scores float32 [n], grp_off int32 [n_grp + 1].  Returns (parent int32,
+    token int32, score float32), each [n_grp, k], the best first; with k beams to a group, parent as
+    it is goes to kv_fork."""
+    torch = _torch()
+    n_grp = grp_off.numel() - 1
+    new = lambda dtype: torch.empty((n_grp, k), dtype=dtype, device=logits.device)
+    parent = new(torch.int32) if parent is None else parent
+    token = new(torch.int32) if token is None else token
+    score_out = new(torch.float32) if score_out is None else score_out
+    if tuple(parent.shape) != (n_grp, k):
+        raise ValueError(f"beam_select: parent must be [{n_grp}, {k}]")
+    args, _keep, dev = _beam_args(logits, scores, grp_off, parent, token, score_out, ws)
+    _issue("w12_beam_select", args, dev)
+    return parent, token, score_out
+
+
 # ----------------------------------------------------------------------------- prepared calls
 class Prepared:
     """One library call with its arguments marshalled once (device pointers, descriptor,
@@ -1387,3 +1476,10 @@ def prepare_attn_shared(q, cache: KvCache, table, kv_len, req_off, grp_off, grp_
     time are prepared with a ws of their own (attn_shared_workspace)."""
     args, keep = _shared_args(q, cache, table, kv_len, req_off, grp_off, grp_len, out, scale, ws)
     return _prepared("w12_attn_shared", args, keep, cache.device)
+
+
+def prepare_beam_select(logits, scores, grp_off, parent, token, score_out, ws=None) -> Prepared:
+    """beam_select of k = parent.shape[1] pairs.  As with prepare_attn_paged, graphs and streams that may run
+    at the same time are prepared with a ws of their own (beam_workspace)."""
+    args, keep, dev = _beam_args(logits, scores, grp_off, parent, token, score_out, ws)
+    return _prepared("w12_beam_select", args, keep, dev)

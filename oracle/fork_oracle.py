@@ -122,3 +122,33 @@ def kv_compact(page: int, table, held, ring, state, refs, first: int, n_clear: i
     ring[:len(left)] = left
     state[0], state[1] = 0, len(left)
     return moves, len(live)
+
+
+def beam_select(logits, scores, off, k: int, max_beams: int = 64):
+    """logits [n, vocab] and scores [n] float64.  Returns (parent, token, score float64) [n_grp, k], and
+    the smallest difference between scores of two rows that the choice or its order turned on
+    (differences of rows with equal logits do not count: inf if there is none)."""
+    n, n_grp = len(logits), len(off) - 1
+    parent, token = np.full((n_grp, k), -1, np.int32), np.full((n_grp, k), -1, np.int32)
+    if not offsets_ok(off, n) or any(int(b) - int(a) > max_beams for a, b in zip(off, off[1:])):
+        return parent, token, np.full((n_grp, k), np.nan), np.inf
+    score, close = np.full((n_grp, k), -np.inf), np.inf
+    with np.errstate(all="ignore"):
+        for g in range(n_grp):
+            best = []
+            for r in range(int(off[g]), int(off[g + 1])):
+                x = np.asarray(logits[r], np.float64)
+                top = x.max()
+                lse = top + np.log(np.exp(x - top).sum())
+                rank = np.where(np.isnan(x), -np.inf, x)
+                order = np.argsort(-rank, kind="stable")[:k]
+                s = scores[r] + (rank[order] - lse)
+                best += [(-np.inf if np.isnan(v) else v, r, int(t)) for v, t in zip(s, order)]
+            best.sort(key=lambda b: -b[0])     # stable: lower rows first, a row's in its own order
+            for j, (v, r, t) in enumerate(best[:k]):
+                parent[g, j], token[g, j], score[g, j] = r, t, v
+            for (v, r, _), (w, q, _) in zip(best[:k], best[1:k + 1]):
+                if r != q and np.isfinite(v) and np.isfinite(w) and not (
+                        scores[r] == scores[q] and np.array_equal(logits[r], logits[q])):
+                    close = min(close, v - w)
+    return parent, token, score, close

@@ -185,3 +185,58 @@ def test_attn_shared_workspace_bytes(L):
     f = L.w12_attn_shared_ws_bytes
     assert f(1, 0, 128) == f(1, 1025, 128) == f(1, 40, 96) == f(3277, 40, 128) == 0
     assert 0 < f(1, 1, 64) < f(2, 1, 64) < f(2, 1, 128) and f(1 << 17, 1, 256) > 0
+
+
+# ---------------------------------------------------------------------------------- the beams
+def test_beam_oracle_worked_example():
+    """Two rows of three tokens: probabilities 1/2, 1/4, 1/4 and 1/8, 3/4, 1/8; prior scores log 1/2 and
+    log 1/3: the pairs' probabilities are 1/4, 1/8, 1/8 and 1/24, 1/4, 1/24."""
+    x = np.log(np.array([[2.0, 1, 1], [1, 6, 1]]))
+    parent, token, score, _ = fo.beam_select(x, np.log([1 / 2, 1 / 3]), [0, 2, 2], 5)
+    assert parent[0].tolist() in ([0, 1, 0, 0, 1], [1, 0, 0, 0, 1]) and sorted(token[0, :2].tolist()) == [0, 1]
+    assert token[0, 2:].tolist() == [1, 2, 0] and np.allclose(np.exp(score[0]), [1 / 4, 1 / 4, 1 / 8, 1 / 8, 1 / 24])
+    assert (parent[1] == -1).all() and (token[1] == -1).all() and (score[1] == -np.inf).all()
+
+
+def test_beam_oracle_ties_and_what_is_no_number():
+    x = np.zeros((3, 4))
+    parent, token, _, close = fo.beam_select(x, np.zeros(3), [0, 3], 6)
+    assert parent[0].tolist() == [0, 0, 0, 0, 1, 1] and token[0].tolist() == [0, 1, 2, 3, 0, 1] and close == np.inf
+    x[0, 2], x[1, 1] = np.nan, -np.inf
+    parent, token, score, _ = fo.beam_select(x, [9.0, 0.0, -1.0], [0, 3], 11)
+    assert parent[0].tolist() == [1, 1, 1, 2, 2, 2, 2, 0, 0, 0, 0] and token[0].tolist() == [0, 2, 3, 0, 1, 2, 3, 0, 1, 3, 2]
+    assert np.isinf(score[0, 7:]).all()
+
+
+def test_beam_oracle_against_torch():
+    import torch
+    g = np.random.default_rng(3)
+    x, s = g.standard_normal((7, 301)) * 3, g.standard_normal(7)
+    parent, token, score, close = fo.beam_select(x, s, [0, 3, 7], 9)
+    p = torch.log_softmax(torch.from_numpy(x), -1) + torch.from_numpy(s)[:, None]
+    for i, (a, b) in enumerate([(0, 3), (3, 7)]):
+        v, at = torch.topk(p[a:b].reshape(-1), 9)
+        assert np.allclose(score[i], v.numpy(), atol=1e-12)
+        assert (parent[i] == a + at.numpy() // 301).all() and (token[i] == at.numpy() % 301).all()
+    assert 0 < close < 1
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(grp_off=None), NULL), (dict(parent=None), NULL), (dict(token=None), NULL), (dict(out=None), NULL),
+    (dict(ws=None), NULL), (dict(logits=None), NULL), (dict(scores=None), NULL), (dict(vocab=0), SHAPE),
+    (dict(vocab=(1 << 21) + 1, stride=1 << 22), SHAPE), (dict(k=0), SHAPE), (dict(k=65), SHAPE), (dict(vocab=3), SHAPE),
+    (dict(stride=999), SHAPE), (dict(stride=1 << 40), SHAPE), (dict(n=4097), RANGE), (dict(n_grp=0), RANGE),
+    (dict(n_grp=4097), RANGE), (dict(dtype=2), FORMAT), (dict(ws_bytes=-1), WS), (dict(logits=FAKE + 2), ALIGN),
+    (dict(ws=FAKE + 8), ALIGN), (dict(scores=FAKE + 1), ALIGN)])
+def test_beam_select_refuses(L, change, status):
+    a = dict(logits=FAKE, dtype=1, stride=1000, n=8, vocab=1000, scores=FAKE, grp_off=FAKE, n_grp=2, k=4, parent=FAKE,
+             token=FAKE, out=FAKE, ws=FAKE, ws_bytes=0)
+    a["ws_bytes"] = L.w12_beam_ws_bytes(8, 1000, 4) + change.pop("ws_bytes", 0)
+    a.update(change)
+    assert L.w12_beam_select(*a.values(), None) == status
+
+
+def test_beam_workspace_bytes(L):
+    f = L.w12_beam_ws_bytes
+    assert f(4097, 10, 1) == f(1, 0, 1) == f(1, (1 << 21) + 1, 1) == f(1, 10, 0) == f(1, 100, 65) == 0
+    assert 16384 < f(1, 10, 1) < f(2, 10, 1) <= f(2, 10, 2) < f(2, 100000, 2) and f(4096, 1 << 21, 64) > 0
