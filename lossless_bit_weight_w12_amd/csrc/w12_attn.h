@@ -15,6 +15,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ int32_t uniform_load(const int32_t* p, uint64_t i) {
   // read through the constant address space (a scalar load): nothing here writes it
@@ -22,14 +25,12 @@ __device__ __forceinline__ int32_t uniform_load(const int32_t* p, uint64_t i) {
 }
 __device__ __forceinline__ uint32_t uni(uint32_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
 
-__device__ __forceinline__ uint32_t bf_pack(float a, float b) {
-  const __bf16 x = (__bf16)a, y = (__bf16)b;   // round to nearest even
-  return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+__device__ __forceinline__ uint32_t bf_pack(float a, float b) {   // round to nearest even, one instruction
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
-__device__ __forceinline__ uint32_t f16_pack(float a, float b) {
-  const _Float16 x = (_Float16)a, y = (_Float16)b;   // round to nearest even
-  return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+__device__ __forceinline__ uint32_t f16_pack(float a, float b) {   // round to nearest even
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, f16x2_t));
 }
 
 // 2^x as the hardware has it (one ulp; results below 2^-126 are zero, far below any rounding

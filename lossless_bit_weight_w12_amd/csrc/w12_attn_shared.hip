@@ -23,57 +23,148 @@ namespace w12 {
 
 namespace {
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
 template <int D, bool F8>
 struct Shared {
   static constexpr int NW = (int)shared_waves(D), NT = D == 256 ? 1 : 2, T = 64 * NW;
-  static constexpr int QT = 16 * NT;             // query rows of a wave
-  static constexpr int QW = QT * NW;             // of a workgroup's item, at most
+  static constexpr int QT = 16 * NT;             // query rows of a wave on the waves' line
+  static constexpr int RT = 32, QW = RT * NW;    // of a wave in a workgroup's item, of the item, at most
   static constexpr int UT = F8 ? 64 : 32;        // tokens of a wave's unit
   using Own = Tile<D, F8, NT, UT>;
-  static constexpr int KS = D / 32, DT = D / 16;
+  static constexpr int KS = D / 32, DT = D / 16;           // matrix steps and tiles of the waves' line,
+  static constexpr int KR = D / 16, DR = D / 32;           // and of a workgroup's item
   static constexpr int SU = D == 256 ? 1 : 2;    // units of 64 tokens of a step through LDS
   static constexpr uint32_t kChunk = 1024;       // one operand of a wave
-  static constexpr uint32_t kHalf = 2 * KS * kChunk;       // K, or V, of a span of 32 tokens
+  static constexpr uint32_t kHalf = KR * kChunk;           // K, or V, of a span of 32 tokens
   static constexpr uint32_t kStep = SU * 2 * 2 * kHalf;
   static constexpr int NL = F8 ? D / 32 : D / 16;          // 16-byte loads of a wave per step
   // Places on the lines: per item, and per unit (of 64 tokens by row tiles of 32, of UT tokens)
-  static constexpr uint32_t kLeadW = 8, kLeadV = 3, kLeastV = 6;
+  static constexpr uint32_t kLeadW = 8, kLeadV = 3;
   static __device__ __forceinline__ uint32_t cost(uint32_t row_tiles) {
     return row_tiles > 4 ? 8u : (row_tiles > 2 ? 6u : 5u);
   }
+
+  // The running softmax of a query row in the staged loop.  Weights are 2^(c s + bias - fine), the
+  // reference bias following the maximum only when that has risen by a factor of 2^8 (so the results are
+  // seldom rescaled; weights reach 2^8, in FP16 times 2^7).  c s + bias is one fused operation, exact
+  // but for its own rounding, and the bias is a number of its own, no rounded product that would have
+  // to be the same elsewhere; where c s is so large (2^24) that the bias cannot follow it within a
+  // factor of 2, `fine` takes the rest.
+  static constexpr float kUp = F8 ? 7.f : 0.f, kRise = 8.f;
+  struct Row {
+    float ref;    // raw score that the reference was taken from
+    float bias;   // kUp - c ref, rounded
+    float fine;
+    float sum;    // this lane's part, of the weights as they enter the product
+  };
+  static __device__ __forceinline__ Row row() { return Row{-INFINITY, kUp, 0.f, 0.f}; }
+  // The reference brought up to a span's largest score mx.
+  static __device__ __forceinline__ void rise(float c, float mx, Row& r, f32x16 (&o)[DR]) {
+    const auto other = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+    mx = fmaxf(__uint_as_float(other[0]), __uint_as_float(other[1]));
+    if (__any((mx - r.ref) * c > kRise)) {
+      const bool none = r.ref == -INFINITY;
+      if (mx > r.ref) {
+        const float bias = r.bias, fine = r.fine;
+        r.ref = mx;
+        r.bias = fmaf(-mx, c, kUp);
+        const float rest = fmaf(mx, c, r.bias) - kUp;
+        r.fine = fabsf(r.bias) < 16777216.f ? 0.f : rest;
+        const float fade = none ? 0.f : pow2((r.bias - bias) - (r.fine - fine));
+        r.sum *= fade;
+#pragma unroll
+        for (int d = 0; d < DR; ++d) o[d] *= fade;
+      }
+    }
+  }
+  // Two scores to their weights 2^(c x + bias).
+  static __device__ __forceinline__ uint32_t weigh(float c, float bias, float x, float y, float& sum) {
+    const float u = pow2(fmaf(x, c, bias)), v = pow2(fmaf(y, c, bias));
+    const uint32_t w = F8 ? f16_pack(u, v) : bf_pack(u, v);
+    if constexpr (F8)
+      sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_t, w), f16x2_t{(_Float16)1.f, (_Float16)1.f}, sum, false);
+    else
+      sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w), bf16x2_t{(__bf16)1.f, (__bf16)1.f}, sum, false);
+    return w;
+  }
+  static __device__ __forceinline__ f32x16 mfma_k(u32x4 k, u32x4 q, f32x16 s) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, k), __builtin_bit_cast(bf16x8_t, q), s, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma_v(u32x4 v, u32x4 p, f32x16 o) {
+    if constexpr (F8)
+      return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, v), __builtin_bit_cast(f16x8_t, p), o, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, p), o, 0, 0, 0);
+  }
+  // What brings a row's results to the reference of the waves' path: weights 2^(c (s - ref) + Own::kUp).
+  static __device__ __forceinline__ float adjust(float c, const Row& r) {
+    return r.ref == -INFINITY ? pow2(Own::kUp - kUp) : pow2(Own::kUp - (fmaf(r.ref, c, r.bias) - r.fine));
+  }
 };
 
-// What the items of a group's shared tokens, or of a request's own, are.
-struct Line {
-  uint32_t q;        // query rows per key head
-  uint32_t units;
-  uint32_t places;   // on its line, all items
+// A group's shared tokens, or a request's own: query rows per key head, and units (of 64 tokens, of
+// UT).
+struct Part {
+  uint32_t q, units;
+  bool wide;   // on the workgroups' line
 };
+constexpr uint32_t kBroken = 0x80000000u;   // in place of what a row sees
 
 __device__ __forceinline__ uint32_t pow2_above(uint32_t x) { return x <= 1 ? 1u : 1u << (32 - __clz((int)(x - 1))); }
 
+// Places on the workgroups' line: for each head the items of QW rows, then that of what is left.
 template <int D, bool F8>
-__device__ __forceinline__ Line line_w(uint32_t q, uint32_t shared, uint32_t hkv) {   // q > QT
+__device__ __forceinline__ uint32_t places_w(const Part& p, uint32_t hkv) {
   using A = Shared<D, F8>;
-  const uint32_t full = q / A::QW, rest = q - full * A::QW;
-  Line l = {q, shared, hkv * full * (A::kLeadW + shared * A::cost(A::NW))};
-  if (rest) l.places += hkv * (A::kLeadW + shared * A::cost((rest + A::QT - 1) / A::QT));
-  return l;
-}
-template <int D, bool F8>
-__device__ __forceinline__ Line line_v(uint32_t q, uint32_t units, uint32_t hkv) {
-  using A = Shared<D, F8>;
-  return Line{q, units, units ? hkv * ((q + A::QT - 1) / A::QT) * (A::kLeadV + units) : 0u};
+  const uint32_t full = p.q / A::QW, rest = p.q - full * A::QW;
+  return hkv * (full * (A::kLeadW + p.units * A::cost(A::NW)) +
+                (rest ? A::kLeadW + p.units * A::cost((rest + A::RT - 1) / A::RT) : 0u));
 }
 
+// A group's shared tokens: units of 64 tokens for workgroups, of UT for waves.
+template <int D, bool F8>
+__device__ __forceinline__ Part part_shared(const SharedArgs& a, uint32_t rows, uint32_t shared) {
+  using A = Shared<D, F8>;
+  const uint32_t q = rows * a.group;
+  const bool wide = q > (uint32_t)A::QT && shared;
+  return Part{q, wide ? shared : shared * (64 / A::UT), wide};
+}
 // A request's own part: units from the shared ones on.
 template <int D, bool F8>
-__device__ __forceinline__ Line line_own(const SharedArgs& a, int32_t len, uint32_t rows, uint32_t shared) {
+__device__ __forceinline__ Part part_own(const SharedArgs& a, int32_t len, uint32_t rows, uint32_t shared) {
   using A = Shared<D, F8>;
   const bool broken = len < 0 || (uint64_t)len > ((uint64_t)a.max_pages << a.page_shift);
   const uint32_t upto = broken ? 0u : ((uint32_t)len + A::UT - 1) / A::UT, from = shared * (64 / A::UT);
-  return line_v<D, F8>(rows * a.group, rows && upto > from ? upto - from : 0u, a.n_kv_heads);
+  return Part{rows * a.group, rows && upto > from ? upto - from : 0u, false};
 }
+
+// How the items of the waves' line are cut: by the line's equal pieces, an item having a lead and a
+// place per unit, or (shift > 0) each into pieces of 2^shift units, a place each.
+struct Cut {
+  uint32_t shift, lead;
+  __device__ __forceinline__ uint32_t places(uint32_t units) const {   // of one item
+    return shift ? (units + (1u << shift) - 1) >> shift : lead + units;
+  }
+  // units of the places [p0, p1) of an item; none: only its lead
+  __device__ __forceinline__ void units_of(uint32_t units, uint32_t p0, uint32_t p1, uint32_t& ua, uint32_t& ub) const {
+    ua = shift ? p0 << shift : (p0 > lead ? p0 - lead : 0u);
+    ub = shift ? min(p1 << shift, units) : (p1 > lead ? p1 - lead : 0u);
+  }
+  // the places of an item's first and last unit
+  __device__ __forceinline__ void ends(uint32_t units, uint32_t& first, uint32_t& last) const {
+    first = shift ? 0u : lead;
+    last = shift ? (units - 1) >> shift : lead + units - 1;
+  }
+};
+
+// What a worker needs of the group or request at which its piece begins.
+struct First {
+  uint32_t at, start, slots;   // its place in the list, its first place on the line, the slots before it
+  uint32_t row0, rows, shared; // batch rows, shared units of 64 tokens
+  uint32_t lead;               // of a group: the request through whose table row the shared tokens are read
+  int32_t len;                 // of a request
+};
 
 template <int D, bool F8>
 __global__ __launch_bounds__((Shared<D, F8>::T)) void k_shared(SharedArgs a) {
@@ -81,76 +172,51 @@ __global__ __launch_bounds__((Shared<D, F8>::T)) void k_shared(SharedArgs a) {
   using Own = typename A::Own;
   constexpr int NW = A::NW, NT = A::NT, T = A::T, KS = A::KS, DT = A::DT, UT = A::UT;
   constexpr uint32_t kMaxReq = W12_MAX_REQ;
-  constexpr uint32_t kBuf = 2 * A::kStep > 3 * 4 * (kMaxReq + 1) ? 2 * A::kStep : 3 * 4 * (kMaxReq + 1);
+  constexpr uint32_t kTables = 24 * (kMaxReq + 1), kBuf = 2 * A::kStep > kTables ? 2 * A::kStep : kTables;
   __shared__ __attribute__((aligned(16))) uint8_t s_buf[kBuf];
   __shared__ uint32_t s_from[kMaxReq];   // per request the units of 64 tokens its group shares
-  __shared__ uint32_t s_w[6][NW];
-  __shared__ uint32_t s_spoil[2][2 * A::SU];
-  __shared__ struct { uint32_t at, start, rows; } s_first[1 + NW];
+  __shared__ uint32_t s_w[5][NW];
+  __shared__ First s_first[1 + NW];
   const int tid = threadIdx.x, lane = tid & 63;
   const uint32_t wave = uni(tid >> 6), b = blockIdx.x;
   const uint32_t hkv = a.n_kv_heads, n_req = a.n_req, n_grp = a.n_grp;
+  // Workgroups of one XCD (b modulo 8) are neighbours on the lines: they read the same heads, and the
+  // tiles of query rows that read the same tokens find them in the L2 that they share.
+  const uint32_t at_line = a.grid % 8 ? b : (b & 7) * (a.grid >> 3) + (b >> 3);
 
-  // ---- what the groups share: the least that any of their rows sees
+  // ---- the tables in LDS, and what the groups share: the least that any of their rows sees
+  // (Every phase is a short loop: what the kernel executes once it has to fetch first.)
+  uint32_t* const s_off = reinterpret_cast<uint32_t*>(s_buf);      // [n_grp + 1]
+  uint32_t* const s_req = s_off + kMaxReq + 1;                     // [n_req + 1]
+  int32_t* const s_len = reinterpret_cast<int32_t*>(s_req + kMaxReq + 1);
+  int32_t* const s_min = s_len + kMaxReq;
+  uint32_t* const s_cnt = reinterpret_cast<uint32_t*>(s_min + kMaxReq);
+  uint32_t* const s_lead = s_cnt + kMaxReq;
+  auto usable = [&](int32_t len) { return len >= 0 && (uint64_t)len <= ((uint64_t)a.max_pages << a.page_shift); };
+  uint32_t* const rec_r = reinterpret_cast<uint32_t*>(a.ws + kSharedReq);
+  uint32_t* const rec_g = reinterpret_cast<uint32_t*>(a.ws + kSharedGrp);
+  u32x2* const rec_row = reinterpret_cast<u32x2*>(a.ws + kSharedRow);
   bool bad = false;
-  {
-    uint32_t* const s_off = reinterpret_cast<uint32_t*>(s_buf);   // [n_grp + 1]
-    int32_t* const s_min = reinterpret_cast<int32_t*>(s_off + kMaxReq + 1);
-    uint32_t* const s_cnt = reinterpret_cast<uint32_t*>(s_min + kMaxReq);
-    for (uint32_t g = tid; g <= n_grp; g += T) {
-      const int32_t o = a.grp_off[g], next = g < n_grp ? a.grp_off[g + 1] : o;
-      bad |= o < 0 || next < o || (g == 0 && o != 0) || (g == n_grp && o != (int32_t)n_req);
-      s_off[g] = (uint32_t)o;
-      if (g < n_grp) {
-        s_min[g] = a.grp_len[g];
-        s_cnt[g] = 0;
+#pragma nounroll
+  for (uint32_t i = tid; i <= max(n_grp, n_req); i += T) {
+    if (i <= n_grp) {
+      const int32_t o = a.grp_off[i], next = i < n_grp ? a.grp_off[i + 1] : (int32_t)n_req;
+      bad |= next < o || (i == 0 && o != 0) || (i == n_grp && o != next);
+      s_off[i] = (uint32_t)o;
+      if (i < n_grp) {
+        s_min[i] = a.grp_len[i];
+        s_cnt[i] = 0;
+        s_lead[i] = ~0u;
       }
     }
-    bad = __syncthreads_or(bad);
-    for (uint32_t r = tid; r < n_req && !bad; r += T) {
-      const int32_t r0 = a.req_off[r], r1 = a.req_off[r + 1], len = a.kv_len[r];
-      const uint32_t g = segment(s_off, n_grp, r);
-      s_from[r] = g;
-      if (r1 > r0 && len >= 0 && (uint64_t)len <= ((uint64_t)a.max_pages << a.page_shift)) {
-        atomicMin(&s_min[g], len - (r1 - r0) + 1);
-        atomicAdd(&s_cnt[g], 1u);
-      }
-    }
-    __syncthreads();
-    for (uint32_t r = tid; r < n_req && !bad; r += T) {
-      const uint32_t g = s_from[r];
-      s_from[r] = s_cnt[g] > 1 && s_min[g] > 0 ? (uint32_t)s_min[g] / 64 : 0u;
-    }
-    __syncthreads();
-  }
-
-  // ---- the lines, and this workgroup's and its waves' pieces of them
-  const uint32_t per_g = (n_grp + T - 1) / T, per_r = (n_req + T - 1) / T;
-  auto grp_line = [&](uint32_t g, uint32_t& rows, bool& wide) {   // (without shared tokens: no places)
-    const uint32_t g0 = (uint32_t)a.grp_off[g], g1 = (uint32_t)a.grp_off[g + 1];
-    const uint32_t shared = g1 > g0 ? s_from[g0] : 0u;
-    rows = (uint32_t)(a.req_off[g1] - a.req_off[g0]);
-    const uint32_t q = rows * a.group;
-    wide = q > (uint32_t)A::QT;
-    if (!shared) return Line{q, 0, 0};
-    return wide ? line_w<D, F8>(q, shared, hkv) : line_v<D, F8>(q, shared * (64 / UT), hkv);
-  };
-  auto own_line = [&](uint32_t r) {
-    const uint32_t rows = (uint32_t)(a.req_off[r + 1] - a.req_off[r]);
-    return line_own<D, F8>(a, a.kv_len[r], rows, s_from[r]);
-  };
-  uint32_t sum[6] = {0, 0, 0, 0, 0, 0};   // places and rows: workgroups' line, waves' groups, requests
-  if (!bad) {
-    for (uint32_t i = 0; i < per_r; ++i) {
-      const uint32_t r = tid * per_r + i;
-      if (r < n_req) {
-        const int32_t r0 = a.req_off[r], r1 = a.req_off[r + 1];
-        bad |= r0 < 0 || r1 < r0 || r1 > (int32_t)a.m;
-      }
+    if (i <= n_req) {
+      const int32_t o = a.req_off[i], next = i < n_req ? a.req_off[i + 1] : o;
+      bad |= o < 0 || next < o || next > (int32_t)a.m;
+      s_req[i] = (uint32_t)o;
+      if (i < n_req) s_len[i] = a.kv_len[i];
     }
   }
-  bad = __syncthreads_or(bad);
-  if (bad) {   // no request table, or no groups: NaN everywhere
+  if (__syncthreads_or(bad)) {   // no request table, or no groups: NaN everywhere
     const uint64_t all = (uint64_t)a.m * a.n_heads * D;
     for (uint64_t i = (uint64_t)b * T + tid; i < all; i += (uint64_t)a.grid * T) {
       const uint64_t row = i / (a.n_heads * D);
@@ -159,122 +225,145 @@ __global__ __launch_bounds__((Shared<D, F8>::T)) void k_shared(SharedArgs a) {
     if (b == 0 && tid == 0) *reinterpret_cast<uint32_t*>(a.ws) = 0u;   // nothing to join
     return;
   }
-  for (uint32_t i = 0; i < per_g; ++i) {
-    const uint32_t g = tid * per_g + i;
-    if (g < n_grp) {
-      uint32_t rows;
-      bool wide;
-      const Line l = grp_line(g, rows, wide);
-      sum[wide ? 0 : 2] += l.places;
-      sum[wide ? 1 : 3] += l.places ? hkv * l.q : 0u;
+#pragma nounroll
+  for (uint32_t r = tid; r < n_req; r += T) {
+    const uint32_t g = segment(s_off, n_grp, r), rows = s_req[r + 1] - s_req[r];
+    s_from[r] = g;
+    if (rows && usable(s_len[r])) {
+      atomicMin(&s_min[g], s_len[r] - (int32_t)rows + 1);
+      atomicAdd(&s_cnt[g], 1u);
+      atomicMin(&s_lead[g], r);
     }
   }
-  for (uint32_t i = 0; i < per_r; ++i) {
-    const uint32_t r = tid * per_r + i;
-    if (r < n_req) {
-      const Line l = own_line(r);
-      sum[4] += l.places;
-      sum[5] += l.places ? hkv * l.q : 0u;
+  __syncthreads();
+#pragma nounroll
+  for (uint32_t r = tid; r < n_req; r += T) {
+    const uint32_t g = s_from[r];
+    s_from[r] = s_cnt[g] > 1 && s_min[g] > 0 ? (uint32_t)s_min[g] / 64 : 0u;
+    if (b == 0)   // (what the join needs: the first workgroup leaves it)
+      for (uint32_t row = s_req[r]; row < s_req[r + 1]; ++row) rec_row[row] = u32x2{r, g};
+  }
+  __syncthreads();
+
+  // ---- the lines, and this workgroup's and its waves' pieces of them
+  const uint32_t n_all = n_grp + n_req, per_t = (n_all + T - 1) / T;   // groups, then requests
+  auto part = [&](uint32_t e, First& f) {
+    const bool own = e >= n_grp;
+    const uint32_t r = own ? e - n_grp : s_off[e], r1 = own ? r + 1 : s_off[e + 1];
+    f.at = e;
+    f.row0 = s_req[r];
+    f.rows = s_req[r1] - f.row0;
+    f.shared = r1 > r ? s_from[r] : 0u;
+    f.lead = own ? 0u : s_lead[e];
+    f.len = own ? s_len[r] : 0;
+    return own ? part_own<D, F8>(a, f.len, f.rows, f.shared) : part_shared<D, F8>(a, f.rows, f.shared);
+  };
+  // places and slots on the workgroups' line; units, items and slots on the waves'
+  uint32_t sum[5] = {0, 0, 0, 0, 0};
+#pragma nounroll
+  for (uint32_t i = 0; i < per_t; ++i) {
+    const uint32_t e = tid * per_t + i;
+    if (e >= n_all) break;
+    First f;
+    const Part p = part(e, f);
+    const uint32_t items = hkv * ((p.q + A::QT - 1) / A::QT), slots = p.units ? hkv * p.q : 0u;
+    if (p.wide) {
+      sum[0] += places_w<D, F8>(p, hkv);
+      sum[1] += slots;
+    } else if (p.units) {
+      sum[2] += items * p.units;
+      sum[3] += items;
+      sum[4] += slots;
     }
   }
-  uint32_t upto[6], total[6];
+  uint32_t upto[5], total[5];
 #pragma unroll
-  for (int k = 0; k < 6; ++k) {
+  for (int k = 0; k < 5; ++k) {   // sums before this thread, and of all
     upto[k] = wave_scan(sum[k]);
     if (lane == 63) s_w[k][wave] = upto[k];
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 6; ++k) {
-    total[k] = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const uint32_t v = uni(s_w[k][w]);
-      if (w < (int)wave) upto[k] += v;
-      total[k] += v;
-    }
-    upto[k] -= sum[k];   // before this thread's
+  for (int k = 0; k < 5; ++k) {
+    uint32_t v = lane < NW ? s_w[k][lane] : 0u;
+    const uint32_t before = wave_scan(lane < (int)wave ? v : 0u);
+    total[k] = (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(v), 63);
+    upto[k] += (uint32_t)__builtin_amdgcn_readlane((int)before, 63) - sum[k];
   }
-  upto[4] += total[2];
-  upto[5] += total[3];
-  const uint32_t all_w = total[0], all_v = total[2] + total[4];
+  const uint32_t all_w = total[0];
   // (pieces of a unit at least, so that every piece between an item's first and last unit has one)
   const uint32_t per_w = max((all_w + a.grid - 1) / a.grid, 2 * A::cost(NW));
-  const uint32_t per_v = max((all_v + a.grid * NW - 1) / (a.grid * NW), A::kLeastV);
-  uint32_t* const rec_r = reinterpret_cast<uint32_t*>(a.ws + kSharedReq);
-  uint32_t* const rec_g = reinterpret_cast<uint32_t*>(a.ws + kSharedGrp);
-  u32x2* const rec_row = reinterpret_cast<u32x2*>(a.ws + kSharedRow);
-  if (b == 0) {
-    if (tid == 0) {
-      uint32_t* const h = reinterpret_cast<uint32_t*>(a.ws);
-      h[1] = per_w;
-      h[2] = per_v;
-      h[0] = 1u;
-    }
-    const uint32_t row_0 = (uint32_t)a.req_off[0], row_n = (uint32_t)a.req_off[n_req];
-    for (uint32_t i = tid; i < row_0; i += T) rec_row[i] = u32x2{~0u, ~0u};
-    for (uint32_t i = row_n + tid; i < a.m; i += T) rec_row[i] = u32x2{~0u, ~0u};
+  // The waves' line: equal pieces, wherever they cut the items; or, where there are so many waves that each
+  // may have a piece of its own of few units, the items in pieces of two, four, eight or sixteen units.
+  const uint32_t waves = a.grid * NW;
+  Cut cut = {0u, A::kLeadV};
+  if (2 * total[3] <= waves) {
+    uint32_t shift = 1;
+    while (shift < 5 && (total[2] >> shift) + total[3] > waves) ++shift;
+    cut.shift = shift < 5 ? shift : 0u;
   }
-  // the records for the join, each by one workgroup, and where the pieces begin
-  auto starts = [&](uint32_t at, uint32_t start, uint32_t places, uint32_t rows, bool line) {
-    if (line) {
-      const uint32_t p = b * per_w;
-      if (p >= start && p < start + places) s_first[0] = {at, start, rows};
+  uint32_t all_v, start_v;
+  if (cut.shift) {
+    uint32_t pieces = 0;
+#pragma nounroll
+    for (uint32_t i = 0; i < per_t; ++i) {
+      const uint32_t e = tid * per_t + i;
+      if (e >= n_all) break;
+      First f;
+      const Part p = part(e, f);
+      if (!p.wide) pieces += hkv * ((p.q + A::QT - 1) / A::QT) * cut.places(p.units);
+    }
+    start_v = wave_scan(pieces);
+    __syncthreads();
+    if (lane == 63) s_w[0][wave] = start_v;
+    __syncthreads();
+    const uint32_t v = lane < NW ? s_w[0][lane] : 0u, before = wave_scan(lane < (int)wave ? v : 0u);
+    all_v = (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(v), 63);
+    start_v += (uint32_t)__builtin_amdgcn_readlane((int)before, 63) - pieces;
+  } else {
+    all_v = total[2] + A::kLeadV * total[3];
+    start_v = upto[2] + A::kLeadV * upto[3];
+  }
+  const uint32_t per_v = cut.shift ? 1u : max((all_v + waves - 1) / waves, 1u);
+  // (pieces of few units go to as many workgroups as there are)
+  const uint32_t next_wave = cut.shift ? a.grid : 1u, first_wave = cut.shift ? at_line : at_line * NW;
+  const uint32_t wp = first_wave + wave * next_wave;   // this wave's place among all
+#pragma nounroll
+  for (uint32_t i = 0; i < per_t; ++i) {
+    const uint32_t e = tid * per_t + i;
+    if (e >= n_all) break;
+    First f;
+    const Part p = part(e, f);
+    const uint32_t slots = p.units ? hkv * p.q : 0u;
+    uint32_t places;
+    if (p.wide) {
+      places = places_w<D, F8>(p, hkv);
+      f.start = upto[0];
+      f.slots = upto[1];
+      upto[0] += places;
+      upto[1] += slots;
+      if (at_line * per_w - f.start < places) s_first[0] = f;
     } else {
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const uint32_t p = (b * NW + w) * per_v;
-        if (p >= start && p < start + places) s_first[1 + w] = {at, start, rows};
-      }
+      places = p.units ? hkv * ((p.q + A::QT - 1) / A::QT) * cut.places(p.units) : 0u;
+      f.start = start_v;
+      f.slots = upto[4];
+      start_v += places;
+      upto[4] += slots;
+#pragma nounroll
+      for (uint32_t w = 0; w < (uint32_t)NW; ++w)
+        if ((first_wave + w * next_wave) * per_v - f.start < places) s_first[1 + w] = f;
     }
-  };
-  for (uint32_t i = 0; i < per_g; ++i) {
-    const uint32_t g = tid * per_g + i;
-    if (g < n_grp) {
-      uint32_t rows;
-      bool wide;
-      const Line l = grp_line(g, rows, wide);
-      const int k = wide ? 0 : 2;
-      starts(g, upto[k], l.places, upto[k + 1], wide);
-      if (g % a.grid == b) {
-        uint32_t* const c = rec_g + kRecWords * g;
-        c[0] = (uint32_t)a.req_off[a.grp_off[g]];
-        c[1] = l.q;
-        c[2] = l.places ? l.units : 0u;
-        c[3] = upto[k];
-        c[4] = upto[k + 1];
-        c[5] = wide;
-      }
-      upto[k] += l.places;
-      upto[k + 1] += l.places ? hkv * l.q : 0u;
+    if (b == 0) {
+      u32x4* const c = reinterpret_cast<u32x4*>(e < n_grp ? rec_g + kRecWords * e : rec_r + kRecWords * (e - n_grp));
+      c[0] = u32x4{f.row0, p.q, p.units, f.start};
+      // (of a request also what its first row sees)
+      c[1] = u32x4{f.slots, e < n_grp ? (uint32_t)p.wide : (usable(f.len) ? (uint32_t)(f.len - (int32_t)f.rows + 1) : kBroken), 0u, 0u};
     }
   }
-  for (uint32_t i = 0; i < per_r; ++i) {
-    const uint32_t r = tid * per_r + i;
-    if (r < n_req) {
-      const Line l = own_line(r);
-      starts(n_grp + r, upto[4], l.places, upto[5], false);
-      if (r % a.grid == b) {
-        const uint32_t r0 = (uint32_t)a.req_off[r], r1 = (uint32_t)a.req_off[r + 1];
-        const int32_t len = a.kv_len[r];
-        uint32_t* const c = rec_r + kRecWords * r;
-        c[0] = r0;
-        c[1] = l.q;
-        c[2] = l.units;
-        c[3] = upto[4];
-        c[4] = upto[5];
-        const bool broken = len < 0 || (uint64_t)len > ((uint64_t)a.max_pages << a.page_shift);
-        c[5] = broken ? 0x80000000u : (uint32_t)(len - (int32_t)(r1 - r0) + 1);   // what its first row sees
-        uint32_t lo = 0, hi = n_grp;   // its group: the last that begins at or before it and is not empty
-        while (hi - lo > 1) {
-          const uint32_t mid = (lo + hi) >> 1;
-          if ((uint32_t)a.grp_off[mid] <= r) lo = mid; else hi = mid;
-        }
-        for (uint32_t row = r0; row < r1; ++row) rec_row[row] = u32x2{r, lo};
-      }
-      upto[4] += l.places;
-      upto[5] += l.places ? hkv * l.q : 0u;
-    }
+  if (b == 0) {
+    if (tid == 0) *reinterpret_cast<u32x4*>(a.ws) = u32x4{1u, per_w, per_v, cut.shift};
+    for (uint32_t i = tid; i < s_req[0]; i += T) rec_row[i] = u32x2{~0u, ~0u};
+    for (uint32_t i = s_req[n_req] + tid; i < a.m; i += T) rec_row[i] = u32x2{~0u, ~0u};
   }
   __syncthreads();
 
@@ -314,310 +403,366 @@ __global__ __launch_bounds__((Shared<D, F8>::T)) void k_shared(SharedArgs a) {
       }
     }
   };
-  // the table row that a group's shared tokens are read through: its first request with tokens
-  auto lead_of = [&](uint32_t g0) {
-    for (uint32_t r = g0;; ++r) {
-      const int32_t len = uniform_load(a.kv_len, r);
-      if (uniform_load(a.req_off, r + 1) > uniform_load(a.req_off, r) && len >= 0 &&
-          (uint64_t)len <= ((uint64_t)a.max_pages << a.page_shift))
-        return r;
-    }
+  // a group's or request's values as the piece's first one has them in LDS
+  auto first_of = [&](const First& s) {
+    return First{uni(s.at), uni(s.start), uni(s.slots), uni(s.row0), uni(s.rows), uni(s.shared), uni(s.lead), (int32_t)uni((uint32_t)s.len)};
+  };
+  auto load_at = [&](First& f) {
+    const bool own = f.at >= n_grp;
+    const uint32_t r = own ? f.at - n_grp : (uint32_t)uniform_load(a.grp_off, f.at);
+    const uint32_t r1 = own ? r + 1 : (uint32_t)uniform_load(a.grp_off, f.at + 1);
+    f.row0 = (uint32_t)uniform_load(a.req_off, r);
+    f.rows = (uint32_t)uniform_load(a.req_off, r1) - f.row0;
+    f.shared = r1 > r ? uni(s_from[r]) : 0u;
+    f.len = own ? uniform_load(a.kv_len, r) : 0;
+    f.lead = r;
+    if (!own && f.shared)   // the group's first request with rows and a length
+      while (uniform_load(a.req_off, f.lead + 1) == uniform_load(a.req_off, f.lead) || !usable(uniform_load(a.kv_len, f.lead))) ++f.lead;
   };
 
   // ---- the workgroup's piece: shared tokens of many rows, through LDS
-  if (b * per_w < all_w) {
-    uint32_t pos = b * per_w;
+  if (at_line * per_w < all_w) {
+    uint32_t pos = at_line * per_w;
     const uint32_t end = min(pos + per_w, all_w);
-    uint32_t g = uni(s_first[0].at), start = uni(s_first[0].start), before = uni(s_first[0].rows);
+    First f = first_of(s_first[0]);
     while (pos < end) {
-      const uint32_t g0 = (uint32_t)uniform_load(a.grp_off, g), g1 = (uint32_t)uniform_load(a.grp_off, g + 1);
-      const uint32_t shared = g1 > g0 ? uni(s_from[g0]) : 0u;
-      const uint32_t row0 = (uint32_t)uniform_load(a.req_off, g0);
-      const uint32_t nq_all = ((uint32_t)uniform_load(a.req_off, g1) - row0) * a.group;
-      const Line l = shared && nq_all > (uint32_t)A::QT ? line_w<D, F8>(nq_all, shared, hkv) : Line{nq_all, 0, 0};
-      if (pos >= start + l.places) {
-        start += l.places;
-        before += l.places ? hkv * nq_all : 0u;
-        ++g;
+      const Part l = part_shared<D, F8>(a, f.rows, f.shared);
+      const uint32_t nq_all = l.q, shared = l.units, row0 = f.row0;
+      const uint32_t full = nq_all / A::QW, one = A::kLeadW + shared * A::cost(NW);
+      const uint32_t rest = nq_all - full * A::QW, c_rest = A::cost((rest + A::RT - 1) / A::RT);
+      const uint32_t per_head = full * one + (rest ? A::kLeadW + shared * c_rest : 0u);
+      if (!l.wide || pos >= f.start + hkv * per_head) {
+        if (l.wide) {
+          f.start += hkv * per_head;
+          f.slots += hkv * nq_all;
+        }
+        do {
+          ++f.at;
+          load_at(f);
+        } while (f.rows == 0 || f.shared == 0);
         continue;
       }
-      // the item: tiles of QW rows, all heads of one after the other, then what is left
-      const uint32_t full = nq_all / A::QW, one = A::kLeadW + shared * A::cost(NW);
-      uint32_t tile, head, first, len, c, nq;
-      if (pos - start < full * hkv * one) {
-        const uint32_t item = (pos - start) / one;
-        tile = item / hkv;
-        head = item - tile * hkv;
-        first = start + item * one;
-        len = one;
-        c = A::cost(NW);
-        nq = A::QW;
-      } else {
-        tile = full;
-        nq = nq_all - full * A::QW;
-        c = A::cost((nq + A::QT - 1) / A::QT);
-        len = A::kLeadW + shared * c;
-        head = (pos - start - full * hkv * one) / len;
-        first = start + full * hkv * one + head * len;
-      }
-      const uint32_t la = pos - first, n_here = min(len - la, end - pos);
+      // the item: a tile of QW rows, or what is left, of a head
+      const uint32_t head = (pos - f.start) / per_head, here = f.start + head * per_head;
+      const uint32_t tile = min((pos - here) / one, full);
+      const bool last = tile == full;
+      const uint32_t first = here + tile * one, c = last ? c_rest : A::cost(NW), nq = last ? rest : (uint32_t)A::QW;
+      const uint32_t len = A::kLeadW + shared * c, la = pos - first, n_here = min(len - la, end - pos);
       pos += n_here;
       if (la + n_here <= A::kLeadW) continue;   // only its lead falls into this piece
       const uint32_t ua = la > A::kLeadW ? (la - A::kLeadW + c - 1) / c : 0u;
       const uint32_t ub = (la + n_here - A::kLeadW + c - 1) / c;
       if (ua >= ub) continue;
-      const uint64_t slot = before + tile * A::QW * hkv + head * nq + (uint64_t)A::QW * b;
-      const uint64_t trow = (uint64_t)lead_of(g0) * a.max_pages;
+      const uint64_t slot = f.slots + head * nq_all + tile * A::QW + (uint64_t)A::QW * at_line;
+      const uint64_t trow = (uint64_t)f.lead * a.max_pages;
       // waves to row tiles, and those that are left to tokens
-      const uint32_t tiles = pow2_above((nq + A::QT - 1) / A::QT), sub = wave & (tiles - 1), turn = wave / tiles;
+      const uint32_t tiles = pow2_above((nq + A::RT - 1) / A::RT), sub = wave & (tiles - 1), turn = wave / tiles;
       const uint32_t turns = min((uint32_t)NW / tiles, 2u * A::SU);
-      const uint32_t nw = turn < turns && nq > sub * A::QT ? min((uint32_t)A::QT, nq - sub * A::QT) : 0u;
-      const uint32_t q0 = tile * A::QW + sub * A::QT;
-      bf16x8_t qf[NT][KS];
-      load_q(row0, head, nw ? q0 : 0u, nw, qf);
-      f32x4 o[NT][DT];
-      float top[NT], sum[NT];
+      const uint32_t nw = turn < turns && nq > sub * A::RT ? min((uint32_t)A::RT, nq - sub * A::RT) : 0u;
+      const uint32_t r16 = lane & 15, g16 = lane >> 4, r32 = lane & 31, h32 = lane >> 5;
+      u32x4 qf[A::KR];   // of query row r32: dimensions 16 s + 8 h32 .. + 7 of step s
+      {
+        const uint32_t qi = tile * A::QW + (r32 < nw ? sub * A::RT + r32 : 0u);
+        const uint32_t row = per_group(qi), gq = qi - row * a.group;
+        const uint16_t* const p = a.q + (uint64_t)(row0 + row) * a.q_stride + (uint64_t)(head * a.group + gq) * D + 8 * h32;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        top[nt] = -INFINITY;
-        sum[nt] = 0.f;
+        for (int k = 0; k < A::KR; ++k) {
+          qf[k] = *reinterpret_cast<const u32x4*>(p + 16 * k);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[nt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int i = 0; i < 4; ++i) qf[k][i] ^= flip;
+        }
       }
-      // fetching: a wave takes K or V of a span of 32 tokens (BF16), or of a unit half of K's tokens or
-      // of V's dimensions (E4M3, decoded on the way into LDS)
-      u32x4 st[A::NL];
-      uint32_t ids[F8 ? 4 : 2] = {}, spoils = 0;
-      const uint32_t f_unit = F8 ? wave >> 2 : wave >> 2, f_half = F8 ? wave & 1 : (wave >> 1) & 1;
-      const bool f_v = F8 ? (wave >> 1) & 1 : wave & 1;
-      const uint32_t r16 = lane & 15, g16 = lane >> 4;
-      auto pages_of = [&](uint32_t u0) {   // requested a step before they are needed
-        const uint32_t u = u0 + f_unit;
-        if (u >= ub) return;
+      f32x16 o[A::DR];   // of query row r32: dimension 32 d + 8 j + 4 h32 + i in place 4 j + i
+      typename A::Row soft = A::row();
 #pragma unroll
-        for (int j = 0; j < (F8 ? 4 : 2); ++j)
-          ids[j] = (uint32_t)uniform_load(a.table, trow + ((u * 64 + (F8 ? 16 * j : 32 * f_half + 16 * j)) >> a.page_shift));
+      for (int d = 0; d < A::DR; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+      // Operands in LDS, 1 KB each, in the lanes' own order.  K of a span of 32 tokens: per 16 dimensions, lane
+      // (row r32, half h32) 8 of them; row 8 j + 4 h + i is token 16 (j / 2) + 8 h + 4 (j % 2) + i, so that a lane's
+      // scores, as the matrix core leaves them (rows 8 j + 4 h32 + i), are 8 consecutive tokens for each of
+      // the two steps of the second product.  V: per 32 dimensions and 16 tokens, lane (dimension r32, half h32) 8
+      // of those.
+      // Fetching: of every step a wave takes K or V of a span: NL loads, half of them from each of the span's two
+      // groups of 16 tokens, that lie in one page: 64 bytes of 16 keys, or 16 tokens of 32 (BF16) or 64
+      // dimensions.  Their addresses are a base, the same for the wave, and a place of the lane that never
+      // changes.  Units past the piece are fetched as its last one, so that nothing around the loads
+      // depends on where the piece ends and the compiler waits for them where they are used.
+      const uint32_t f_unit = wave >> 2, f_half = (wave >> 1) & 1;
+      const bool f_v = wave & 1;
+      constexpr uint32_t es = F8 ? 1 : 2;
+      const uint32_t f_dist = f_v ? 64u << a.page_shift : 64u, f_place = f_v ? es : es * D;
+      const uint32_t k_tok = 8 * ((r16 >> 2) & 1) + 4 * (r16 >> 3) + (r16 & 3);   // of row r16 among 16 tokens
+      const uint32_t f_lane = f_v ? (F8 ? (uint32_t)lane << a.page_shift : ((r32 << a.page_shift) + 8 * h32) * 2)
+                                  : k_tok * D * es + 16 * g16;
+      const uint8_t* const f_cache = f_v ? a.vc : a.kc;
+      u32x4 st[A::NL];
+      uint32_t id_0 = 0, id_1 = 0, spoils = 0;
+      auto pages_of = [&](uint32_t u0) {   // requested a step before they are needed
+        const uint32_t t0 = min(u0 + f_unit, ub - 1) * 64 + 32 * f_half;
+        id_0 = (uint32_t)uniform_load(a.table, trow + (t0 >> a.page_shift));
+        id_1 = (uint32_t)uniform_load(a.table, trow + ((t0 + 16) >> a.page_shift));
       };
       auto fetch = [&](uint32_t u0) {
-        const uint32_t u = u0 + f_unit;
-        if (u >= ub) return;
-        spoils = 0;
+        const uint32_t t0 = min(u0 + f_unit, ub - 1) * 64 + 32 * f_half;
+        const bool ok_0 = id_0 < a.n_pages, ok_1 = id_1 < a.n_pages;
+        spoils = (ok_0 ? 0u : 1u) | (ok_1 ? 0u : 2u);   // (of values too: all bits set is NaN in either type)
+        const uint64_t page = ((uint64_t)D * es) << a.page_shift;
+        const uint8_t* const p = f_cache + ((uint64_t)(ok_0 ? id_0 : 0u) * hkv + head) * page + (uint64_t)(t0 & mask) * f_place;
+        const uint8_t* const q = f_cache + ((uint64_t)(ok_1 ? id_1 : 0u) * hkv + head) * page + (uint64_t)((t0 + 16) & mask) * f_place;
 #pragma unroll
-        for (int j = 0; j < (F8 ? 4 : 2); ++j) {
-          const bool ok = ids[j] < a.n_pages;
-          spoils |= ok ? 0u : 1u << j;
-          ids[j] = ok ? ids[j] : 0u;
-        }
-        if constexpr (F8) {
-          if (f_v) {
-            const uint32_t lo = (g16 & 1) ? ids[1] : ids[0], hi = (g16 & 1) ? ids[3] : ids[2];
-            const uint32_t id = (g16 & 2) ? hi : lo, place = (u * 64 + 16 * g16) & mask;
-            const uint8_t* p = a.vc + ((((uint64_t)id * hkv + head) * D + f_half * (D / 2) + r16) << a.page_shift) + place;
-            const uint32_t next = 16u << a.page_shift;
+        for (int i = 0; i < A::NL / 2; ++i) st[i] = Own::load16(p + i * f_dist + f_lane);
 #pragma unroll
-            for (int i = 0; i < A::NL; ++i) st[i] = Own::load16(p + (uint64_t)i * next);
-          } else {
-            const uint32_t lo = (r16 & 4) ? ids[1] : ids[0], hi = (r16 & 4) ? ids[3] : ids[2];
-            const uint32_t id = (r16 & 8) ? hi : lo;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const uint32_t place = (u * 64 + 16 * (r16 >> 2) + 4 * (2 * f_half + t) + (r16 & 3)) & mask;
-              const uint8_t* p = a.kc + ((((uint64_t)id * hkv + head) << a.page_shift) + place) * D + 16 * g16;
-#pragma unroll
-              for (int i = 0; i < A::NL / 2; ++i) st[t * (A::NL / 2) + i] = Own::load16(p + 64 * i);
-            }
-          }
-        } else {
-          const uint32_t t0 = u * 64 + 32 * f_half;
-          if (f_v) {
-            const uint32_t id = (g16 & 2) ? ids[1] : ids[0], place = (t0 + 8 * g16) & mask;
-            const uint8_t* p = a.vc + (((((uint64_t)id * hkv + head) * D + r16) << a.page_shift) + place) * 2;
-            const uint32_t next = 32u << a.page_shift;
-#pragma unroll
-            for (int i = 0; i < A::NL; ++i) st[i] = Own::load16(p + (uint64_t)i * next);
-          } else {
-            const uint32_t id = (r16 & 8) ? ids[1] : ids[0];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const uint32_t place = (t0 + 8 * (r16 >> 2) + 4 * t + (r16 & 3)) & mask;
-              const uint8_t* p = a.kc + ((((uint64_t)id * hkv + head) << a.page_shift) + place) * (D * 2) + 16 * g16;
-#pragma unroll
-              for (int i = 0; i < KS; ++i) st[t * KS + i] = Own::load16(p + 64 * i);
-            }
-          }
-        }
+        for (int i = 0; i < A::NL / 2; ++i) st[A::NL / 2 + i] = Own::load16(q + i * f_dist + f_lane);
       };
-      auto put = [&](uint32_t u0, uint32_t buf) {
-        if (u0 + f_unit >= ub) return;
-        uint8_t* const step = s_buf + buf * A::kStep + 16 * lane;
-        if constexpr (F8) {
+      // In LDS the second group's keys lie 16 rows on, its values' step one operand; a load's 64 bytes of a key
+      // are 2 (BF16) or 4 operands, its dimensions of V 2 or 4.
+      const uint32_t put_0 = (2 * f_unit + f_half) * 2 * A::kHalf + (f_v ? A::kHalf : 0u) +
+                             (f_v ? (F8 ? (uint32_t)h32 * 2048 + r32 * 16 : 16u * lane)
+                                  : (F8 ? g16 * 1024 : (g16 >> 1) * 1024 + (g16 & 1) * 512) + r16 * 16);
+      const uint32_t put_1 = put_0 + (f_v ? 1024 : 256);
+      auto put = [&](uint32_t buf) {
+        if (spoils) {   // keys in a page that is none: NaN, and so are the scores and the rows
 #pragma unroll
-          for (int i = 0; i < A::NL; ++i) {
+          for (int i = 0; i < A::NL; ++i)
+            if ((spoils >> (i < A::NL / 2 ? 0 : 1)) & 1u) st[i] = u32x4{~0u, ~0u, ~0u, ~0u};
+        }
+#pragma unroll
+        for (int i = 0; i < A::NL; ++i) {
+          uint8_t* const to = s_buf + buf * A::kStep + (i < A::NL / 2 ? put_0 : put_1) + (i % (A::NL / 2)) * (F8 ? 4096 : 2048);
+          if constexpr (F8) {   // 16 dimensions of a token or tokens of a dimension: two operands' halves
             const u32x4 x[1] = {st[i]};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (f_v) {   // tokens 8h .. 8h + 7 of the lane's 16: span h
-                u32x4* const to = reinterpret_cast<u32x4*>(step + (2 * f_unit + h) * 2 * A::kHalf + A::kHalf + (f_half * (DT / 2) + i) * A::kChunk);
-                *to = Own::operand_v(x, h);
-              } else {     // dimensions 8h .. 8h + 7 of the lane's 16: matrix step 2 i + h
-                const int t = i / (A::NL / 2), k = 2 * (i % (A::NL / 2)) + h;
-                u32x4* const to = reinterpret_cast<u32x4*>(step + (2 * f_unit + f_half) * 2 * A::kHalf + (t * KS + k) * A::kChunk);
-                *to = __builtin_bit_cast(u32x4, Own::operand(x, h));
-              }
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<u32x4*>(to + 512 * h) = f_v ? Own::operand_v(x, h) : __builtin_bit_cast(u32x4, Own::operand(x, h));
+          } else {
+            *reinterpret_cast<u32x4*>(to) = st[i];
+          }
+        }
+      };
+      // The products of N spans of 32 tokens, one behind the other so that the matrix core works beside the
+      // softmax: while the weights of a span are formed the next one's scores are, and while its maximum is
+      // taken the values of the one before are summed: K0, K1, V0, K2, V1, K3, V2, V3.  (One after the other, a
+      // wave's products and its softmax take the same time, 0.5 us per 64 tokens each, and the two waves
+      // of a SIMD did not make up for it.)  The operands come through a ring of registers, requested
+      // kRing operands before they are used: a matrix step on one takes 32 cycles, a read among eight
+      // waves' some 200.
+      constexpr int kRing = 8;
+      auto run = [&](auto spans, uint32_t buf, uint32_t span) {
+        constexpr int N = decltype(spans)::value, KR = A::KR, DR = A::DR;
+        const uint8_t* const from = s_buf + buf * A::kStep + span * 2 * A::kHalf + 16 * lane;
+        u32x4 ring[kRing];
+        auto read = [&](int j) {   // operand j of the sequence
+          if (j >= 2 * N * KR) return;
+          const int n = j / KR, c = j % KR;
+          const bool of_v = n == 2 * N - 1 || (n >= 2 && n % 2 == 0);
+          const int sp = n == 2 * N - 1 ? N - 1 : (n < 2 ? n : (n % 2 ? (n + 1) / 2 : (n - 2) / 2));
+          const int at = of_v ? (int)A::kHalf + ((c % DR) * 2 + c / DR) * (int)A::kChunk : c * (int)A::kChunk;   // V: tiles in turn
+          ring[j % kRing] = *reinterpret_cast<const u32x4*>(from + sp * 2 * (int)A::kHalf + at);
+        };
+#pragma unroll
+        for (int j = 0; j < kRing; ++j) read(j);
+        f32x16 even, odd;   // scores of the spans in turn
+        u32x4 p[2];
+        auto score = [&](int i, int c, f32x16& s) {   // step c of span i
+          const int j = (i < 2 ? i : 2 * i - 1) * KR + c;
+          if (c == 0)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) s[x] = 0.f;
+          s = A::mfma_k(ring[j % kRing], qf[c], s);
+          read(j + kRing);
+        };
+        auto value = [&](int i, int c) {
+          const int j = (i == N - 1 ? 2 * N - 1 : 2 * i + 2) * KR + c;
+          o[c % DR] = A::mfma_v(ring[j % kRing], p[c / DR], o[c % DR]);
+          read(j + kRing);
+        };
+#pragma unroll
+        for (int c = 0; c < KR; ++c) {
+          score(0, c, even);
+          fence();
+        }
+        // (the compiler's scheduler is told to deal the products, the reads and the rest out evenly)
+        auto one = [&](auto index, f32x16& x, f32x16& y) {   // span `index`, its scores and those of the next
+          constexpr int i = decltype(index)::value;
+          fence();
+          float m0 = x[0], m1 = x[1];
+#pragma unroll
+          for (int k = 2; k < 16; k += 4) {
+            m0 = fmaxf(fmaxf(m0, x[k]), x[k + 1]);
+            if (k + 2 < 16) m1 = fmaxf(fmaxf(m1, x[k + 2]), x[k + 3]);
+          }
+#pragma unroll
+          for (int c = 0; c < KR; ++c)
+            if (i) value(i - 1, c);
+          if (i) {
+#pragma unroll
+            for (int c = 0; c < KR; ++c) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
           }
-        } else {
-          uint8_t* const to = step + (2 * f_unit + f_half) * 2 * A::kHalf + (f_v ? A::kHalf : 0u);
+          fence();
+          A::rise(cs, fmaxf(m0, m1), soft, o);
+          float scale = cs, bias = soft.bias;
+          if (__any(soft.fine != 0.f)) {   // scores beyond 2^24
 #pragma unroll
-          for (int i = 0; i < A::NL; ++i) *reinterpret_cast<u32x4*>(to + i * A::kChunk) = st[i];
+            for (int k = 0; k < 16; ++k) x[k] = fmaf(x[k], cs, soft.bias) - soft.fine;
+            scale = 1.f;
+            bias = 0.f;
+          }
+          fence();
+#pragma unroll
+          for (int c = 0; c < KR; ++c)
+            if (i + 1 < N) score(i + 1, c, y);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) p[k >> 2][k & 3] = A::weigh(scale, bias, x[2 * k], x[2 * k + 1], soft.sum);
+          if (i + 1 < N) {
+#pragma unroll
+            for (int c = 0; c < KR; ++c) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x002, 48 / KR, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+          }
+          fence();
+        };
+        one(std::integral_constant<int, 0>{}, even, odd);
+        if constexpr (N > 1) one(std::integral_constant<int, 1>{}, odd, even);
+        if constexpr (N > 2) {
+          one(std::integral_constant<int, 2>{}, even, odd);
+          one(std::integral_constant<int, 3>{}, odd, even);
         }
-        if (!f_v && lane == 0) s_spoil[buf][2 * f_unit + f_half] = spoils;
+#pragma unroll
+        for (int c = 0; c < KR; ++c) {
+          value(N - 1, c);
+          fence();
+        }
       };
-      // the products of NS spans of 32 tokens
-      auto unit = [&](auto spans, uint32_t buf, uint32_t span) {
-        constexpr int NS = decltype(spans)::value;
-        using Part = Tile<D, F8, NT, 32 * NS>;
-        const uint8_t* const from = s_buf + buf * A::kStep + span * 2 * A::kHalf + 16 * lane;
-        f32x4 s[NT][2 * NS];
-#pragma unroll
-        for (int t = 0; t < 2 * NS; ++t) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            const bf16x8_t kk = *reinterpret_cast<const bf16x8_t*>(from + (t / 2) * 2 * A::kHalf + ((t & 1) * KS + i) * A::kChunk);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              s[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, qf[nt][i], s[nt][t], 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < NS; ++k) {
-          const uint32_t spoilt = uni(s_spoil[buf][span + k]);
-          if (spoilt && ((spoilt >> (F8 ? g16 : g16 >> 1)) & 1u)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][2 * k] = s[nt][2 * k + 1] = f32x4{NAN, NAN, NAN, NAN};
-          }
-        }
-        u32x4 p[NT][NS];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) Part::template weights<false>(cs, 0u, s[nt], top[nt], sum[nt], o[nt], p[nt]);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            const u32x4 vv = *reinterpret_cast<const u32x4*>(from + k * 2 * A::kHalf + A::kHalf + d * A::kChunk);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) o[nt][d] = Own::mfma_v(vv, p[nt][k], o[nt][d]);
-          }
-      };
-      __syncthreads();   // the buffers are free
-      pages_of(ua);
-      fetch(ua);
-      pages_of(ua + A::SU);
-      // (a loop for each form of a unit: one loop with both would hold the results twice)
-      auto steps = [&](auto&& work) {
+      // (a loop for each number of spans: one loop with all would hold the results more than once)
+      auto steps = [&](auto spans) {
+        constexpr int N = decltype(spans)::value;
+        __syncthreads();   // the buffers are free
+        pages_of(ua);
+        fetch(ua);
+        pages_of(ua + A::SU);
+        put(0);
+        fetch(ua + A::SU);
+        pages_of(ua + 2 * A::SU);
         uint32_t buf = 0;
-        for (uint32_t u0 = ua; u0 < ub; u0 += A::SU) {
-          put(u0, buf);
-          fetch(u0 + A::SU);
-          pages_of(u0 + 2 * A::SU);
+        auto next = [&](uint32_t u0) {
+          put(buf ^ 1);
+          fetch(u0 + 2 * A::SU);
+          pages_of(u0 + 3 * A::SU);
+        };
+        // While a step is worked on the next goes to the other half of the buffer, before the products in
+        // one half of the waves and behind them in the other, so that the two waves of a SIMD do not want the
+        // same at the same time.
+        uint32_t u0 = ua;
+#pragma nounroll
+        for (; u0 + (N == 4 ? 1 : 0) < ub; u0 += A::SU) {
           __syncthreads();
-          work(u0, buf);
+          if (wave < NW / 2) next(u0);
+          if (nw && (N == 4 || u0 + turn * N / 2 < ub)) run(spans, buf, N == 4 ? 0u : turn * N);
+          if (wave >= NW / 2) next(u0);
           buf ^= 1;
         }
+        if (N == 4 && u0 < ub) {   // the last step's one unit
+          __syncthreads();
+          if (nw) run(std::integral_constant<int, N == 4 ? 2 : N>{}, buf, 0);
+        }
       };
-      if (!nw)
-        steps([](uint32_t, uint32_t) {});
-      else if (turns <= (uint32_t)A::SU)
-        steps([&](uint32_t u0, uint32_t buf) {
-#pragma nounroll
-          for (uint32_t k = turn; k < (uint32_t)A::SU && u0 + k < ub; k += turns)
-            unit(std::integral_constant<int, 2>{}, buf, 2 * k);
-        });
-      else
-        steps([&](uint32_t u0, uint32_t buf) {
-          if (u0 + (turn >> 1) < ub) unit(std::integral_constant<int, 1>{}, buf, turn);
-        });
+      // spans of a step for each turn
+      const uint32_t each = 2 * A::SU / turns;
+      if (A::SU == 2 && each == 4) steps(std::integral_constant<int, 2 * A::SU>{});
+      else if (each == 2) steps(std::integral_constant<int, 2>{});
+      else steps(std::integral_constant<int, 1>{});
+      float top = soft.ref, sum = soft.sum;
+      {
+        const float f = A::adjust(cs, soft);
+        sum *= f;
+#pragma unroll
+        for (int d = 0; d < A::DR; ++d) o[d] *= f;
+      }
       // the token turns joined, half of them at a time, through LDS in the lanes' own order
       f32x4* const s_o = reinterpret_cast<f32x4*>(s_buf);
-      float2* const s_ml = reinterpret_cast<float2*>(s_buf + (uint32_t)(NW / 2) * NT * DT * 1024);
+      float2* const s_ml = reinterpret_cast<float2*>(s_buf + (uint32_t)(NW / 2) * A::DR * 4096);
       for (uint32_t h = turns / 2; h >= 1; h >>= 1) {
         __syncthreads();
         const uint32_t at = (turn % h) * tiles + sub;   // < NW / 2
         if (nw && turn >= h && turn < 2 * h) {
+          s_ml[at * 64 + lane] = make_float2(top, sum);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            s_ml[(at * NT + nt) * 64 + lane] = make_float2(top[nt], sum[nt]);
+          for (int d = 0; d < A::DR; ++d)
 #pragma unroll
-            for (int d = 0; d < DT; ++d) s_o[((at * NT + nt) * DT + d) * 64 + lane] = o[nt][d];
-          }
+            for (int j = 0; j < 4; ++j)
+              s_o[((at * A::DR + d) * 4 + j) * 64 + lane] = f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
         }
         __syncthreads();
         if (nw && turn < h) {
+          const float2 x = s_ml[at * 64 + lane];
+          const float m = fmaxf(top, x.x);
+          const float f = top == -INFINITY ? 1.f : pow2((top - m) * cs);   // (without a maximum: 0, or NaN)
+          const float e = x.x == -INFINITY ? 1.f : pow2((x.x - m) * cs);
+          top = m;
+          sum = sum * f + x.y * e;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float2 x = s_ml[(at * NT + nt) * 64 + lane];
-            const float m = fmaxf(top[nt], x.x);
-            const float f = top[nt] == -INFINITY ? 1.f : pow2((top[nt] - m) * cs);   // (without a maximum: 0, or NaN)
-            const float e = x.x == -INFINITY ? 1.f : pow2((x.x - m) * cs);
-            top[nt] = m;
-            sum[nt] = sum[nt] * f + x.y * e;
+          for (int d = 0; d < A::DR; ++d)
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[nt][d] = o[nt][d] * f + s_o[((at * NT + nt) * DT + d) * 64 + lane] * e;
-          }
+            for (int j = 0; j < 4; ++j) {
+              const f32x4 y = s_o[((at * A::DR + d) * 4 + j) * 64 + lane];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[d][4 * j + i] = o[d][4 * j + i] * f + y[i] * e;
+            }
         }
       }
-      if (turn == 0 && nw) store(slot + sub * A::QT, nw, o, top, sum);
+      if (turn == 0 && nw) {
+        const auto other = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+        sum = __uint_as_float(other[0]) + __uint_as_float(other[1]);
+        if (r32 < nw) {
+          const uint64_t at = slot + sub * A::RT + r32;
+          if (h32 == 0) ml[at] = make_float2(top, sum);
+          float* const p = values + at * D + 4 * h32;
+#pragma unroll
+          for (int d = 0; d < A::DR; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<f32x4*>(p + 32 * d + 8 * j) = f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+        }
+      }
     }
   }
 
   // ---- the wave's piece: own tokens, and shared ones of few rows, straight from the cache
-  const uint32_t wp = b * NW + wave;
   uint32_t pos = wp * per_v;
   if (pos >= all_v) return;
   const uint32_t end = min(pos + per_v, all_v);
-  uint32_t at = uni(s_first[1 + wave].at), start = uni(s_first[1 + wave].start), before = uni(s_first[1 + wave].rows);
+  First f = first_of(s_first[1 + wave]);
   while (pos < end) {
-    const bool own = at >= n_grp;
-    uint32_t row0, rows, from = 0;
-    int32_t base;   // what row 0 sees
-    uint32_t req, g0 = 0;
-    Line l;
-    if (own) {
-      req = at - n_grp;
-      row0 = (uint32_t)uniform_load(a.req_off, req);
-      rows = (uint32_t)uniform_load(a.req_off, req + 1) - row0;
-      const int32_t len = uniform_load(a.kv_len, req);
-      const uint32_t shared = uni(s_from[req]);
-      l = line_own<D, F8>(a, len, rows, shared);
-      from = shared * (64 / UT);
-      base = len - (int32_t)rows + 1;
-    } else {
-      g0 = (uint32_t)uniform_load(a.grp_off, at);
-      const uint32_t g1 = (uint32_t)uniform_load(a.grp_off, at + 1);
-      row0 = (uint32_t)uniform_load(a.req_off, g0);
-      rows = (uint32_t)uniform_load(a.req_off, g1) - row0;
-      const uint32_t shared = g1 > g0 ? uni(s_from[g0]) : 0u;
-      l = shared && rows * a.group <= (uint32_t)A::QT ? line_v<D, F8>(rows * a.group, shared * (64 / UT), hkv) : Line{0, 0, 0};
-      base = (int32_t)(shared * 64);
-      req = 0;
-    }
-    if (pos >= start + l.places) {
-      start += l.places;
-      before += l.places ? hkv * l.q : 0u;
-      ++at;
+    const bool own = f.at >= n_grp;
+    const Part l = own ? part_own<D, F8>(a, f.len, f.rows, f.shared) : part_shared<D, F8>(a, f.rows, f.shared);
+    const uint32_t len1 = l.units && !l.wide ? cut.places(l.units) : 0u, places = hkv * ((l.q + A::QT - 1) / A::QT) * len1;
+    if (pos >= f.start + places) {
+      f.start += places;
+      f.slots += len1 ? hkv * l.q : 0u;
+      ++f.at;
+      load_at(f);
       continue;
     }
-    if (!own) req = lead_of(g0);
-    const uint32_t len1 = A::kLeadV + l.units, item = (pos - start) / len1, first = start + item * len1;
+    const uint32_t row0 = f.row0, req = own ? f.at - n_grp : f.lead, from = own ? f.shared * (64 / UT) : 0u;
+    const int32_t base = own ? f.len - (int32_t)f.rows + 1 : (int32_t)(f.shared * 64);   // what row 0 sees
+    const uint32_t item = (pos - f.start) / len1, first = f.start + item * len1;
     const uint32_t la = pos - first, n_here = min(len1 - la, end - pos);
     pos += n_here;
-    if (la + n_here <= A::kLeadV) continue;
-    const uint32_t ua = from + (la > A::kLeadV ? la - A::kLeadV : 0u), ub = from + la + n_here - A::kLeadV;
+    uint32_t ua, ub;
+    cut.units_of(l.units, la, la + n_here, ua, ub);
+    if (ua >= ub) continue;
+    ua += from;
+    ub += from;
     const uint32_t tiles = (l.q + A::QT - 1) / A::QT, head = item / tiles, q0 = (item - head * tiles) * A::QT;
     const uint32_t nw = min((uint32_t)A::QT, l.q - q0);
-    const uint64_t slot = region + before + head * l.q + q0 + (uint64_t)A::QT * wp;
+    const uint64_t slot = region + f.slots + head * l.q + q0 + (uint64_t)A::QT * wp;
     const uint64_t trow = (uint64_t)req * a.max_pages;
     // all the wave's rows at once, or, where a value that is not finite lies among the tokens that some
     // of them see and some do not, one batch row after the other
@@ -726,17 +871,25 @@ template <int D, bool F8>
 __global__ __launch_bounds__(256) void k_shared_join(SharedArgs a) {
   using A = Shared<D, F8>;
   constexpr int L = D / 4, SG = 64 / L;   // lanes of one part, parts at a time
+  constexpr uint32_t kFlight = 8;         // reads of a lane at once
   const int lane = threadIdx.x & 63;
   const uint32_t id = uni(blockIdx.x * 4 + (threadIdx.x >> 6));
   if (id >= a.m * a.n_heads) return;
   const uint32_t row = id / a.n_heads, h = id - row * a.n_heads;
-  const uint32_t* const hdr = reinterpret_cast<const uint32_t*>(a.ws);
-  const u32x2 where = reinterpret_cast<const u32x2*>(a.ws + kSharedRow)[row];
-  const uint32_t valid = hdr[0], per_w = hdr[1], per_v = hdr[2];
-  if (!valid || where[0] == ~0u) return;
-  const uint32_t* const r = reinterpret_cast<const uint32_t*>(a.ws + kSharedReq) + kRecWords * where[0];
-  const uint32_t* const g = reinterpret_cast<const uint32_t*>(a.ws + kSharedGrp) + kRecWords * where[1];
-  const uint32_t hkv = a.n_kv_heads, kvh = h / a.group, gq = h - kvh * a.group;
+  const int32_t* const hdr = reinterpret_cast<const int32_t*>(a.ws);
+  const int32_t* const rows = reinterpret_cast<const int32_t*>(a.ws + kSharedRow);
+  const uint32_t valid = (uint32_t)uniform_load(hdr, 0), per_w = (uint32_t)uniform_load(hdr, 1);
+  const uint32_t per_v = (uint32_t)uniform_load(hdr, 2);
+  const Cut cut = {(uint32_t)uniform_load(hdr, 3), A::kLeadV};
+  const uint32_t req = (uint32_t)uniform_load(rows, 2ull * row), grp = (uint32_t)uniform_load(rows, 2ull * row + 1);
+  if (!valid || req == ~0u) return;
+  uint32_t r[6], g[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    r[i] = (uint32_t)uniform_load(reinterpret_cast<const int32_t*>(a.ws + kSharedReq), kRecWords * req + i);
+    g[i] = (uint32_t)uniform_load(reinterpret_cast<const int32_t*>(a.ws + kSharedGrp), kRecWords * grp + i);
+  }
+  const uint32_t kvh = h / a.group, gq = h - kvh * a.group;
   const float2* const ml = reinterpret_cast<const float2*>(a.ws + kSharedMl);
   const uint64_t region = (uint64_t)a.m * a.n_heads + (uint64_t)kSharedGrid * A::QW;
   const float* const values =
@@ -746,58 +899,73 @@ __global__ __launch_bounds__(256) void k_shared_join(SharedArgs a) {
   uint32_t g_w0 = 0, g_n = 0, g_step = A::QT, r_w0 = 0, r_n = 0;
   if (g[2]) {
     const uint32_t nq_all = g[1], units = g[2], qi = (row - g[0]) * a.group + gq;
+    g_slot = (uint64_t)g[4] + kvh * nq_all + qi;
     if (g[5]) {
       const uint32_t full = nq_all / A::QW, one = A::kLeadW + units * A::cost(A::NW), tile = qi / A::QW;
-      const bool last = tile == full;
-      const uint32_t nq = last ? nq_all - full * A::QW : (uint32_t)A::QW, c = last ? A::cost((nq + A::QT - 1) / A::QT) : A::cost(A::NW);
-      const uint32_t first = g[3] + (last ? full * hkv * one + kvh * (A::kLeadW + units * c) : (tile * hkv + kvh) * one);
-      g_w0 = (first + A::kLeadW) / per_w;
-      g_n = (first + A::kLeadW + (units - 1) * c) / per_w - g_w0 + 1;
-      g_slot = (uint64_t)g[4] + tile * A::QW * hkv + kvh * nq + (qi - tile * A::QW);
+      const uint32_t rest = nq_all - full * A::QW, c_rest = A::cost((rest + A::RT - 1) / A::RT);
+      const uint32_t per_head = full * one + (rest ? A::kLeadW + units * c_rest : 0u);
+      const uint32_t c = tile == full ? c_rest : A::cost(A::NW), first = g[3] + kvh * per_head + tile * one + A::kLeadW;
+      g_w0 = first / per_w;
+      g_n = (first + (units - 1) * c) / per_w - g_w0 + 1;
       g_step = A::QW;
     } else {
-      const uint32_t first = g[3] + kvh * (A::kLeadV + units);
-      g_w0 = (first + A::kLeadV) / per_v;
-      g_n = (first + A::kLeadV + units - 1) / per_v - g_w0 + 1;
-      g_slot = region + g[4] + kvh * nq_all + qi;
+      uint32_t p0, p1;
+      cut.ends(units, p0, p1);
+      const uint32_t first = g[3] + kvh * cut.places(units);
+      g_w0 = (first + p0) / per_v;
+      g_n = (first + p1) / per_v - g_w0 + 1;
+      g_slot += region;
     }
+    g_slot += (uint64_t)g_w0 * g_step;
   }
   if (r[2]) {
     const uint32_t q = r[1], units = r[2], qi = (row - r[0]) * a.group + gq, tiles = (q + A::QT - 1) / A::QT;
-    const uint32_t first = r[3] + (kvh * tiles + qi / A::QT) * (A::kLeadV + units);
-    r_w0 = (first + A::kLeadV) / per_v;
-    r_n = (first + A::kLeadV + units - 1) / per_v - r_w0 + 1;
-    r_slot = region + r[4] + kvh * q + qi;
+    uint32_t p0, p1;
+    cut.ends(units, p0, p1);
+    const uint32_t first = r[3] + (kvh * tiles + qi / A::QT) * cut.places(units);
+    r_w0 = (first + p0) / per_v;
+    r_n = (first + p1) / per_v - r_w0 + 1;
+    r_slot = region + r[4] + kvh * q + qi + (uint64_t)r_w0 * A::QT;
   }
   const uint32_t n = g_n + r_n;
   auto slot_of = [&](uint32_t i) {
-    return i < g_n ? g_slot + (uint64_t)(g_w0 + i) * g_step : r_slot + (uint64_t)(r_w0 + i - g_n) * A::QT;
+    return i < g_n ? g_slot + (uint64_t)i * g_step : r_slot + (uint64_t)(i - g_n) * A::QT;
   };
   const float cs = fabsf(a.score_scale);
   float m = -INFINITY, l = 0.f;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   const uint32_t sg = lane / L, d = 4 * (lane % L);
   for (uint32_t i0 = 0; i0 < n; i0 += 64) {
-    float2 x = make_float2(-INFINITY, 0.f);
-    if (i0 + lane < n) x = ml[slot_of(i0 + lane)];
-    const float mx = fmaxf(m, wave_max(x.x));
+    const uint32_t here = min(64u, n - i0);
+    f32x4 x[kFlight];
+    auto request = [&](uint32_t i) {   // (past the end: the last one again, unused)
+#pragma unroll
+      for (uint32_t k = 0; k < kFlight; ++k)
+        x[k] = *reinterpret_cast<const f32x4*>(values + slot_of(i0 + min(i + k * SG + sg, here - 1)) * D + d);
+    };
+    request(0);
+    const float2 y = (uint32_t)lane < here ? ml[slot_of(i0 + lane)] : make_float2(-INFINITY, 0.f);
+    const float mx = fmaxf(m, wave_max(y.x));
     const float fade = m == -INFINITY ? 1.f : pow2((m - mx) * cs);   // (without a maximum: 0, or NaN that stays)
-    const float f = x.x == -INFINITY ? 1.f : pow2((x.x - mx) * cs);
-    l = l * fade + wave_sum(x.y * f);
+    const float f = y.x == -INFINITY ? 1.f : pow2((y.x - mx) * cs);
+    l = l * fade + wave_sum(y.y * f);
     v *= fade;
     m = mx;
-    const uint32_t here = min(64u, n - i0);
-    for (uint32_t i = 0; i < here; i += SG) {
-      const uint32_t k = i + sg;
-      const float fk = __shfl(f, (int)min(k, 63u));
-      if (k < here) v += *reinterpret_cast<const f32x4*>(values + slot_of(i0 + k) * D + d) * fk;
+    for (uint32_t i = 0; i < here; i += kFlight * SG) {
+      if (i) request(i);
+#pragma unroll
+      for (uint32_t k = 0; k < kFlight; ++k) {
+        const uint32_t j = i + k * SG + sg;
+        const float fk = __shfl(f, (int)min(j, 63u));
+        if (j < here) v += x[k] * fk;
+      }
     }
   }
 #pragma unroll
   for (int o = L; o < 64; o <<= 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], o);
-  const bool broken = r[5] == 0x80000000u;
+  const bool broken = r[5] == kBroken;
   const int32_t sees = (int32_t)r[5] + (int32_t)(row - r[0]);
   const float f = broken ? NAN : (sees > 0 ? a.v_scale / l : 0.f);
   if (sg == 0) {
@@ -818,7 +986,7 @@ hipError_t shared_go(const SharedArgs& given, hipStream_t s) {
   const uint64_t items = (((uint64_t)a.m * a.group + A::QT - 1) / A::QT + a.n_req + a.n_grp) * a.n_kv_heads;
   uint64_t grid = kSharedGrid;
   if (units < (1u << 20) && items < (1u << 20)) {
-    const uint64_t wg = (items * (units + A::kLeadV) / A::kLeastV + A::NW - 1) / A::NW;
+    const uint64_t wg = (items * (units / 2 + 1) + A::NW - 1) / A::NW;
     grid = wg < 1 ? 1 : (wg < grid ? wg : grid);
   }
   a.grid = (uint32_t)grid;
