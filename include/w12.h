@@ -617,9 +617,9 @@ w12_status w12_kv_compact(const w12_pages* p, int32_t* refs, uint32_t first, uin
                           int32_t* moves, int32_t* moved, void* stream);
 
 /* w12_attn_paged where requests share their first tokens, which are read once for all of them: group
- * g is requests grp_off[g] .. grp_off[g+1]-1, and the first grp_len[g] tokens of each lie in the same
- * pages (those in the table row of its first request that has rows and a length are read; below 1:
- * nothing is shared).  Requests in no company are groups of one.  Results are those of w12_attn_paged up to the
+ * g is requests grp_off[g] .. grp_off[g+1]-1, and the first grp_len[g] tokens of each are the same, in
+ * the same pages or in copies of them (the pages in the table row of its first request that has rows
+ * and a length are read; below 1: nothing is shared).  Requests in no company are groups of one.  Results are those of w12_attn_paged up to the
  * order of the FP32 sums, with the same rules for rows that see no token, for what lies behind a
  * row's last token, for rows of no request, and for requests and pages that are none (a shared
  * page that is none makes the rows of its whole group NaN).  Every row gets NaN when grp_off is not

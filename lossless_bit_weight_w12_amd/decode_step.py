@@ -20,6 +20,8 @@ appended with v to the layer's paged cache (w12_qk_rope), the rows of every requ
 its cache (w12_attn_paged), and o reads that (o = attention W_o^T) in place of rms(q); the block
 tables are brought in line with the requests' lengths once per step (w12_kv_plan).  The accepted
 lengths of requests that the pool refused become -1 in an elementwise minimum of torch's.
+Requests that continue one prompt may share its pages (w12_kv_fork, and w12_kv_copy of the last
+pages that they may not share) and have them read once for all of them (w12_attn_shared).
 """
 from __future__ import annotations
 
@@ -39,7 +41,12 @@ class DecodeAttention:
     a request without rows stays as it is, and of a request whose last row had a draft too, that
     one is no row yet.  A request that the pool had too few pages for, or whose length is none,
     has accepted -1: it keeps its length and comes again, with the same rows, once pages are
-    free."""
+    free.
+
+    Where pages has counts of holders (page_table(shared=True)) a step begins with w12_kv_fork and
+    copies, in all layers' caches, what that asks for: request r continues request parent[r] as it was
+    before the step (parent None: itself), with length[r] of its tokens.  The pool serves all requests
+    or none.  groups: (grp_off, grp_len) of w12_attn_shared, requests whose first tokens are read once."""
     n_heads: int
     pages: object      # w12.PageTable, shared by the layers
     caches: list       # w12.KvCache per layer
@@ -47,6 +54,8 @@ class DecodeAttention:
     length: object     # int32 [n_req]
     req_off: object    # int32 [n_req + 1]
     scale: float = None    # default head_dim ** -0.5
+    parent: object = None  # int32 [n_req], with counts of holders only
+    groups: tuple = None   # (int32 [n_grp + 1], int32 [n_grp])
 
 
 class DecodeStack:
@@ -84,6 +93,8 @@ class DecodeStack:
                 raise ValueError("DecodeAttention: a cache does not hold the pool's pages")
             if (L["q"].n, L["k"].n, L["v"].n, L["o"].k) != (at.n_heads * d, kv_heads * d, kv_heads * d, at.n_heads * d):
                 raise ValueError("DecodeAttention: the heads do not fit q, k, v and o")
+        if at.parent is not None and at.pages.refs is None:
+            raise ValueError("DecodeAttention: a parent needs counts of the pages' holders")
         i32 = dict(dtype=torch.int32, device=dev)
         self.kv_len = torch.empty_like(at.length)
         self.pos, self.slot = torch.empty(self.m, **i32), torch.empty(self.m, **i32)
@@ -92,7 +103,12 @@ class DecodeStack:
         # request's.  What a step gives for them means nothing; no other row depends on it.
         self.turned, self.a = torch.zeros_like(self.out["q"]), torch.zeros_like(self.a)
         self.accepted = torch.empty(at.length.numel(), **i32)
-        self.attn_ws = w12.attn_workspace(dev)
+        if at.pages.refs is not None:
+            self.copies = torch.empty((at.length.numel(), 4), **i32)
+        if at.groups is None:
+            self.attn_ws = w12.attn_workspace(dev)
+        else:
+            self.attn_ws = w12.attn_shared_workspace(self.m, at.n_heads, max(c.k.shape[3] for c in at.caches), dev)
         # The fills above are through before the stack is handed out: its steps may run on any
         # stream, and a ticket that is cleared while a join is under way would end it early.
         torch.cuda.current_stream(dev).synchronize()
@@ -102,10 +118,13 @@ class DecodeStack:
         at, o, c = self.attention, self.out, self.attention.caches[li]
         heads = lambda t: t.view(self.m, -1, c.k.shape[3])
         q = heads(self.turned)
+        tables = (at.pages.table, self.kv_len, at.req_off)
+        if at.groups is None:
+            attn = w12.prepare_attn_paged(q, c, *tables, heads(self.a), at.scale, self.attn_ws)
+        else:
+            attn = w12.prepare_attn_shared(q, c, *tables, *at.groups, heads(self.a), at.scale, self.attn_ws)
         return [w12.prepare_qk_rope(heads(o["q"]), heads(o["k"]), heads(o["v"]), c, at.ropes[li], self.pos,
-                                    self.slot, q),
-                w12.prepare_attn_paged(q, c, at.pages.table, self.kv_len, at.req_off, heads(self.a), at.scale,
-                                       self.attn_ws)]
+                                    self.slot, q), attn]
 
     def _layer_calls(self, L, first: bool, li: int):
         calls = self._chain_calls(L, first)
@@ -155,7 +174,12 @@ class DecodeStack:
             raise ValueError("a step with attention verifies its requests: req_ndraft is missing")
         import torch
         self.stream = torch.cuda.current_stream(self.head.device)
-        self.plan_call = w12.prepare_kv_plan(at.pages, at.length, at.req_off, self.kv_len, self.pos, self.slot)
+        if at.pages.refs is None:
+            self.plan_calls = [w12.prepare_kv_plan(at.pages, at.length, at.req_off, self.kv_len, self.pos, self.slot)]
+        else:
+            self.plan_calls = [w12.prepare_kv_fork(at.pages, at.parent, at.length, at.req_off, self.kv_len, self.pos,
+                                                   self.slot, self.copies),
+                               w12.prepare_kv_copy(at.caches, self.copies)]
         self.verify_call = w12.prepare_verify_batched(self.h, self.head, at.req_off, req_ndraft, draft,
                                                       self.argmax, self.accepted)
 
@@ -169,10 +193,14 @@ class DecodeStack:
             with torch.cuda.stream(self.stream):   # that of the prepared calls
                 torch.minimum(self.accepted, self.kv_len.view(-1), out=self.accepted)
 
+    def _plan(self):
+        if self.attention is not None:
+            for c in self.plan_calls:
+                c()
+
     def run(self):
         """One step from the current contents of self.h (after prepare)."""
-        if self.attention is not None:
-            self.plan_call()
+        self._plan()
         for calls in self.calls:
             for c in calls:
                 c()
@@ -188,8 +216,7 @@ class DecodeStack:
         caps = {}
         self.h.copy_(h0)
         o = self.out
-        if self.attention is not None:
-            self.plan_call()
+        self._plan()
         for li, calls in enumerate(self.calls):
             if li in capture:
                 x_qkv = (self.h if li == 0 or not self.fused_rms else o["down"]).clone()

@@ -1227,8 +1227,8 @@ def _shared_args(q, cache: KvCache, table, kv_len, req_off, grp_off, grp_len, ou
 
 def attn_shared(q, cache: KvCache, table, kv_len, req_off, grp_off, grp_len, out=None, scale=None, ws=None):
     """attn_paged for requests that share their first tokens (w12_attn_shared): the first grp_len[g]
-    tokens of requests grp_off[g] .. grp_off[g+1]-1 lie in the same pages and are read once for all of
-    them.  grp_off int32 [n_grp + 1] from 0 to n_req, grp_len int32 [n_grp].  Returns out (BF16; rows
+    tokens of requests grp_off[g] .. grp_off[g+1]-1 are the same (in the same pages or copies of them)
+    and are read once for all of them.  grp_off int32 [n_grp + 1] from 0 to n_req, grp_len int32 [n_grp].  Returns out (BF16; rows
     of no request are left as they were)."""
     if q.dim() != 3:
         raise ValueError("attn_shared: q must be [m, n_heads, head_dim]")
