@@ -20,14 +20,15 @@ constexpr uint32_t kForkWG = 256;        // workgroups of a launch, at most (one
 constexpr uint32_t kEntries = 8192;      // table entries of a workgroup in LDS at a time
 constexpr uint32_t kWriter = 0x10000u;   // a mark of a request that writes
 
-__device__ __forceinline__ int32_t load_dev(const int32_t* p) {   // past this XCD's L2, as the atomics are
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Words that one workgroup alone uses in a launch.
+__device__ __forceinline__ int32_t load_here(const int32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
-__device__ __forceinline__ void store_dev(int32_t* p, int32_t v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void add_here(int32_t* p, int32_t v) {
+  __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
-__device__ __forceinline__ void add_dev(int32_t* p, int32_t v) {
-  __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void max_here(int32_t* p, int32_t v) {
+  __hip_atomic_fetch_max(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
 // Sum over the workgroup's threads, the same in all of them.
@@ -102,192 +103,185 @@ __device__ __forceinline__ Fork fork_req(const ForkArgs& a, uint32_t r, bool& ba
   return f;
 }
 
-// The requests in LDS.  flags: bit 31 of keep: writes.
-template <int N>
-struct ForkTable {
-  int32_t src[N];
-  uint32_t held[N], keep[N];
+// The requests in LDS.  Flags of keep: the request writes into the last page it takes, and gets a
+// copy of it.
+constexpr uint32_t kWrites = 1u << 31, kCopied = 1u << 30, kKeep = kCopied - 1u;
+template <int T, int N>
+struct ForkLds {
+  int32_t src[N], len[N];   // len: -1: not served
+  uint32_t held[N], keep[N], need[N + 1], off[N + 1];
+  int32_t old[kEntries];
+  uint32_t w[T / 64], cols, sum[2], last;
 };
-constexpr uint32_t kWrites = 1u << 31;
+
+// Reads them, a thread some in a row; need[r + 1]: pages behind those it takes.  Whether the offsets
+// are none; T * ceil(N / T) requests at most.
+template <int T, int N>
+__device__ __forceinline__ bool fork_requests(const ForkArgs& a, ForkLds<T, N>& s) {
+  const uint32_t t = threadIdx.x, n = a.n_req, per = (n + T - 1) / T;
+  if (t == 0) s.cols = s.need[0] = 0;
+  __syncthreads();
+  uint32_t cols = 0;
+  bool bad = false;
+#pragma unroll
+  for (uint32_t i = 0; i < N / T; ++i) {
+    const uint32_t r = t * per + i;
+    if (i >= per || r >= n) break;
+    const Fork f = fork_req(a, r, bad);
+    s.src[r] = f.src;
+    s.held[r] = f.held;
+    s.keep[r] = f.keep | (f.writes ? kWrites : 0u);
+    s.need[r + 1] = f.want - f.keep;
+    s.len[r] = f.served ? f.len : -1;
+    s.off[r] = f.off;
+    if (r + 1 == n) s.off[n] = f.off + f.rows;
+    cols = max(cols, max(f.held, f.keep));
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) cols = max(cols, (uint32_t)__shfl_xor((int)cols, o));
+  if ((t & 63) == 0) atomicMax(&s.cols, cols);
+  return __syncthreads_or(bad);
+}
+
+// The table's columns c0 .. c0 + w - 1 as they are.
+template <int T, int N>
+__device__ __forceinline__ void fork_columns(const ForkArgs& a, ForkLds<T, N>& s, uint32_t c0, uint32_t w) {
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < w * a.n_req; e += T) {
+    const uint32_t r = e / w, j = e - r * w;
+    s.old[j * a.n_req + r] = c0 + j < s.held[r] ? a.table[(uint64_t)r * a.max_pages + c0 + j] : -1;
+  }
+  __syncthreads();
+}
 
 // What request r's place in column c holds (x) and will hold of src's pages (y), -1: nothing.
-template <int N>
-__device__ __forceinline__ void entry(const ForkArgs& a, const ForkTable<N>& q, const int32_t* s_old, uint32_t n,
-                                      uint32_t r, uint32_t j, uint32_t c, int32_t& x, int32_t& y, bool& tail) {
-  const uint32_t keep = q.keep[r] & ~kWrites;
-  x = s_old[j * n + r];
+template <int T, int N>
+__device__ __forceinline__ void entry(const ForkArgs& a, const ForkLds<T, N>& s, uint32_t r, uint32_t j, uint32_t c,
+                                      int32_t& x, int32_t& y, bool& tail) {
+  const uint32_t n = a.n_req, flags = s.keep[r], keep = flags & kKeep;
+  x = s.old[j * n + r];
   y = -1;
   tail = false;
   if (c < keep) {
-    const int32_t src = q.src[r];
-    y = (uint32_t)src < n ? s_old[j * n + (uint32_t)src] : a.table[(uint64_t)(uint32_t)src * a.max_pages + c];
-    tail = c + 1 == keep && (q.keep[r] & kWrites);
+    const int32_t src = s.src[r];
+    y = (uint32_t)src < n ? s.old[j * n + (uint32_t)src] : a.table[(uint64_t)(uint32_t)src * a.max_pages + c];
+    tail = c + 1 == keep && (flags & kWrites);
   }
 }
 
-// Both kernels of w12_kv_fork deal the columns that somebody holds to the workgroups: the holders
-// of a page hold it in the same column (a request that continues another one has its first
-// tokens in the same places), so one workgroup sees everything about a page.  A column's old
-// entries are in LDS, so that the rows can change places.  The first kernel counts: the change of
-// each page's holders, the requests that write into their last page (the lowest may keep it if
-// nobody else holds it), and the pages nobody holds any longer; the second knows from the sums
-// where the pages it gives back go and whether there are enough, and writes.  Entries that stay are
-// passed over before any atomic, so a prompt's shared pages cost nothing.
+// The columns that somebody holds are dealt to the workgroups, of both halves of w12_kv_fork alike:
+// the holders of a page hold it in the same column (a request that continues another one has its
+// first tokens in the same places), so one workgroup sees everything about a page, and what it
+// counts per page needs no wider scope than its own.  A column's old entries are in LDS, so that
+// the rows can change places.  The first half counts: the change of each page's holders, the
+// requests that write into their last page (the lowest may keep it if nobody else holds it), and
+// the pages nobody holds any longer; the second knows from the sums where the pages it gives back
+// go and whether there are enough, and writes.  Entries that stay are passed over before any
+// atomic, so a prompt's shared pages cost nothing.
 //
-// Bound by latency (dependent reads behind two launches).
+// Two launches, or one where a single workgroup takes all columns.  Bound by latency (dependent
+// reads behind the launches).
+struct Columns {   // of a workgroup, and how many of them are in LDS at a time
+  uint32_t begin, end, width;
+};
 template <int T, int N>
-__global__ __launch_bounds__(T) void k_fork_look(ForkArgs a) {
-  __shared__ ForkTable<N> q;
-  __shared__ int32_t s_old[kEntries];
-  __shared__ uint32_t s_w[T / 64], s_cols, s_bad;
-  const uint32_t t = threadIdx.x, n = a.n_req, b = blockIdx.x;
+__device__ __forceinline__ Columns columns(const ForkArgs& a, const ForkLds<T, N>& s) {
+  const uint32_t per = (s.cols + gridDim.x - 1) / gridDim.x;
+  return Columns{blockIdx.x * per, min(s.cols, (blockIdx.x + 1) * per), max(1u, min(per, kEntries / a.n_req))};
+}
+
+// The first half: the number of pages that this workgroup's columns give back.
+template <int T, int N>
+__device__ __forceinline__ uint32_t fork_look(const ForkArgs& a, ForkLds<T, N>& s) {
+  const uint32_t t = threadIdx.x, n = a.n_req;
   int32_t* const delta = a.refs + a.n_pages;
   int32_t* const mark = delta + a.n_pages;
-  uint32_t* const counts = reinterpret_cast<uint32_t*>(a.refs) + 5ull * a.n_pages;
-  if (t == 0) s_cols = s_bad = 0;
-  __syncthreads();
-  const int32_t head = a.state[0], count = a.state[1];
-  bool bad = head < 0 || (uint32_t)head >= a.n_pages || count < 0 || (uint32_t)count > a.n_pages || a.state[2] != 0;
-  uint32_t cols = 0;
-  for (uint32_t r = t; r < n; r += T) {
-    const Fork f = fork_req(a, r, bad);
-    q.src[r] = f.src;
-    q.held[r] = f.held;
-    q.keep[r] = f.keep | (f.writes ? kWrites : 0u);
-    cols = max(cols, max(f.held, f.keep));
-    if (b == 0 && !f.writes) {
-      int32_t* const e = a.copies + 4ull * r;
-      e[0] = e[1] = -1;
-      e[2] = e[3] = 0;
-    }
-  }
-  atomicMax(&s_cols, cols);
-  if (bad) s_bad = 1;
-  __syncthreads();
-  if (b == 0 && t == 0) counts[kForkWG] = s_bad;
-  if (s_bad) return;
-  cols = s_cols;
-  const uint32_t per = (cols + gridDim.x - 1) / gridDim.x, c_end = min(cols, (b + 1) * per);
-  const uint32_t width = max(1u, min(per, kEntries / n));
   uint32_t freed = 0;
   auto valid = [&](int32_t p) { return (uint32_t)p < a.n_pages; };
-  for (uint32_t c0 = b * per; c0 < c_end; c0 += width) {
-    const uint32_t w = min(width, c_end - c0), all = w * n;
-    __syncthreads();
-    for (uint32_t e = t; e < all; e += T) {
-      const uint32_t r = e / w, j = e - r * w;
-      s_old[j * n + r] = c0 + j < q.held[r] ? a.table[(uint64_t)r * a.max_pages + c0 + j] : -1;
-    }
-    __syncthreads();
+  const Columns k = columns(a, s);
+  for (uint32_t c0 = k.begin; c0 < k.end; c0 += k.width) {
+    const uint32_t w = min(k.width, k.end - c0), all = w * n;
+    fork_columns(a, s, c0, w);
     bool any = false;
     for (uint32_t e = t; e < all; e += T) {
       const uint32_t j = e / n, r = e - j * n;
       int32_t x, y;
       bool tail;
-      entry(a, q, s_old, n, r, j, c0 + j, x, y, tail);
+      entry(a, s, r, j, c0 + j, x, y, tail);
       if (x == y && !tail) continue;
       any = true;
       if (valid(x)) {
-        add_dev(delta + x, -1);
-        __hip_atomic_fetch_max(mark + x, (int32_t)(n - r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        add_here(delta + x, -1);
+        max_here(mark + x, (int32_t)(n - r));
       }
       if (valid(y)) {
-        if (tail) __hip_atomic_fetch_max(mark + y, (int32_t)(kWriter + n - r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        else add_dev(delta + y, 1);
+        if (tail) max_here(mark + y, (int32_t)(kWriter + n - r));
+        else add_here(delta + y, 1);
       }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     if (!__syncthreads_or(any)) continue;
     for (uint32_t e = t; e < all; e += T) {
       const uint32_t j = e / n, r = e - j * n;
       int32_t x, y;
       bool tail;
-      entry(a, q, s_old, n, r, j, c0 + j, x, y, tail);
+      entry(a, s, r, j, c0 + j, x, y, tail);
       if (x == y && !tail) continue;
-      if (valid(x)) freed += load_dev(mark + x) == (int32_t)(n - r) && a.refs[x] + load_dev(delta + x) == 0;
+      if (valid(x)) freed += load_here(mark + x) == (int32_t)(n - r) && a.refs[x] + load_here(delta + x) == 0;
       if (tail) {   // the lowest of those that write keeps a page that nobody else holds
-        const bool stays = !valid(y) || (load_dev(mark + y) == (int32_t)(kWriter + n - r) && a.refs[y] + load_dev(delta + y) == 0);
-        int32_t* const c = a.copies + 4ull * r;
-        c[0] = y;
-        c[1] = y;
-        c[2] = stays ? 0 : a.len[r] & ((1 << a.page_shift) - 1);
-        c[3] = 0;
+        const bool stays = !valid(y) || (load_here(mark + y) == (int32_t)(kWriter + n - r) && a.refs[y] + load_here(delta + y) == 0);
+        const int32_t part = s.len[r] & ((1 << a.page_shift) - 1);
+        if (!stays) atomicOr(&s.keep[r], kCopied);
+        *reinterpret_cast<i32x4*>(a.copies + 4ull * r) = i32x4{y, y, stays ? 0 : part, 0};
       }
     }
   }
-  freed = block_sum<T>(freed, s_w);
-  if (t == 0) counts[b] = freed;
+  if (blockIdx.x == 0)
+    for (uint32_t r = t; r < n; r += T)
+      if (!(s.keep[r] & kWrites)) *reinterpret_cast<i32x4*>(a.copies + 4ull * r) = i32x4{-1, -1, 0, 0};
+  return block_sum<T>(freed, s.w);
 }
 
+// The second half.  none: the first one has found a table that is none; before, freed: pages given back
+// by the workgroups before and by all.
 template <int T, int N>
-__global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
+__device__ __forceinline__ void fork_apply(const ForkArgs& a, ForkLds<T, N>& s, bool none, uint32_t before, uint32_t freed) {
   constexpr uint32_t kPer = N / T;
-  __shared__ ForkTable<N> q;
-  __shared__ uint32_t s_need[N + 1], s_off[N + 1];
-  __shared__ int32_t s_len[N];   // -1: not served
-  __shared__ int32_t s_old[kEntries];
-  __shared__ uint32_t s_w[T / 64], s_cols, s_last, s_sum[2];
-  const uint32_t t = threadIdx.x, n = a.n_req, b = blockIdx.x, lane = t & 63, wave = t >> 6;
-  const uint32_t first = b * T + t, step = gridDim.x * T;   // of the flat lists
+  const uint32_t t = threadIdx.x, n = a.n_req, lane = t & 63, wave = t >> 6, cols = s.cols;
+  const uint32_t first = blockIdx.x * T + t, step = gridDim.x * T;   // of the flat lists
   int32_t* const delta = a.refs + a.n_pages;
   int32_t* const mark = delta + a.n_pages;
-  const uint32_t* const counts = reinterpret_cast<const uint32_t*>(a.refs) + 5ull * a.n_pages;
   const uint32_t shift = a.page_shift, in_page = (1u << shift) - 1u;
-  if (t == 0) s_cols = s_sum[0] = s_sum[1] = 0;
-  __syncthreads();
   const uint32_t head = (uint32_t)a.state[0], count = (uint32_t)a.state[1];
-  const bool none = counts[kForkWG] != 0;   // the first kernel has left everything as it was
-  bool bad = false;   // (known)
-  uint32_t cols = 0, need[kPer], sum = 0;
   const uint32_t per_t = (n + T - 1) / T;
+  uint32_t need[kPer], sum = 0;
 #pragma unroll
   for (uint32_t i = 0; i < kPer; ++i) {
     const uint32_t r = t * per_t + i;
-    need[i] = 0;
-    if (i < per_t && r < n) {
-      const Fork f = fork_req(a, r, bad);
-      q.src[r] = f.src;
-      q.held[r] = f.held;
-      q.keep[r] = f.keep | (f.writes ? kWrites : 0u);
-      need[i] = f.want - f.keep + (f.writes && a.copies[4ull * r + 2] > 0 ? 1u : 0u);
-      s_len[r] = f.served ? f.len : -1;
-      s_off[r] = f.off;
-      if (r + 1 == n) s_off[n] = f.off + f.rows;
-      cols = max(cols, max(f.held, f.keep));
-    }
+    need[i] = i < per_t && r < n ? s.need[r + 1] + ((s.keep[r] & kCopied) ? 1u : 0u) : 0u;
     sum = sat_add(sum, need[i]);
   }
-  atomicMax(&s_cols, cols);
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const uint32_t u = __shfl_up(sum, o);
     if (lane >= (uint32_t)o) sum = sat_add(sum, u);
   }
-  if (lane == 63) s_w[wave] = sum;
-  if (t < gridDim.x && T >= kForkWG) {   // pages given back, by the workgroups before and by all
-    const uint32_t v = counts[t];
-    atomicAdd(&s_sum[0], t < b ? v : 0u);
-    atomicAdd(&s_sum[1], v);
-  }
+  if (lane == 63) s.w[wave] = sum;
   __syncthreads();
   uint32_t total = 0;
 #pragma unroll
   for (uint32_t w = 0; w < T / 64; ++w) {
-    if (w < wave) sum = sat_add(sum, s_w[w]);
-    total = sat_add(total, s_w[w]);
+    if (w < wave) sum = sat_add(sum, s.w[w]);
+    total = sat_add(total, s.w[w]);
   }
 #pragma unroll
   for (int i = (int)kPer - 1; i >= 0; --i) {
     const uint32_t r = t * per_t + i;
     if (i < (int)per_t && r < n) {
-      s_need[r + 1] = sum;
+      s.need[r + 1] = sum;
       sum -= need[i];
     }
   }
-  if (t == 0) s_need[0] = 0u;
-  const uint32_t freed = s_sum[1];
   const bool enough = !none && total <= count && (uint64_t)count + freed <= a.n_pages;
-  cols = s_cols;
   __syncthreads();
 
   auto ring_at = [&](uint32_t j) {   // j <= n_pages
@@ -295,28 +289,20 @@ __global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
     return i >= a.n_pages ? i - a.n_pages : i;
   };
   auto valid = [&](int32_t p) { return (uint32_t)p < a.n_pages; };
-  auto copied = [&](uint32_t r) {   // a page of its own for the last one it takes
-    return (q.keep[r] & kWrites) && a.copies[4ull * r + 2] > 0;
-  };
+  auto copied = [&](uint32_t r) { return (s.keep[r] & kCopied) != 0; };
   // the page that request r gets for its column c >= keep, or (c = keep - 1) for the copy
   auto fresh = [&](uint32_t r, uint32_t c, bool copy) {
-    const uint32_t at = s_need[r] + (c + (copy ? 1u : 0u) - (q.keep[r] & ~kWrites));
-    const int32_t p = at < s_need[r + 1] ? a.ring[ring_at(at)] : -1;
+    const uint32_t at = s.need[r] + (c + (copy ? 1u : 0u) - (s.keep[r] & kKeep));
+    const int32_t p = at < s.need[r + 1] ? a.ring[ring_at(at)] : -1;
     return valid(p) ? p : -1;
   };
 
   // ---- the columns
-  const uint32_t per = (cols + gridDim.x - 1) / gridDim.x, c_end = none ? 0u : min(cols, (b + 1) * per);
-  const uint32_t width = max(1u, min(per, kEntries / n));
-  uint32_t back = s_sum[0];   // where this workgroup's pages go in the ring
-  for (uint32_t c0 = b * per; c0 < c_end; c0 += width) {
-    const uint32_t w = min(width, c_end - c0), all = w * n;
-    __syncthreads();
-    for (uint32_t e = t; e < all; e += T) {
-      const uint32_t r = e / w, j = e - r * w;
-      s_old[j * n + r] = c0 + j < q.held[r] ? a.table[(uint64_t)r * a.max_pages + c0 + j] : -1;
-    }
-    __syncthreads();
+  const Columns k = columns(a, s);
+  uint32_t back = before;   // where this workgroup's pages go in the ring
+  for (uint32_t c0 = k.begin; c0 < k.end && !none; c0 += k.width) {
+    const uint32_t w = min(k.width, k.end - c0), all = w * n;
+    fork_columns(a, s, c0, w);
     bool any = false;
     for (uint32_t e0 = 0; e0 < all; e0 += T) {
       const uint32_t e = e0 + t;
@@ -326,14 +312,14 @@ __global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
       if (e < all) {
         const uint32_t j = e / n;
         r = e - j * n;
-        entry(a, q, s_old, n, r, j, c0 + j, x, y, tail);
+        entry(a, s, r, j, c0 + j, x, y, tail);
       }
       const bool moves = e < all && (x != y || tail);
-      const bool gone = moves && valid(x) && load_dev(mark + x) == (int32_t)(n - r) && a.refs[x] + load_dev(delta + x) == 0;
+      const bool gone = moves && valid(x) && load_here(mark + x) == (int32_t)(n - r) && a.refs[x] + load_here(delta + x) == 0;
       any |= moves;
       if (__syncthreads_or(gone)) {
         uint32_t some;
-        const uint32_t rank = block_rank<T>(gone, s_w, some);
+        const uint32_t rank = block_rank<T>(gone, s.w, some);
         if (gone && enough) a.ring[ring_at(count + back + rank)] = x;
         back += some;
       }
@@ -345,69 +331,63 @@ __global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
         const uint32_t j = e / n, r = e - j * n;
         int32_t x, y;
         bool tail;
-        entry(a, q, s_old, n, r, j, c0 + j, x, y, tail);
+        entry(a, s, r, j, c0 + j, x, y, tail);
         if (x == y && !tail) continue;
         const bool to = valid(y) && !(tail && copied(r));
         if (enough) {
-          if (valid(x)) add_dev(a.refs + x, -1);
-          if (to) add_dev(a.refs + y, 1);
+          if (valid(x)) add_here(a.refs + x, -1);
+          if (to) add_here(a.refs + y, 1);
         }
-        if (valid(x)) {
-          store_dev(delta + x, 0);
-          store_dev(mark + x, 0);
-        }
-        if (valid(y)) {
-          store_dev(delta + y, 0);
-          store_dev(mark + y, 0);
-        }
+        if (valid(x)) delta[x] = mark[x] = 0;
+        if (valid(y)) delta[y] = mark[y] = 0;
       }
     if (enough)
       for (uint32_t e = t; e < all; e += T) {
         const uint32_t r = e / w, j = e - r * w, c = c0 + j;
         int32_t x, y;
         bool tail;
-        entry(a, q, s_old, n, r, j, c, x, y, tail);
-        const uint32_t keep = q.keep[r] & ~kWrites, news = s_need[r + 1] - s_need[r];
+        entry(a, s, r, j, c, x, y, tail);
+        const uint32_t keep = s.keep[r] & kKeep, news = s.need[r + 1] - s.need[r];
         if (tail && copied(r)) {
           y = fresh(r, c, true);
-          if (valid(y)) store_dev(a.refs + y, 1);
+          if (valid(y)) a.refs[y] = 1;
           a.copies[4ull * r + 1] = y;
         } else if (c >= keep) {
           const bool more = c - keep < news - (copied(r) ? 1u : 0u);
-          y = more ? fresh(r, c, copied(r)) : x;   // (entries past the pages keep their values)
-          if (more && valid(y)) store_dev(a.refs + y, 1);
-          if (!more) continue;
+          if (!more) continue;   // (entries past the pages keep their values)
+          y = fresh(r, c, copied(r));
+          if (valid(y)) a.refs[y] = 1;
         }
         if (y != x) a.table[(uint64_t)r * a.max_pages + c] = y;
       }
   }
   if (enough)   // pages in columns that nobody held
     for (uint32_t e = first; e < total; e += step) {
-      const uint32_t r = segment(s_need, n, e), own = copied(r) ? 1u : 0u, i = e - s_need[r];
-      const uint32_t c = (q.keep[r] & ~kWrites) + i - own;
+      const uint32_t r = segment(s.need, n, e), own = copied(r) ? 1u : 0u, i = e - s.need[r];
+      const uint32_t c = (s.keep[r] & kKeep) + i - own;
       if (i < own || c < cols) continue;
       const int32_t p = fresh(r, c, own != 0);
-      if (valid(p)) store_dev(a.refs + p, 1);
+      if (valid(p)) a.refs[p] = 1;
       a.table[(uint64_t)r * a.max_pages + c] = p;
     }
   // ---- the rows, and the requests
   for (uint32_t i = first; i < a.m; i += step) {
-    int32_t p = -1, s = -1;
-    if (enough && i >= s_off[0] && i < s_off[n]) {
-      const uint32_t r = segment(s_off, n, i);
-      if (s_len[r] >= 0) {
-        p = s_len[r] + (int32_t)(i - s_off[r]);
+    int32_t p = -1, q = -1;
+    if (enough && i >= s.off[0] && i < s.off[n]) {
+      const uint32_t r = segment(s.off, n, i);
+      if (s.len[r] >= 0) {
+        p = s.len[r] + (int32_t)(i - s.off[r]);
         const uint32_t c = (uint32_t)p >> shift;
         const bool copy = copied(r);
-        const int32_t page = c < (q.keep[r] & ~kWrites) && !copy ? a.copies[4ull * r] : fresh(r, c, copy);
-        if (valid(page)) s = (page << shift) | (p & (int32_t)in_page);
+        const int32_t page = c < (s.keep[r] & kKeep) && !copy ? a.copies[4ull * r] : fresh(r, c, copy);
+        if (valid(page)) q = (page << shift) | (p & (int32_t)in_page);
       }
     }
     a.pos[i] = p;
-    a.slot[i] = s;
+    a.slot[i] = q;
   }
   for (uint32_t r = first; r < n; r += step)
-    a.kv_len[r] = enough && s_len[r] >= 0 ? s_len[r] + (int32_t)(s_off[r + 1] - s_off[r]) : -1;
+    a.kv_len[r] = enough && s.len[r] >= 0 ? s.len[r] + (int32_t)(s.off[r + 1] - s.off[r]) : -1;
   // what others read last: every workgroup is through with the old values
   if (none) {
     for (uint32_t r = first; r < n; r += step) *reinterpret_cast<i32x4*>(a.copies + 4ull * r) = i32x4{-1, -1, 0, 0};
@@ -417,23 +397,73 @@ __global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
   if (gridDim.x > 1) {
     if (t == 0) {
       uint32_t* const ticket = reinterpret_cast<uint32_t*>(a.state + 2);
-      s_last = __hip_atomic_fetch_add(ticket, kTicket, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+      s.last = __hip_atomic_fetch_add(ticket, kTicket, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                (gridDim.x - 1) * kTicket;
-      if (s_last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (s.last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
-    if (!s_last) return;
+    if (!s.last) return;
   }
   if (!enough) {   // nothing has changed
     for (uint32_t r = t; r < n; r += T) *reinterpret_cast<i32x4*>(a.copies + 4ull * r) = i32x4{-1, -1, 0, 0};
     return;
   }
   for (uint32_t r = t; r < n; r += T)
-    if (s_len[r] >= 0) a.held[r] = (int32_t)((q.keep[r] & ~kWrites) + s_need[r + 1] - s_need[r] - (copied(r) ? 1u : 0u));
+    if (s.len[r] >= 0) a.held[r] = (int32_t)((s.keep[r] & kKeep) + s.need[r + 1] - s.need[r] - (copied(r) ? 1u : 0u));
   if (t == 0) {
     a.state[0] = (int32_t)ring_at(total);
     a.state[1] = (int32_t)(count - total + freed);
   }
+}
+
+__device__ __forceinline__ bool no_ring(const ForkArgs& a) {
+  const int32_t head = a.state[0], count = a.state[1];
+  return head < 0 || (uint32_t)head >= a.n_pages || count < 0 || (uint32_t)count > a.n_pages || a.state[2] != 0;
+}
+
+template <int T, int N>
+__global__ __launch_bounds__(T) void k_fork_look(ForkArgs a) {
+  __shared__ ForkLds<T, N> s;
+  uint32_t* const counts = reinterpret_cast<uint32_t*>(a.refs) + 5ull * a.n_pages;
+  const bool state = no_ring(a), none = fork_requests(a, s) || state;
+  if (blockIdx.x == 0 && threadIdx.x == 0) counts[kForkWG] = none;
+  if (none) return;
+  const uint32_t freed = fork_look(a, s);
+  if (threadIdx.x == 0) counts[blockIdx.x] = freed;
+}
+
+template <int T, int N>
+__global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
+  static_assert(T >= (int)kForkWG, "a thread per workgroup's count");
+  __shared__ ForkLds<T, N> s;
+  const uint32_t* const counts = reinterpret_cast<const uint32_t*>(a.refs) + 5ull * a.n_pages;
+  const uint32_t t = threadIdx.x, v = t < gridDim.x ? counts[t] : 0u, n = a.n_req;
+  const bool none = counts[kForkWG] != 0;   // the first kernel has left everything as it was
+  if (t < 2) s.sum[t] = 0;
+  fork_requests(a, s);
+  for (uint32_t r = t; r < n; r += T)
+    if ((s.keep[r] & kWrites) && !none && a.copies[4ull * r + 2] > 0) s.keep[r] |= kCopied;
+  uint32_t before = t < blockIdx.x ? v : 0u, freed = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    before += __shfl_xor(before, o);
+    freed += __shfl_xor(freed, o);
+  }
+  if ((t & 63) == 0 && t < gridDim.x) {
+    atomicAdd(&s.sum[0], before);
+    atomicAdd(&s.sum[1], freed);
+  }
+  __syncthreads();
+  fork_apply(a, s, none, s.sum[0], s.sum[1]);
+}
+
+template <int T, int N>
+__global__ __launch_bounds__(T) void k_fork_one(ForkArgs a) {
+  __shared__ ForkLds<T, N> s;
+  const bool state = no_ring(a), none = fork_requests(a, s) || state;
+  const uint32_t freed = none ? 0u : fork_look(a, s);
+  __syncthreads();
+  fork_apply(a, s, none, 0u, freed);
 }
 
 // ------------------------------------------------------------------------------- the copies
@@ -585,7 +615,9 @@ hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
   const uint64_t work = (uint64_t)a.n_req * a.max_pages;
   uint64_t wg = ((work > a.m ? work : a.m) + 1023) / 1024;
   wg = wg < 1 ? 1 : (wg > kForkWG ? kForkWG : wg);
-  if (a.n_req <= 256) {
+  if (wg == 1 && a.n_req <= 256) {
+    hipLaunchKernelGGL((k_fork_one<256, 256>), dim3(1), dim3(256), 0, s, a);
+  } else if (a.n_req <= 256) {
     hipLaunchKernelGGL((k_fork_look<256, 256>), dim3((uint32_t)wg), dim3(256), 0, s, a);
     hipLaunchKernelGGL((k_fork_apply<256, 256>), dim3((uint32_t)wg), dim3(256), 0, s, a);
   } else {
