@@ -497,66 +497,76 @@ __global__ __launch_bounds__(kCopyT) void k_kv_copy(CopyArgs a) {
 
 // ---------------------------------------------------------------------- clearing a range
 // Three launches: the workgroups' counts; ranks of the pages that move and of the free pages
-// outside, the new ring; then the moves, the counts and the tables' names.  Bound by latency.
-struct Clear {   // of all pages, and of those before the workgroup's
+// outside, the new ring; then the moves, the counts and the tables' names.  One launch of one
+// workgroup for small pools: a third of the time at 401 pages (us: 6.1 for 16), the same at 1500 pages,
+// twice the time at 8000.  Bound by latency.
+constexpr uint32_t kClearOnePages = 2048, kClearOnePlaces = 8192;
+struct Clear {   // free pages outside the range and pages in use in it: all, and those before the workgroup's
   uint32_t out, in, out_before, in_before;
 };
 
 template <int T>
-__device__ __forceinline__ Clear clear_counts(const ClearArgs& a, uint32_t* s_sum) {
+__device__ __forceinline__ Clear clear_counts(const ClearArgs& a, uint32_t* s_w) {   // s_w [4 * T / 64]
   const uint32_t* const counts = reinterpret_cast<const uint32_t*>(a.refs) + 5ull * a.n_pages;
   const uint32_t t = threadIdx.x;
-  if (t < 4) s_sum[t] = 0;
-  __syncthreads();
+  uint32_t v[4] = {0, 0, 0, 0};
   if (t < a.blocks) {
-    const uint32_t o = counts[2 * t], i = counts[2 * t + 1];
-    atomicAdd(&s_sum[0], o);
-    atomicAdd(&s_sum[1], i);
+    v[0] = counts[2 * t];
+    v[1] = counts[2 * t + 1];
     if (t < blockIdx.x) {
-      atomicAdd(&s_sum[2], o);
-      atomicAdd(&s_sum[3], i);
+      v[2] = v[0];
+      v[3] = v[1];
     }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v[i] += __shfl_xor(v[i], o);
+    if ((t & 63) == 0) s_w[4 * (t >> 6) + i] = v[i];
+  }
   __syncthreads();
-  return Clear{s_sum[0], s_sum[1], s_sum[2], s_sum[3]};
+  Clear n{0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) {
+    n.out += s_w[4 * w];
+    n.in += s_w[4 * w + 1];
+    n.out_before += s_w[4 * w + 2];
+    n.in_before += s_w[4 * w + 3];
+  }
+  __syncthreads();
+  return n;
 }
 
-__global__ __launch_bounds__(256) void k_clear_count(ClearArgs a) {
-  __shared__ uint32_t s_w[4];
-  uint32_t* const counts = reinterpret_cast<uint32_t*>(a.refs) + 5ull * a.n_pages;
-  const uint32_t x0 = blockIdx.x * a.per, x1 = min(a.n_pages, x0 + a.per);
+// Pages x0 .. x1 - 1: free ones outside (x), in use inside (y).
+template <int T>
+__device__ __forceinline__ uint2 clear_count(const ClearArgs& a, uint32_t x0, uint32_t x1, uint32_t* s_w) {
   uint32_t out = 0, in = 0;
-  for (uint32_t x = x0 + threadIdx.x; x < x1; x += 256) {
+  for (uint32_t x = x0 + threadIdx.x; x < x1; x += T) {
     const bool inside = x - a.first < a.n_clear, live = a.refs[x] > 0;
     out += !inside && !live;
     in += inside && live;
   }
-  out = block_sum<256>(out, s_w);
-  in = block_sum<256>(in, s_w);
-  if (threadIdx.x == 0) {
-    counts[2 * blockIdx.x] = out;
-    counts[2 * blockIdx.x + 1] = in;
-  }
+  out = block_sum<T>(out, s_w);
+  in = block_sum<T>(in, s_w);
+  return uint2{out, in};
 }
 
-__global__ __launch_bounds__(256) void k_clear_rank(ClearArgs a) {
-  __shared__ uint32_t s_w[4], s_sum[4];
-  const Clear n = clear_counts<256>(a, s_sum);
+template <int T>
+__device__ __forceinline__ void clear_rank(const ClearArgs& a, const Clear& n, uint32_t x0, uint32_t x1, uint32_t* s_w) {
   if (n.in > n.out) return;
   int32_t* const rank = a.refs + 3ull * a.n_pages;
   int32_t* const target = rank + a.n_pages;
-  const uint32_t x0 = blockIdx.x * a.per, x1 = min(a.n_pages, x0 + a.per);
   uint32_t out = n.out_before, in = n.in_before;
-  for (uint32_t x = x0; x < x1; x += 256) {
+  for (uint32_t x = x0; x < x1; x += T) {
     const uint32_t p = x + threadIdx.x;
     const bool inside = p - a.first < a.n_clear, live = p < x1 && a.refs[p] > 0;
-    uint32_t some, k = block_rank<256>(p < x1 && !inside && !live, s_w, some);
+    uint32_t some, k = block_rank<T>(p < x1 && !inside && !live, s_w, some);
     if (p < x1 && !inside && !live) {
       if (out + k < n.in) target[out + k] = (int32_t)p;
       else a.ring[out + k - n.in] = (int32_t)p;
     }
     out += some;
-    k = block_rank<256>(inside && live, s_w, some);
+    k = block_rank<T>(inside && live, s_w, some);
     if (p < x1 && inside) {
       rank[p] = live ? (int32_t)(in + k) : -1;
       a.ring[n.out - n.in + (p - a.first)] = (int32_t)p;
@@ -565,9 +575,8 @@ __global__ __launch_bounds__(256) void k_clear_rank(ClearArgs a) {
   }
 }
 
-__global__ __launch_bounds__(256) void k_clear_move(ClearArgs a) {
-  __shared__ uint32_t s_sum[4];
-  const Clear n = clear_counts<256>(a, s_sum);
+template <int T>
+__device__ __forceinline__ void clear_move(const ClearArgs& a, const Clear& n) {
   const bool enough = n.in <= n.out;
   const int32_t* const rank = a.refs + 3ull * a.n_pages;
   const int32_t* const target = rank + a.n_pages;
@@ -577,7 +586,7 @@ __global__ __launch_bounds__(256) void k_clear_move(ClearArgs a) {
     return (uint32_t)k < n.in ? target[k] : -1;
   };
   const uint64_t wg = (uint64_t)blockIdx.y * gridDim.x + blockIdx.x, all = (uint64_t)gridDim.x * gridDim.y;
-  for (uint64_t i = wg * 256 + t; i < a.n_clear; i += all * 256) {
+  for (uint64_t i = wg * T + t; i < a.n_clear; i += all * T) {
     const uint32_t p = a.first + (uint32_t)i;
     const int32_t to = enough ? moved(p) : -1;
     if (to >= 0) {
@@ -587,18 +596,20 @@ __global__ __launch_bounds__(256) void k_clear_move(ClearArgs a) {
     *reinterpret_cast<i32x4*>(a.moves + 4 * i) =
         to >= 0 ? i32x4{(int32_t)p, to, (int32_t)a.page_size, 0} : i32x4{-1, -1, 0, 0};
   }
-  if (enough)
+  if (enough) {   // a wave takes 64 places of a row
+    const uint32_t wave = blockIdx.y * (T / 64) + (t >> 6), lane = t & 63, waves = gridDim.y * (T / 64);
     for (uint32_t r = blockIdx.x; r < a.max_req; r += gridDim.x) {
       const int32_t held = a.held[r];
       if (held < 0 || (uint32_t)held > a.max_pages) continue;
       int32_t* const row = a.table + (uint64_t)r * a.max_pages;
-      for (uint32_t c = blockIdx.y * 256 + t; c < (uint32_t)held; c += gridDim.y * 256) {
+      for (uint32_t c = wave * 64 + lane; c < (uint32_t)held; c += waves * 64) {
         const int32_t p = row[c];
         if ((uint32_t)p >= a.n_pages || (uint32_t)p - a.first >= a.n_clear) continue;
         const int32_t to = moved((uint32_t)p);
         if (to >= 0) row[c] = to;
       }
     }
+  }
   if (wg == 0 && t == 0) {
     *a.moved = enough ? (int32_t)n.in : -1;
     if (enough) {
@@ -608,6 +619,38 @@ __global__ __launch_bounds__(256) void k_clear_move(ClearArgs a) {
   }
 }
 
+__global__ __launch_bounds__(256) void k_clear_count(ClearArgs a) {
+  __shared__ uint32_t s_w[4];
+  uint32_t* const counts = reinterpret_cast<uint32_t*>(a.refs) + 5ull * a.n_pages;
+  const uint32_t x0 = blockIdx.x * a.per;
+  const uint2 n = clear_count<256>(a, x0, min(a.n_pages, x0 + a.per), s_w);
+  if (threadIdx.x == 0) {
+    counts[2 * blockIdx.x] = n.x;
+    counts[2 * blockIdx.x + 1] = n.y;
+  }
+}
+
+__global__ __launch_bounds__(256) void k_clear_rank(ClearArgs a) {
+  __shared__ uint32_t s_w[16];
+  const Clear n = clear_counts<256>(a, s_w);
+  const uint32_t x0 = blockIdx.x * a.per;
+  clear_rank<256>(a, n, x0, min(a.n_pages, x0 + a.per), s_w);
+}
+
+__global__ __launch_bounds__(256) void k_clear_move(ClearArgs a) {
+  __shared__ uint32_t s_w[16];
+  clear_move<256>(a, clear_counts<256>(a, s_w));
+}
+
+__global__ __launch_bounds__(1024) void k_clear_one(ClearArgs a) {
+  __shared__ uint32_t s_w[16];
+  const uint2 c = clear_count<1024>(a, 0, a.n_pages, s_w);
+  const Clear n{c.x, c.y, 0, 0};
+  clear_rank<1024>(a, n, 0, a.n_pages, s_w);
+  __syncthreads();
+  clear_move<1024>(a, n);
+}
+
 }  // namespace
 
 hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
@@ -615,7 +658,7 @@ hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
   const uint64_t work = (uint64_t)a.n_req * a.max_pages;
   uint64_t wg = ((work > a.m ? work : a.m) + 1023) / 1024;
   wg = wg < 1 ? 1 : (wg > kForkWG ? kForkWG : wg);
-  if (wg == 1 && a.n_req <= 256) {
+  if (wg == 1 && a.n_req <= 256) {   // (16 requests of 77 places, us: 20.6 in one launch, 19.0 in two)
     hipLaunchKernelGGL((k_fork_one<256, 256>), dim3(1), dim3(256), 0, s, a);
   } else if (a.n_req <= 256) {
     hipLaunchKernelGGL((k_fork_look<256, 256>), dim3((uint32_t)wg), dim3(256), 0, s, a);
@@ -635,6 +678,10 @@ hipError_t launch_kv_copy(const CopyArgs& a, uint32_t n_copies, uint32_t n_layer
 
 hipError_t launch_kv_compact(const ClearArgs& given, hipStream_t s) {
   ClearArgs a = given;
+  if (a.n_pages <= kClearOnePages && (uint64_t)a.max_req * a.max_pages <= kClearOnePlaces) {
+    hipLaunchKernelGGL(k_clear_one, dim3(1), dim3(1024), 0, s, a);
+    return hipGetLastError();
+  }
   a.per = (a.n_pages + 255) / 256;
   a.per = a.per < 256 ? 256 : a.per;
   a.blocks = (a.n_pages + a.per - 1) / a.per;
