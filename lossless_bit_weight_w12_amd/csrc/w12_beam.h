@@ -19,12 +19,16 @@ struct BeamArgs {
   uint8_t* ws;
 };
 
-// A workgroup takes 256 threads' worth of 16 or 64 values each: the small share, whose many parts a
-// row's join takes one by one, for few rows and short lists.
-constexpr uint32_t kBeamT = 256, kBeamMany = 64, kBeamFew = 16, kBeamShort = 16;
+// A workgroup takes 256 threads' worth of 16, 32 or 64 values each: the smallest share that leaves
+// at most four workgroups to a CU (us for 151936 BF16 logits, k = 8: 12 x 4 rows 20.3, 16.4, 20.4; 24 x 4
+// rows 27.6, 22.4, 20.2), and the largest for long lists and rows, whose parts a join takes up to
+// 256 of.
+constexpr uint32_t kBeamT = 256, kBeamShort = 16;
 inline uint32_t beam_values(uint32_t n, uint32_t vocab, uint32_t k) {
-  const uint64_t many = (uint64_t)n * ((vocab + kBeamT * kBeamMany - 1) / (kBeamT * kBeamMany));
-  return k > kBeamShort || vocab > (1u << 19) || many >= 512 ? kBeamMany : kBeamFew;
+  if (k > kBeamShort || vocab > (1u << 19)) return 64;
+  for (uint32_t v = 16; v < 64; v *= 2)
+    if ((uint64_t)n * ((vocab + kBeamT * v - 1) / (kBeamT * v)) <= 1024) return v;
+  return 64;
 }
 // (rows may begin anywhere in a 16-byte vector: up to 7 places more)
 inline uint32_t beam_splits(uint32_t n, uint32_t vocab, uint32_t k) {

@@ -11,11 +11,13 @@
 // candidates' ranks among themselves give their order.  Where equal values make them too many,
 // the k are taken one after the other.
 //
-// Exponentials: exp2 of the hardware on the rounded product with log2(e), and the product's
-// remainder to first order; sums of a thread in FP32, of threads and parts in FP64.  That keeps lse
-// within about 1e-8, so the choice is that of FP64 unless scores are as close as that.
+// Exponentials: exp2 of the hardware on the correctly rounded product with log2(e) (of 48 bits, so
+// that roundings have no side they prefer); sums of a thread in FP32, of threads and parts in FP64.
+// That keeps lse within about 1e-7, so the choice is that of FP64 unless scores are as close as that.
 //
 // Bound by HBM for many rows, else by the dependent steps behind the reads.
+#include <type_traits>
+
 #include "w12.h"
 #include "w12_beam.h"
 
@@ -41,30 +43,46 @@ __device__ __forceinline__ uint64_t order64(double x) {
 }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t token) { return (uint64_t)order(x) << 32 | (uint32_t)~token; }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) {
-  return (uint64_t)(uint32_t)__shfl_xor((int)(v >> 32), o) << 32 | (uint32_t)__shfl_xor((int)(uint32_t)v, o);
+// Over the wave's lanes, the result in all of them: maxima of whole numbers, sums of FP64.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));   // within rows of 16 lanes
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xf, 0xf, false));   // a row's last lane to the next row
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xf, 0xf, false));   // lane 31 to the upper half
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint64_t u = shfl_xor64(v, o);
-    v = u > v ? u : v;
-  }
-  return v;
+  const uint32_t hi = wave_max((uint32_t)(v >> 32));
+  const uint64_t with = __ballot((uint32_t)(v >> 32) == hi);
+  if ((with & (with - 1)) == 0)   // one lane alone, as a rule
+    return (uint64_t)hi << 32 | (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, __ffsll((unsigned long long)with) - 1);
+  return (uint64_t)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
 }
-template <class F>
-__device__ __forceinline__ F wave_sum(F v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+template <int C, int Rows>
+__device__ __forceinline__ double add_from(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, C, Rows, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), C, Rows, 0xf, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v = add_from<0x111, 0xf>(v);
+  v = add_from<0x112, 0xf>(v);
+  v = add_from<0x114, 0xf>(v);
+  v = add_from<0x118, 0xf>(v);
+  v = add_from<0x142, 0xa>(v);
+  v = add_from<0x143, 0xc>(v);
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), 63) << 32 |
+                                        (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63));
 }
 
 // exp(t), t <= 0.
 __device__ __forceinline__ float exp_of(float t) {
   constexpr float kL = 1.44269502f, kLow = 1.92596299e-8f;   // log2(e)
-  const float h = t * kL, r = fmaf(t, kL, -h) + t * kLow;
-  const float e = __builtin_amdgcn_exp2f(h);
-  return t > -100.f ? fmaf(e, r * 0.693147181f, e) : e;   // (t = -inf has no remainder)
+  return __builtin_amdgcn_exp2f(fmaf(t, kL, t * kLow));
 }
 
 struct Part {   // of a row, in the workspace
@@ -80,7 +98,7 @@ __device__ __forceinline__ void store_dev(F* p, F v) { __hip_atomic_store(p, v, 
 
 // V values per vector of 16 bytes, N values of a thread, lists of up to K.
 template <bool F32, int N, int K>
-__global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
+__global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
   constexpr int V = F32 ? 4 : 8, U = N / V, T = (int)kBeamT, W = T / 64;
   constexpr uint32_t kKeys = K > 16 ? 1024 : 640;   // keys of one row in LDS, per wave
   __shared__ union {
@@ -141,13 +159,17 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
   __syncthreads();
   {
     bool bad = false;
-    uint32_t before = 0;
-    for (uint32_t g = t; g <= a.n_grp; g += T) {
-      const int32_t o = a.grp_off[g], next = g < a.n_grp ? a.grp_off[g + 1] : o;
-      bad |= o < 0 || next < o || o > (int32_t)a.n || next - o > W12_MAX_BEAMS;
-      before += o <= (int32_t)row;
+    uint32_t before = 0;   // groups that begin at this row or before it
+    for (uint32_t g0 = 0; g0 <= a.n_grp; g0 += T) {
+      const uint32_t g = g0 + t;
+      bool here = false;
+      if (g <= a.n_grp) {
+        const int32_t o = a.grp_off[g], next = a.grp_off[g < a.n_grp ? g + 1 : g];
+        bad |= o < 0 || next < o || o > (int32_t)a.n || next - o > W12_MAX_BEAMS;
+        here = o <= (int32_t)row;
+      }
+      before += (uint32_t)__popcll(__ballot(here));
     }
-    before = wave_sum(before);
     if (lane == 0 && before) atomicAdd(&s_grp, before);
     bad = __syncthreads_or(bad);
     if (split == 0 && row == 0)   // groups without rows, and a table that is none
@@ -159,16 +181,18 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
       }
     if (bad || row >= a.n || s_grp == 0 || s_grp > a.n_grp) return;
   }
-  const uint32_t grp = s_grp - 1;
+  const uint32_t grp = s_grp - 1, r0 = (uint32_t)a.grp_off[grp], rows = (uint32_t)a.grp_off[grp + 1] - r0;
 
   // ---- maximum, sum, and a bound that at least k values reach
   bool any = false;
-  float most = -INFINITY;
+  float most = -INFINITY, vec[U];   // of the vectors too
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     any |= (int32_t)token(i, 0) > -V && (int32_t)token(i, 0) < (int32_t)a.vocab;   // (a vector may hold more than the row)
+    vec[i] = at(i, 0);
 #pragma unroll
-    for (int j = 0; j < V; ++j) most = fmaxf(most, at(i, j));
+    for (int j = 1; j < V; ++j) vec[i] = fmaxf(vec[i], at(i, j));
+    most = fmaxf(most, vec[i]);
   }
   s.part.most[t] = any ? most : NAN;
   __syncthreads();
@@ -182,8 +206,8 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
       most = fmaxf(most, f[i]);
     }
   }
-#pragma unroll
-  for (int i = 1; i < 64; i <<= 1) most = fmaxf(most, __shfl_xor(most, i));
+  const uint32_t top = wave_max(order(most));
+  most = value(top);
   auto reach = [&](uint32_t v) {
     uint32_t c = 0;
 #pragma unroll
@@ -192,12 +216,9 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
   };
   uint32_t bound = 1;
   if (reach(1) > k) {
-    uint32_t hi = order(most) + 1;
-    bound = min(min(o[0] ? o[0] : ~0u, o[1] ? o[1] : ~0u), min(o[2] ? o[2] : ~0u, o[3] ? o[3] : ~0u));
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) bound = min(bound, (uint32_t)__shfl_xor((int)bound, i));
-    bound = __builtin_amdgcn_readfirstlane((int)bound);
-    hi = __builtin_amdgcn_readfirstlane((int)hi);
+    uint32_t hi = top + 1;
+    const uint32_t low = min(min(o[0] - 1, o[1] - 1), min(o[2] - 1, o[3] - 1));   // (0, none, wraps round)
+    bound = ~wave_max(~low) + 1;
     while (hi - bound > 1) {
       const uint32_t mid = bound + (hi - bound) / 2, c = reach(mid);
       if (c < k) {
@@ -208,6 +229,11 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
       }
     }
   }
+  auto packed = [&] {   // values are taken from the vectors anew, rather than held
+#pragma unroll
+    for (int i = 0; i < U; ++i) asm volatile("" : "+v"(raw[i]));
+  };
+  packed();
   const float shift = most == -INFINITY ? 0.f : most;
   float sum = 0.f;
 #pragma unroll
@@ -218,19 +244,27 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
   if (lane == 0) s_sum[wave] = all;
 
   // ---- candidates, and the k best of them in order
-  const bool plain = bound > order(-INFINITY);   // no NaN, no place outside the row reaches it
-  const float at_least = value(bound);
+  packed();
+  auto found = [&](float x, uint32_t tok) {
+    const uint32_t c = atomicAdd(&s_count, 1u);
+    if (c < kCand) s.part.cand[c] = key_of(x, tok);
+  };
+  if (bound > order(-INFINITY)) {   // no NaN, no place outside the row reaches it
+    const float at_least = value(bound);
 #pragma unroll
-  for (int i = 0; i < U; ++i)
+    for (int i = 0; i < U; ++i)
+      if (vec[i] >= at_least) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float x = at(i, j);
-      const bool on = plain ? x >= at_least : token(i, j) < a.vocab && order(x) >= bound;
-      if (on) {
-        const uint32_t c = atomicAdd(&s_count, 1u);
-        if (c < kCand) s.part.cand[c] = key_of(x, token(i, j));
+        for (int j = 0; j < V; ++j)
+          if (at(i, j) >= at_least) found(at(i, j), token(i, j));
       }
-    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (token(i, j) < a.vocab && order(at(i, j)) >= bound) found(at(i, j), token(i, j));
+  }
   __syncthreads();
   const uint64_t mine = (uint64_t)row * S + split;
   uint64_t* const list = lists + mine * k;
@@ -254,13 +288,18 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
     uint64_t last = ~0ull;
     for (uint32_t r = 0; r < k; ++r) {
       uint64_t best = 0;
+      packed();
+      uint32_t tok = token_0;
+      asm volatile("" : "+v"(tok));   // (nor are the tokens held)
 #pragma unroll
-      for (int i = 0; i < U; ++i)
+      for (int i = 0; i < U; ++i) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const uint64_t key = key_of(at(i, j), token(i, j));
-          if (token(i, j) < a.vocab && key < last && key > best) best = key;
+          const uint64_t key = key_of(at(i, j), tok + i * T * V + j);
+          if (tok + i * T * V + j < a.vocab && key < last && key > best) best = key;
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
       best = wave_max64(best);
       if (lane == 0) s_best[wave] = best;
       __syncthreads();
@@ -275,9 +314,8 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
   // ---- the group's last workgroup joins
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  const uint32_t r0 = (uint32_t)a.grp_off[grp], rows = (uint32_t)a.grp_off[grp + 1] - r0;
   if (t == 0) {
-    uint32_t* const ticket = reinterpret_cast<uint32_t*>(a.ws) + grp;
+    uint32_t* const ticket = reinterpret_cast<uint32_t*>(a.ws) + grp * (4096 / a.n_grp);
     s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == rows * S - 1;
     if (s_last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
@@ -290,79 +328,107 @@ __global__ __launch_bounds__(kBeamT) void k_beam(BeamArgs a) {
     const bool in_lds = S * k <= kKeys;
     if (in_lds)
       for (uint32_t i = lane; i < S * k; i += 64) s.join.keys[wave][i] = load_dev(from + i);
-    float top = -INFINITY;
-    for (uint32_t i = lane; i < S; i += 64) top = fmaxf(top, load_dev(&parts[first + i].top));
+    float tops[4];
+    double sums[4];
 #pragma unroll
-    for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i));
+    for (uint32_t i = 0; i < 4; ++i) {
+      const bool on = lane + 64 * i < S;
+      tops[i] = on ? load_dev(&parts[first + lane + 64 * i].top) : -INFINITY;
+      sums[i] = on ? load_dev(&parts[first + lane + 64 * i].sum) : 0.0;
+    }
+    const float top = value(wave_max(order(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])))));
     const double to = top == -INFINITY ? 0.0 : (double)top;
     double v = 0;
-    for (uint32_t i = lane; i < S; i += 64) {
-      const float x = load_dev(&parts[first + i].top);
-      const double y = load_dev(&parts[first + i].sum);
-      v += x == -INFINITY ? y : y * exp((double)x - to);   // (0, or NaN that stays)
-    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (64u * i < S) v += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)tops[i] - to);   // (0, or NaN that stays)
     v = wave_sum(v);
     if (lane == 0) s.join.lse[b] = (top == -INFINITY ? -(double)INFINITY : to) + log(v);
-    auto key = [&](uint32_t l, uint32_t p) -> uint64_t {
-      if (l >= S || p >= k) return 0;
-      return in_lds ? s.join.keys[wave][l * k + p] : load_dev(from + l * k + p);
-    };
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();   // one wave writes and reads: LDS keeps the order
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    uint64_t head[4];
-    uint32_t pos[4] = {0, 0, 0, 0};
+    // Every lane has the head of a list, and the one behind it before it is asked for; without
+    // branches: 64 of 640 keys in 6 us, in 14 where only the lane that won read on.
+    auto merge = [&](auto heads, auto key) {
+      constexpr int H = decltype(heads)::value;
+      uint64_t head[H], next[H], mine = 0;
+      uint32_t pos[H];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) head[i] = key(lane + 64 * i, 0);
-    for (uint32_t r = 0; r < k; ++r) {
-      uint64_t best = head[0];
+      for (int i = 0; i < H; ++i) {
+        head[i] = key(lane + 64 * i, 0u);
+        next[i] = key(lane + 64 * i, 1u);
+        pos[i] = 1;
+      }
+      for (uint32_t r = 0; r < k; ++r) {
+        uint64_t best = head[0];
 #pragma unroll
-      for (int i = 1; i < 4; ++i) best = head[i] > best ? head[i] : best;
-      const uint64_t won = wave_max64(best);
-      if (lane == 0) s.join.rows[b][r] = won;
+        for (int i = 1; i < H; ++i) best = head[i] > best ? head[i] : best;
+        const uint64_t won = wave_max64(best);
+        mine = lane == r ? won : mine;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (won && head[i] == won) head[i] = key(lane + 64 * i, ++pos[i]);   // keys are distinct
-    }
+        for (int i = 0; i < H; ++i) {
+          const bool here = head[i] == won;   // keys are distinct but for 0, which nothing follows
+          head[i] = here ? next[i] : head[i];
+          pos[i] += here;
+          next[i] = key(lane + 64 * i, pos[i]);
+        }
+      }
+      if (lane < k) s.join.rows[b][lane] = mine;
+    };
+    auto near = [&](uint32_t l, uint32_t p) {
+      const bool on = l < S && p < k;
+      const uint64_t v = s.join.keys[wave][on ? l * k + p : 0u];
+      return on ? v : (uint64_t)0;
+    };
+    auto far = [&](uint32_t l, uint32_t p) { return l < S && p < k ? load_dev(from + l * k + p) : (uint64_t)0; };
+    if (!in_lds) merge(std::integral_constant<int, 4>(), far);
+    else if (S > 64) merge(std::integral_constant<int, 4>(), near);
+    else merge(std::integral_constant<int, 1>(), near);
   }
   __syncthreads();
   if (wave != 0) return;
   // a lane per row: the best score of all, lower rows first
   const bool on = lane < rows;
-  const double base_score = on ? (double)a.scores[r0 + lane] : 0.0;
-  uint32_t pos = 0;
-  uint64_t key = 0, ord = 0;
-  double score = 0;
-  auto next = [&] {
-    key = on && pos < k ? s.join.rows[lane][pos] : 0;
-    score = base_score + ((double)value((uint32_t)(key >> 32)) - s.join.lse[lane]);
-    score = score == score ? score : -(double)INFINITY;
-    ord = key ? order64(score) : 0;
-    ++pos;
+  const double base_score = on ? (double)a.scores[r0 + lane] : 0.0, lse = on ? s.join.lse[lane] : 0.0;
+  uint32_t pos = 1;
+  auto ahead = [&](uint32_t p) {
+    const uint64_t v = s.join.rows[on ? lane : 0u][p < k ? p : 0u];
+    return on && p < k ? v : (uint64_t)0;
   };
-  next();
+  uint64_t key = ahead(0), next = ahead(1);
+  int32_t parent = -1, tok = -1;   // of the lane's place in the answer
+  float out = -INFINITY;
   for (uint32_t r = 0; r < k; ++r) {
-    const uint64_t won = wave_max64(ord), tied = __ballot(ord == won);
-    const uint64_t out = (uint64_t)grp * k + r;
-    if (won == 0) {
-      if (lane == 0) {
-        a.parent[out] = a.token[out] = -1;
-        a.out[out] = -INFINITY;
-      }
-    } else if ((int)lane == __ffsll((unsigned long long)tied) - 1) {
-      a.parent[out] = (int32_t)(r0 + lane);
-      a.token[out] = (int32_t)~(uint32_t)key;
-      a.out[out] = (float)score;
-      next();
+    double score = base_score + ((double)value((uint32_t)(key >> 32)) - lse);
+    score = score == score ? score : -(double)INFINITY;
+    const uint64_t ord = key ? order64(score) : 0, won = wave_max64(ord);
+    if (won == 0) break;
+    const int w = __ffsll((unsigned long long)__ballot(ord == won)) - 1;
+    const int32_t token_w = (int32_t)~(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, w);
+    const float score_w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint((float)score), w));
+    if (lane == r) {
+      parent = (int32_t)r0 + w;
+      tok = token_w;
+      out = score_w;
     }
+    const bool here = (int)lane == w;
+    key = here ? next : key;
+    pos += here;
+    next = ahead(pos);
+  }
+  if (lane < k) {
+    const uint64_t at_out = (uint64_t)grp * k + lane;
+    a.parent[at_out] = parent;
+    a.token[at_out] = tok;
+    a.out[at_out] = out;
   }
 }
 
 template <bool F32, int N>
 hipError_t beam_go(const BeamArgs& a, hipStream_t s) {
   const dim3 grid(a.splits, a.n ? a.n : 1);
-  if (a.k <= kBeamShort) hipLaunchKernelGGL((k_beam<F32, N, (int)kBeamShort>), grid, dim3(kBeamT), 0, s, a);
-  else hipLaunchKernelGGL((k_beam<F32, N, W12_MAX_BEAM_K>), grid, dim3(kBeamT), 0, s, a);
+  if (N < 64 || a.k <= kBeamShort) hipLaunchKernelGGL((k_beam<F32, N, (int)kBeamShort>), grid, dim3(kBeamT), 0, s, a);
+  else if constexpr (N == 64) hipLaunchKernelGGL((k_beam<F32, N, W12_MAX_BEAM_K>), grid, dim3(kBeamT), 0, s, a);
   return hipGetLastError();
 }
 
@@ -371,9 +437,11 @@ hipError_t beam_go(const BeamArgs& a, hipStream_t s) {
 hipError_t launch_beam_select(const BeamArgs& given, bool f32, hipStream_t s) {
   BeamArgs a = given;
   a.splits = beam_splits(a.n, a.vocab, a.k);
-  const bool many = beam_values(a.n, a.vocab, a.k) == kBeamMany;
-  if (f32) return many ? beam_go<true, (int)kBeamMany>(a, s) : beam_go<true, (int)kBeamFew>(a, s);
-  return many ? beam_go<false, (int)kBeamMany>(a, s) : beam_go<false, (int)kBeamFew>(a, s);
+  switch (beam_values(a.n, a.vocab, a.k)) {
+    case 16: return f32 ? beam_go<true, 16>(a, s) : beam_go<false, 16>(a, s);
+    case 32: return f32 ? beam_go<true, 32>(a, s) : beam_go<false, 32>(a, s);
+    default: return f32 ? beam_go<true, 64>(a, s) : beam_go<false, 64>(a, s);
+  }
 }
 
 }  // namespace w12

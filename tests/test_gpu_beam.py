@@ -1,7 +1,7 @@
 """The choice of beams on the GPU against the 64-bit oracle.  Rows and tokens have to be equal unless two
-rows' scores are closer than 1e-7 (a row's log-sum-exp is within 1e-8: every term's exponential is off
-by 2^-23 at most, in either direction, the FP32 sums of at most 64 terms of a thread by 2^-24 of them
-per addition, likewise, and both are averaged over the row); the inputs here are drawn so that none
+rows' scores are closer than 1e-7 (what a row's log-sum-exp is within: a term exp(t) is off by 2^-23 of
+itself and 2^-24 |t| exp(t), in either direction, the FP32 sums of at most 64 terms of a thread by
+2^-24 of them per addition, likewise, and all of them are averaged over the row); the inputs here are drawn so that none
 are.  Scores are rounded to FP32: 2^-24 of them, and 1e-7 for the log-sum-exp."""
 import numpy as np
 import pytest
