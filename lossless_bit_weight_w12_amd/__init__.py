@@ -2,7 +2,9 @@
 verification with a certified exact-argmax LM head, in one pass over the W12 head or in
 two levels (an 8-bit screen copy first), the GEMMs of FP8 targets (E4M3 weights with
 128 x 128 block scales) in the same kernel family, and the attention side of a decode step
-(block tables, norm and rotation with the cache append, attention over the paged cache).
+(block tables, norm and rotation with the cache append, attention over the paged cache), also of
+several continuations of one prompt (shared pages and their copies, attention that reads shared
+tokens once, the choice of beams).
 The compute lives in libw12.so (HIP kernels for gfx950 behind a C ABI, declared in
 include/w12.h); this package is its thin Python binding."""
 from .w12 import (ATTN_WS_BYTES, ENCODE_TOTAL_OFFSET, EXPORTS, F8Tensor, KV_BF16, KV_E4M3,

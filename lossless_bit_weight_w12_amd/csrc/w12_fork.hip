@@ -180,7 +180,8 @@ __device__ __forceinline__ void entry(const ForkArgs& a, const ForkLds<T, N>& s,
 // atomic, so a prompt's shared pages cost nothing.
 //
 // Two launches, or one where a single workgroup takes all columns.  Bound by latency (dependent
-// reads behind the launches).
+// reads behind the launches): 4 requests 9 us in one launch, 96 of 265 places 21 us in two (9 and 13 on the
+// GPU; 28 with the counts per page at the device's scope, that is past the L2).
 struct Columns {   // of a workgroup, and how many of them are in LDS at a time
   uint32_t begin, end, width;
 };
