@@ -215,6 +215,21 @@ def test_a_longest_table():
     assert (np.abs(host(x.run()) - want) <= tol + 2.0 ** -10 * np.abs(host(x.c.v)).max()).all()
 
 
+@pytest.mark.parametrize("n,f8", [(3, False), (40, False), (40, True)])
+def test_pages_beyond_32_bits(n, f8):
+    """Pages whose offset within the cache passes 2^32 bytes: the bits of the same pages at its start."""
+    x = Group(np.random.default_rng(66), [beams(n, 400, 30, 1)], 8, 8, 128, 16, f8, only_first=False)
+    want = x.run().clone()
+    small, total = x.c, 280000 if f8 else 140000
+    k, v = (torch.empty((total, *t.shape[1:]), dtype=t.dtype, device=DEV) for t in (small.k, small.v))
+    at = total - small.k.shape[0]
+    k[at:].view(torch.uint8).copy_(small.k.view(torch.uint8))
+    v[at:].view(torch.uint8).copy_(small.v.view(torch.uint8))
+    x.c = w12.KvCache(k, v, small.k_scale, small.v_scale)
+    x.seen = np.where(x.seen >= 0, x.seen + at, x.seen)
+    assert torch.equal(x.run(out=torch.full_like(want, 7)), want)
+
+
 def test_streams_and_captured_graphs():
     """Two streams at once, and two graphs replayed beside eager calls: no workspace is shared."""
     g = np.random.default_rng(63)

@@ -42,7 +42,7 @@ def logits(g, n, vocab, f32, scale=2.5):
     ([1], 1, 1), ([2], 3, 3), ([1], 7, 7), ([4], 64, 64), ([4, 1, 0, 3], 1000, 8), ([2, 2], 4095, 5), ([3], 4097, 16),
     ([3], 4096, 17), ([5, 5], 16383, 64), ([1, 1, 1], 16385, 33), ([4] * 3, 50257, 8), ([16, 2], 32001, 32),
     ([64], 5003, 64), ([64], 20011, 16), ([4], 151936, 8), ([4] * 24, 30011, 8), ([1] * 60, 151, 4), ([2], 700001, 64),
-    ([1], 1 << 21, 16)])
+    ([1], 1 << 21, 16), ([2], 300007, 4), ([8] * 10, 60000, 12), ([2], 90001, 16)])
 def test_choice(rows, vocab, k, f32):
     print("beam_select", rows, vocab, k, f32, flush=True)
     g = np.random.default_rng([71, vocab, k, f32])

@@ -110,6 +110,29 @@ def test_fork_reorders_beams(n_req, max_pages):
         tokens = tokens[parent] + 1
 
 
+@pytest.mark.parametrize("n_req,max_pages", [(256, 9000), (4096, 600)])
+def test_fork_of_more_columns_than_fit_at_once(n_req, max_pages):
+    """A few requests hold almost every column, so that a workgroup takes its columns in turns."""
+    g = np.random.default_rng(n_req + 1)
+    n_pages = 8 * max_pages + 4 * n_req
+    p = Pool(n_pages, 16, n_req, max_pages, head=n_pages - 5)
+    rows = g.integers(1, 20, n_req)
+    long = g.permutation(n_req)[:3]
+    rows[long] = 16 * max_pages - g.integers(20, 40, 3)
+    p.fork(None, np.zeros(n_req), offsets(rows), int(rows.sum()))
+    tokens = rows
+    for i in range(3):
+        parent = np.arange(n_req)
+        some = g.permutation(n_req)[:n_req // 3]
+        parent[some] = long[i]
+        parent[long[(i + 1) % 3]] = some[0]
+        length = np.minimum(tokens[parent], g.integers(1, 16 * max_pages, n_req)) if i == 1 else tokens[parent]
+        out = p.fork(parent, length, np.arange(n_req + 1), n_req)
+        assert (out[0] == length + 1).all()
+        tokens = length + 1
+        long = some[:3]
+
+
 def test_fork_refuses_a_request():
     """Lengths, parents and counts that are none refuse their request alone."""
     p = Pool(60, 16, 8, 5)
@@ -175,6 +198,18 @@ def test_copies_of_all_layers(page, heads, dim, layers, f8):
     wk, wv = k.numpy().copy(), v.numpy().copy()
     fo.kv_copy(wk, wv, copies)
     assert np.array_equal(cpu(dk), wk) and np.array_equal(cpu(dv), wv)
+
+
+def test_copies_beyond_32_bits():
+    """Pages whose offset within a cache passes 2^32 bytes."""
+    n_pages, heads, dim, page = 140000, 8, 128, 16
+    k, v = (torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in ((n_pages, heads, page, dim), (n_pages, heads, dim, page)))
+    ends = torch.arange(heads * page * dim, device=DEV).bfloat16()
+    for i in (3, n_pages - 2):
+        k[i], v[i] = (ends + i % 7).view(heads, page, dim), (ends - i % 5).view(heads, dim, page)
+    w12.kv_copy([w12.KvCache(k, v)], i32([[n_pages - 2, 5, 16, 0], [3, n_pages - 1, 16, 0]]))
+    assert torch.equal(k[5], k[n_pages - 2]) and torch.equal(v[5], v[n_pages - 2])
+    assert torch.equal(k[n_pages - 1], k[3]) and torch.equal(v[n_pages - 1], v[3])
 
 
 def test_copies_of_none():
