@@ -18,6 +18,7 @@ struct ForkArgs {
   const int32_t* len;      // [n_req]
   const int32_t* req_off;  // [n_req + 1]
   uint32_t n_req, m;
+  uint32_t grid, n_inv, at_once;   // workgroups, the inverse of n_req, columns in LDS; set by the launch
   int32_t* kv_len;         // [n_req]
   int32_t* pos;            // [m]
   int32_t* slot;           // [m]

@@ -20,6 +20,13 @@ constexpr uint32_t kForkWG = 256;        // workgroups of a launch, at most (one
 constexpr uint32_t kEntries = 8192;      // table entries of a workgroup in LDS at a time
 constexpr uint32_t kWriter = 0x10000u;   // a mark of a request that writes
 
+// x / d, for x d < 2^32: inv = floor((2^32 - 1) / d) is less than 2^32 / d by 1 at most, the product by less
+// than x / 2^32 + 1, so the quotient is it or one more.
+__device__ __forceinline__ uint32_t divide(uint32_t x, uint32_t d, uint32_t inv) {
+  const uint32_t q = __umulhi(x, inv);
+  return q + (x - q * d >= d);
+}
+
 // Words that one workgroup alone uses in a launch.
 __device__ __forceinline__ int32_t load_here(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
@@ -147,8 +154,9 @@ __device__ __forceinline__ bool fork_requests(const ForkArgs& a, ForkLds<T, N>& 
 template <int T, int N>
 __device__ __forceinline__ void fork_columns(const ForkArgs& a, ForkLds<T, N>& s, uint32_t c0, uint32_t w) {
   __syncthreads();
+  const uint32_t inv = 0xffffffffu / w;
   for (uint32_t e = threadIdx.x; e < w * a.n_req; e += T) {
-    const uint32_t r = e / w, j = e - r * w;
+    const uint32_t r = divide(e, w, inv), j = e - r * w;
     s.old[j * a.n_req + r] = c0 + j < s.held[r] ? a.table[(uint64_t)r * a.max_pages + c0 + j] : -1;
   }
   __syncthreads();
@@ -187,8 +195,18 @@ struct Columns {   // of a workgroup, and how many of them are in LDS at a time
 };
 template <int T, int N>
 __device__ __forceinline__ Columns columns(const ForkArgs& a, const ForkLds<T, N>& s) {
-  const uint32_t per = (s.cols + gridDim.x - 1) / gridDim.x;
-  return Columns{blockIdx.x * per, min(s.cols, (blockIdx.x + 1) * per), max(1u, min(per, kEntries / a.n_req))};
+  const uint32_t per = a.grid == 1 ? s.cols : (s.cols + a.grid - 1) / a.grid;
+  return Columns{blockIdx.x * per, min(s.cols, (blockIdx.x + 1) * per), max(1u, min(per, a.at_once))};
+}
+
+// A page in the middle of a call: its mark, and who will hold it but for those that write into it (read
+// together: one read less to wait for).
+struct Page {
+  int32_t mark, holders;
+};
+__device__ __forceinline__ Page page_now(const ForkArgs& a, int32_t p) {
+  const int32_t change = load_here(a.refs + a.n_pages + p), mark = load_here(a.refs + 2ull * a.n_pages + p);
+  return Page{mark, a.refs[p] + change};
 }
 
 // The first half: the number of pages that this workgroup's columns give back.
@@ -199,13 +217,14 @@ __device__ __forceinline__ uint32_t fork_look(const ForkArgs& a, ForkLds<T, N>& 
   int32_t* const mark = delta + a.n_pages;
   uint32_t freed = 0;
   auto valid = [&](int32_t p) { return (uint32_t)p < a.n_pages; };
+  auto page = [&](int32_t p, bool read) { return read ? page_now(a, p) : Page{0, 0}; };
   const Columns k = columns(a, s);
   for (uint32_t c0 = k.begin; c0 < k.end; c0 += k.width) {
     const uint32_t w = min(k.width, k.end - c0), all = w * n;
     fork_columns(a, s, c0, w);
     bool any = false;
     for (uint32_t e = t; e < all; e += T) {
-      const uint32_t j = e / n, r = e - j * n;
+      const uint32_t j = divide(e, n, a.n_inv), r = e - j * n;
       int32_t x, y;
       bool tail;
       entry(a, s, r, j, c0 + j, x, y, tail);
@@ -222,14 +241,15 @@ __device__ __forceinline__ uint32_t fork_look(const ForkArgs& a, ForkLds<T, N>& 
     }
     if (!__syncthreads_or(any)) continue;
     for (uint32_t e = t; e < all; e += T) {
-      const uint32_t j = e / n, r = e - j * n;
+      const uint32_t j = divide(e, n, a.n_inv), r = e - j * n;
       int32_t x, y;
       bool tail;
       entry(a, s, r, j, c0 + j, x, y, tail);
       if (x == y && !tail) continue;
-      if (valid(x)) freed += load_here(mark + x) == (int32_t)(n - r) && a.refs[x] + load_here(delta + x) == 0;
+      const Page at_x = page(x, valid(x)), at_y = page(y, tail && valid(y));
+      freed += at_x.mark == (int32_t)(n - r) && at_x.holders == 0;
       if (tail) {   // the lowest of those that write keeps a page that nobody else holds
-        const bool stays = !valid(y) || (load_here(mark + y) == (int32_t)(kWriter + n - r) && a.refs[y] + load_here(delta + y) == 0);
+        const bool stays = !valid(y) || (at_y.mark == (int32_t)(kWriter + n - r) && at_y.holders == 0);
         const int32_t part = s.len[r] & ((1 << a.page_shift) - 1);
         if (!stays) atomicOr(&s.keep[r], kCopied);
         *reinterpret_cast<i32x4*>(a.copies + 4ull * r) = i32x4{y, y, stays ? 0 : part, 0};
@@ -242,17 +262,18 @@ __device__ __forceinline__ uint32_t fork_look(const ForkArgs& a, ForkLds<T, N>& 
   return block_sum<T>(freed, s.w);
 }
 
-// The second half.  none: the first one has found a table that is none; before, freed: pages given back
+// The second half.  ring: its head and count as they were; none: the first one has found a table that is none; before, freed: pages given back
 // by the workgroups before and by all.
 template <int T, int N>
-__device__ __forceinline__ void fork_apply(const ForkArgs& a, ForkLds<T, N>& s, bool none, uint32_t before, uint32_t freed) {
+__device__ __forceinline__ void fork_apply(const ForkArgs& a, ForkLds<T, N>& s, uint2 ring, bool none, uint32_t before,
+                                           uint32_t freed) {
   constexpr uint32_t kPer = N / T;
   const uint32_t t = threadIdx.x, n = a.n_req, lane = t & 63, wave = t >> 6, cols = s.cols;
-  const uint32_t first = blockIdx.x * T + t, step = gridDim.x * T;   // of the flat lists
+  const uint32_t first = blockIdx.x * T + t, step = a.grid * T;   // of the flat lists
   int32_t* const delta = a.refs + a.n_pages;
   int32_t* const mark = delta + a.n_pages;
   const uint32_t shift = a.page_shift, in_page = (1u << shift) - 1u;
-  const uint32_t head = (uint32_t)a.state[0], count = (uint32_t)a.state[1];
+  const uint32_t head = ring.x, count = ring.y;
   const uint32_t per_t = (n + T - 1) / T;
   uint32_t need[kPer], sum = 0;
 #pragma unroll
@@ -311,12 +332,13 @@ __device__ __forceinline__ void fork_apply(const ForkArgs& a, ForkLds<T, N>& s, 
       bool tail = false;
       uint32_t r = 0;
       if (e < all) {
-        const uint32_t j = e / n;
+        const uint32_t j = divide(e, n, a.n_inv);
         r = e - j * n;
         entry(a, s, r, j, c0 + j, x, y, tail);
       }
       const bool moves = e < all && (x != y || tail);
-      const bool gone = moves && valid(x) && load_here(mark + x) == (int32_t)(n - r) && a.refs[x] + load_here(delta + x) == 0;
+      const Page now = moves && valid(x) ? page_now(a, x) : Page{0, 0};
+      const bool gone = now.mark == (int32_t)(n - r) && now.holders == 0 && moves;
       any |= moves;
       if (__syncthreads_or(gone)) {
         uint32_t some;
@@ -329,7 +351,7 @@ __device__ __forceinline__ void fork_apply(const ForkArgs& a, ForkLds<T, N>& s, 
     // the counts, and the call's own words back to zero
     if (any)
       for (uint32_t e = t; e < all; e += T) {
-        const uint32_t j = e / n, r = e - j * n;
+        const uint32_t j = divide(e, n, a.n_inv), r = e - j * n;
         int32_t x, y;
         bool tail;
         entry(a, s, r, j, c0 + j, x, y, tail);
@@ -342,9 +364,10 @@ __device__ __forceinline__ void fork_apply(const ForkArgs& a, ForkLds<T, N>& s, 
         if (valid(x)) delta[x] = mark[x] = 0;
         if (valid(y)) delta[y] = mark[y] = 0;
       }
+    const uint32_t inv = 0xffffffffu / w;
     if (enough)
       for (uint32_t e = t; e < all; e += T) {
-        const uint32_t r = e / w, j = e - r * w, c = c0 + j;
+        const uint32_t r = divide(e, w, inv), j = e - r * w, c = c0 + j;
         int32_t x, y;
         bool tail;
         entry(a, s, r, j, c, x, y, tail);
@@ -395,11 +418,11 @@ __device__ __forceinline__ void fork_apply(const ForkArgs& a, ForkLds<T, N>& s, 
     return;
   }
   __syncthreads();
-  if (gridDim.x > 1) {
+  if (a.grid > 1) {
     if (t == 0) {
       uint32_t* const ticket = reinterpret_cast<uint32_t*>(a.state + 2);
       s.last = __hip_atomic_fetch_add(ticket, kTicket, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               (gridDim.x - 1) * kTicket;
+               (a.grid - 1) * kTicket;
       if (s.last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
@@ -438,8 +461,9 @@ __global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
   static_assert(T >= (int)kForkWG, "a thread per workgroup's count");
   __shared__ ForkLds<T, N> s;
   const uint32_t* const counts = reinterpret_cast<const uint32_t*>(a.refs) + 5ull * a.n_pages;
-  const uint32_t t = threadIdx.x, v = t < gridDim.x ? counts[t] : 0u, n = a.n_req;
+  const uint32_t t = threadIdx.x, v = t < a.grid ? counts[t] : 0u, n = a.n_req;
   const bool none = counts[kForkWG] != 0;   // the first kernel has left everything as it was
+  const uint2 ring = {(uint32_t)a.state[0], (uint32_t)a.state[1]};
   if (t < 2) s.sum[t] = 0;
   fork_requests(a, s);
   for (uint32_t r = t; r < n; r += T)
@@ -450,21 +474,22 @@ __global__ __launch_bounds__(T) void k_fork_apply(ForkArgs a) {
     before += __shfl_xor(before, o);
     freed += __shfl_xor(freed, o);
   }
-  if ((t & 63) == 0 && t < gridDim.x) {
+  if ((t & 63) == 0 && t < a.grid) {
     atomicAdd(&s.sum[0], before);
     atomicAdd(&s.sum[1], freed);
   }
   __syncthreads();
-  fork_apply(a, s, none, s.sum[0], s.sum[1]);
+  fork_apply(a, s, ring, none, s.sum[0], s.sum[1]);
 }
 
 template <int T, int N>
 __global__ __launch_bounds__(T) void k_fork_one(ForkArgs a) {
   __shared__ ForkLds<T, N> s;
+  const uint2 ring = {(uint32_t)a.state[0], (uint32_t)a.state[1]};
   const bool state = no_ring(a), none = fork_requests(a, s) || state;
   const uint32_t freed = none ? 0u : fork_look(a, s);
   __syncthreads();
-  fork_apply(a, s, none, 0u, freed);
+  fork_apply(a, s, ring, none, 0u, freed);
 }
 
 // ------------------------------------------------------------------------------- the copies
@@ -656,11 +681,15 @@ __global__ __launch_bounds__(1024) void k_clear_one(ClearArgs a) {
 
 }  // namespace
 
-hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
+hipError_t launch_kv_fork(const ForkArgs& given, hipStream_t s) {
+  ForkArgs a = given;
   // a workgroup for every 1024 places of the tables, or rows
   const uint64_t work = (uint64_t)a.n_req * a.max_pages;
   uint64_t wg = ((work > a.m ? work : a.m) + 1023) / 1024;
   wg = wg < 1 ? 1 : (wg > kForkWG ? kForkWG : wg);
+  a.grid = (uint32_t)wg;
+  a.n_inv = 0xffffffffu / a.n_req;
+  a.at_once = kEntries / a.n_req;
   if (wg == 1 && a.n_req <= 256) {   // (16 requests of 77 places, us: 20.6 in one launch, 19.0 in two)
     hipLaunchKernelGGL((k_fork_one<256, 256>), dim3(1), dim3(256), 0, s, a);
   } else if (a.n_req <= 256) {
