@@ -188,8 +188,8 @@ __device__ __forceinline__ void entry(const ForkArgs& a, const ForkLds<T, N>& s,
 // atomic, so a prompt's shared pages cost nothing.
 //
 // Two launches, or one where a single workgroup takes all columns.  Bound by latency (dependent
-// reads behind the launches): 4 requests 9 us in one launch, 96 of 265 places 21 us in two (9 and 13 on the
-// GPU; 28 with the counts per page at the device's scope, that is past the L2).
+// reads behind the launches): 4 requests 8.5 us in one launch, 96 of 515 places 16 us in two (with the
+// counts per page at the device's scope, that is past the L2, a third more).
 struct Columns {   // of a workgroup, and how many of them are in LDS at a time
   uint32_t begin, end, width;
 };
@@ -683,21 +683,26 @@ __global__ __launch_bounds__(1024) void k_clear_one(ClearArgs a) {
 
 hipError_t launch_kv_fork(const ForkArgs& given, hipStream_t s) {
   ForkArgs a = given;
-  // a workgroup for every 1024 places of the tables, or rows
-  const uint64_t work = (uint64_t)a.n_req * a.max_pages;
-  uint64_t wg = ((work > a.m ? work : a.m) + 1023) / 1024;
-  wg = wg < 1 ? 1 : (wg > kForkWG ? kForkWG : wg);
-  a.grid = (uint32_t)wg;
+  // One workgroup for up to 1024 places of the tables, or rows, else one for every 512, so that a thread takes
+  // one place, two behind 256 workgroups (us for 96 beams of 515 places: 20.7 with 1024 places and 256
+  // threads, 17.0 with 512 and 256, 16.0 with 512 threads; 8 requests of 96 in one launch 11.6, in two 13.4; 4
+  // requests of 24 with 256 threads 8.5, with 512 9.1)
+  const uint64_t places = (uint64_t)a.n_req * a.max_pages, work = places > a.m ? places : a.m;
+  const uint64_t wg = work <= 1024 && a.n_req <= 512 ? 1 : (work + 511) / 512;
+  a.grid = (uint32_t)(wg > kForkWG ? kForkWG : wg);
   a.n_inv = 0xffffffffu / a.n_req;
   a.at_once = kEntries / a.n_req;
-  if (wg == 1 && a.n_req <= 256) {   // (16 requests of 77 places, us: 20.6 in one launch, 19.0 in two)
-    hipLaunchKernelGGL((k_fork_one<256, 256>), dim3(1), dim3(256), 0, s, a);
-  } else if (a.n_req <= 256) {
-    hipLaunchKernelGGL((k_fork_look<256, 256>), dim3((uint32_t)wg), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_fork_apply<256, 256>), dim3((uint32_t)wg), dim3(256), 0, s, a);
+  const dim3 grid(a.grid);
+  if (a.grid == 1 && work <= 256) {
+    hipLaunchKernelGGL((k_fork_one<256, 256>), grid, dim3(256), 0, s, a);
+  } else if (a.grid == 1 && a.n_req <= 512) {
+    hipLaunchKernelGGL((k_fork_one<512, 512>), grid, dim3(512), 0, s, a);
+  } else if (a.n_req <= 512) {
+    hipLaunchKernelGGL((k_fork_look<512, 512>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((k_fork_apply<512, 512>), grid, dim3(512), 0, s, a);
   } else {
-    hipLaunchKernelGGL((k_fork_look<1024, 4096>), dim3((uint32_t)wg), dim3(1024), 0, s, a);
-    hipLaunchKernelGGL((k_fork_apply<1024, 4096>), dim3((uint32_t)wg), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((k_fork_look<1024, 4096>), grid, dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((k_fork_apply<1024, 4096>), grid, dim3(1024), 0, s, a);
   }
   return hipGetLastError();
 }
