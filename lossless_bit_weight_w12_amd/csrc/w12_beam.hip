@@ -15,12 +15,10 @@
 // that roundings have no side they prefer); sums of a thread in FP32, of threads and parts in FP64.
 // That keeps lse within about 1e-7, so the choice is that of FP64 unless scores are as close as that.
 //
-// Bound by the dependent steps behind the reads (a part's list, its ticket, the join): 4 rows of 151936 FP32
-// logits 13 us, and by those and the exponentials for many rows: 96 rows in BF16 (29 MB, 4.9 us of reading)
-// 20 us, k = 64 about 40 us more.  Tickets of a call lie as far apart as their 16 KB allow: beside each other
-// in one line they passed one after the other, 18 ns each (38 us in place of 20).
-#include <type_traits>
-
+// Bound by the dependent steps behind the reads: 4 rows of 151936 FP32 logits 12.2 us, of them 4 for the
+// part, 1.2 for the ticket, 5 for the join; 96 rows in BF16 (29 MB, 4.9 us of reading) 19.4, of them 7 to
+// 12 for the part; k = 64 takes 24 to 27 us more.  Tickets of a call lie as far apart as their 16 KB allow: beside
+// each other in one line they passed one after the other, 18 ns each (38 us in place of 20).
 #include "w12.h"
 #include "w12_beam.h"
 
@@ -31,6 +29,7 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kCand = 1024;   // candidates of a part, at most
+constexpr uint32_t kRanked = 128;  // of a row
 
 // Values as whole numbers of the same order: -0 as 0, NaN as -inf; nothing gives 0.
 __device__ __forceinline__ uint32_t order(float x) {
@@ -88,6 +87,13 @@ __device__ __forceinline__ float exp_of(float t) {
   return __builtin_amdgcn_exp2f(fmaf(t, kL, t * kLow));
 }
 
+// LDS that the wave has written and reads: it keeps the order.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 struct Part {   // of a row, in the workspace
   float top;
   uint32_t pad;
@@ -103,14 +109,14 @@ __device__ __forceinline__ void store_dev(F* p, F v) { __hip_atomic_store(p, v, 
 template <bool F32, int N, int K>
 __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
   constexpr int V = F32 ? 4 : 8, U = N / V, T = (int)kBeamT, W = T / 64;
-  constexpr uint32_t kKeys = K > 16 ? 1024 : 640;   // keys of one row in LDS, per wave
+  constexpr uint32_t kKeys = K > 16 ? 1024 : 640;   // keys of one row in a wave's registers
   __shared__ union {
     struct {
       uint64_t cand[kCand];
       float most[T];
     } part;
     struct {
-      uint64_t keys[W][kKeys];
+      uint64_t keys[W][kRanked];
       uint64_t rows[W12_MAX_BEAMS][K];
       double lse[W12_MAX_BEAMS];
     } join;
@@ -324,13 +330,17 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
   }
   __syncthreads();
   if (!s_last) return;
-  // a wave per row: its lse, and its k best of the parts' lists (four at most a lane)
+  // a wave per row: its lse, and its k best of the parts' lists
+  const double base_score = lane < rows ? (double)a.scores[r0 + lane] : 0.0;   // (of the last step, requested now)
   for (uint32_t b = wave; b < rows; b += W) {
     const uint64_t first = (uint64_t)(r0 + b) * S;
     const uint64_t* const from = lists + first * k;
-    const bool in_lds = S * k <= kKeys;
-    if (in_lds)
-      for (uint32_t i = lane; i < S * k; i += 64) s.join.keys[wave][i] = load_dev(from + i);
+    const uint32_t all = S * k;
+    uint64_t v[kKeys / 64];
+    if (all <= kKeys) {
+#pragma unroll
+      for (uint32_t i = 0; i < kKeys / 64; ++i) v[i] = lane + 64 * i < all ? load_dev(from + lane + 64 * i) : (uint64_t)0;
+    }
     float tops[4];
     double sums[4];
 #pragma unroll
@@ -339,25 +349,75 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
       tops[i] = on ? load_dev(&parts[first + lane + 64 * i].top) : -INFINITY;
       sums[i] = on ? load_dev(&parts[first + lane + 64 * i].sum) : 0.0;
     }
-    const float top = value(wave_max(order(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])))));
+    const uint32_t top_order = wave_max(order(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]))));
+    const float top = value(top_order);
     const double to = top == -INFINITY ? 0.0 : (double)top;
-    double v = 0;
+    double all_sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (64u * i < S) v += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)tops[i] - to);   // (0, or NaN that stays)
-    v = wave_sum(v);
-    if (lane == 0) s.join.lse[b] = (top == -INFINITY ? -(double)INFINITY : to) + log(v);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();   // one wave writes and reads: LDS keeps the order
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    // Every lane has the head of a list, and the one behind it before it is asked for; without
-    // branches: 64 of 640 keys in 6 us, in 14 where only the lane that won read on.
-    auto merge = [&](auto heads, auto key) {
-      constexpr int H = decltype(heads)::value;
-      uint64_t head[H], next[H], mine = 0;
-      uint32_t pos[H];
+      if (64u * i < S) all_sum += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)tops[i] - to);   // (0, or NaN that stays)
+    all_sum = wave_sum(all_sum);
+    if (lane == 0) s.join.lse[b] = (top == -INFINITY ? -(double)INFINITY : to) + log(all_sum);
+    // As in a part: a bound that at least k keys reach and not many more, and those by their ranks among
+    // themselves.  (Taking the largest head of the lists k times took 0.2 us a time.)
+    uint32_t count = kRanked + 1;
+    if (all <= kKeys) {
+      auto reach = [&](uint32_t x) {
+        uint32_t c = 0;
 #pragma unroll
-      for (int i = 0; i < H; ++i) {
+        for (uint32_t i = 0; i < kKeys / 64; ++i)
+          if (64 * i < all) c += (uint32_t)__popcll(__ballot((uint32_t)(v[i] >> 32) >= x));
+        return c;
+      };
+      uint32_t low = 1;
+      count = reach(1);
+      if (count > k + k / 2 + 8) {
+        uint32_t mine = 0;   // (64 keys at least reach the least of the lanes' largest)
+#pragma unroll
+        for (uint32_t i = 0; i < kKeys / 64; ++i) mine = max(mine, (uint32_t)(v[i] >> 32));
+        uint32_t high = top_order + 1;
+        low = max(~wave_max(~mine), 1u);
+        count = reach(low);
+        while (high - low > 1 && count > k + k / 2 + 8) {
+          const uint32_t mid = low + (high - low) / 2, c = reach(mid);
+          if (c < k) {
+            high = mid;
+          } else {
+            low = mid;
+            count = c;
+          }
+        }
+      }
+      if (count <= kRanked) {
+        uint64_t* const list = s.join.keys[wave];
+        uint32_t at = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < kKeys / 64; ++i)
+          if (64 * i < all) {
+            const bool in = (uint32_t)(v[i] >> 32) >= low;
+            const uint64_t with = __ballot(in);
+            if (in) list[at + (uint32_t)__popcll(with & ((1ull << lane) - 1ull))] = v[i];
+            at += (uint32_t)__popcll(with);
+          }
+        wave_sync();
+        const uint64_t x = lane < count ? list[lane] : 0, y = lane + 64 < count ? list[lane + 64] : 0;
+        uint32_t rx = 0, ry = 0;
+        for (uint32_t i = 0; i < count; ++i) {
+          const uint64_t z = list[i];
+          rx += z > x;
+          ry += z > y;
+        }
+        if (lane < count && rx < k) s.join.rows[b][rx] = x;
+        if (lane + 64 < count && ry < k) s.join.rows[b][ry] = y;
+        if (lane >= count && lane < k) s.join.rows[b][lane] = 0;   // (there are no more)
+      }
+    }
+    if (count > kRanked) {   // more keys than that, or too many equal logits: one after the other
+      auto key = [&](uint32_t l, uint32_t p) { return l < S && p < k ? load_dev(from + l * k + p) : (uint64_t)0; };
+      uint64_t head[4], next[4], mine = 0;
+      uint32_t pos[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         head[i] = key(lane + 64 * i, 0u);
         next[i] = key(lane + 64 * i, 1u);
         pos[i] = 1;
@@ -365,11 +425,11 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
       for (uint32_t r = 0; r < k; ++r) {
         uint64_t best = head[0];
 #pragma unroll
-        for (int i = 1; i < H; ++i) best = head[i] > best ? head[i] : best;
+        for (int i = 1; i < 4; ++i) best = head[i] > best ? head[i] : best;
         const uint64_t won = wave_max64(best);
         mine = lane == r ? won : mine;
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const bool here = head[i] == won;   // keys are distinct but for 0, which nothing follows
           head[i] = here ? next[i] : head[i];
           pos[i] += here;
@@ -377,22 +437,45 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
         }
       }
       if (lane < k) s.join.rows[b][lane] = mine;
-    };
-    auto near = [&](uint32_t l, uint32_t p) {
-      const bool on = l < S && p < k;
-      const uint64_t v = s.join.keys[wave][on ? l * k + p : 0u];
-      return on ? v : (uint64_t)0;
-    };
-    auto far = [&](uint32_t l, uint32_t p) { return l < S && p < k ? load_dev(from + l * k + p) : (uint64_t)0; };
-    if (!in_lds) merge(std::integral_constant<int, 4>(), far);
-    else if (S > 64) merge(std::integral_constant<int, 4>(), near);
-    else merge(std::integral_constant<int, 1>(), near);
+    }
   }
   __syncthreads();
   if (wave != 0) return;
+  auto score_of = [&](uint64_t key, double base, double lse) {
+    const double score = base + ((double)value((uint32_t)(key >> 32)) - lse);
+    return score == score ? score : -(double)INFINITY;
+  };
+  if (rows * k <= 64) {   // a lane per pair, by its rank; equal scores in the order of the lanes
+    const uint32_t r = lane / k, p = lane - r * k;
+    const bool on = r < rows;
+    const uint64_t key = on ? s.join.rows[on ? r : 0][p] : 0;
+    const uint64_t bits = __builtin_bit_cast(uint64_t, base_score);
+    const double base = __builtin_bit_cast(double, (uint64_t)(uint32_t)__shfl((int)(bits >> 32), (int)(r & 63)) << 32 |
+                                                       (uint32_t)__shfl((int)(uint32_t)bits, (int)(r & 63)));
+    const double score = score_of(key, base, on ? s.join.lse[r] : 0.0);
+    const uint64_t ord = key ? order64(score) : 0;
+    uint32_t rank = 0;
+    for (uint32_t i = 0; i < rows * k; ++i) {
+      const uint64_t z = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(ord >> 32), (int)i) << 32 |
+                         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)ord, (int)i);
+      rank += z > ord || (z == ord && i < lane);
+    }
+    const uint32_t found = (uint32_t)__popcll(__ballot(ord != 0));
+    const uint64_t at_out = (uint64_t)grp * k;
+    if (ord && rank < k) {
+      a.parent[at_out + rank] = (int32_t)(r0 + r);
+      a.token[at_out + rank] = (int32_t)~(uint32_t)key;
+      a.out[at_out + rank] = (float)score;
+    }
+    if (lane >= found && lane < k) {
+      a.parent[at_out + lane] = a.token[at_out + lane] = -1;
+      a.out[at_out + lane] = -INFINITY;
+    }
+    return;
+  }
   // a lane per row: the best score of all, lower rows first
   const bool on = lane < rows;
-  const double base_score = on ? (double)a.scores[r0 + lane] : 0.0, lse = on ? s.join.lse[lane] : 0.0;
+  const double lse = on ? s.join.lse[lane] : 0.0;
   uint32_t pos = 1;
   auto ahead = [&](uint32_t p) {
     const uint64_t v = s.join.rows[on ? lane : 0u][p < k ? p : 0u];
@@ -402,8 +485,7 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
   int32_t parent = -1, tok = -1;   // of the lane's place in the answer
   float out = -INFINITY;
   for (uint32_t r = 0; r < k; ++r) {
-    double score = base_score + ((double)value((uint32_t)(key >> 32)) - lse);
-    score = score == score ? score : -(double)INFINITY;
+    const double score = score_of(key, base_score, lse);
     const uint64_t ord = key ? order64(score) : 0, won = wave_max64(ord);
     if (won == 0) break;
     const int w = __ffsll((unsigned long long)__ballot(ord == won)) - 1;
