@@ -30,10 +30,9 @@ inline uint32_t beam_values(uint32_t n, uint32_t vocab, uint32_t k) {
     if ((uint64_t)n * ((vocab + kBeamT * v - 1) / (kBeamT * v)) <= 1024) return v;
   return 64;
 }
-// (rows may begin anywhere in a 16-byte vector: up to 7 places more)
 inline uint32_t beam_splits(uint32_t n, uint32_t vocab, uint32_t k) {
   const uint32_t per = kBeamT * beam_values(n, vocab, k);
-  return (vocab + 7 + per - 1) / per;
+  return (vocab + per - 1) / per;
 }
 // Workspace: a ticket per group; per row and part its maximum, its sum and its k best.
 constexpr uint64_t kBeamTickets = 4096 * 4;

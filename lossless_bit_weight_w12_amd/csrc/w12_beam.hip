@@ -27,6 +27,7 @@ namespace w12 {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));   // in memory, at an element's alignment
 
 constexpr uint32_t kCand = 1024;   // candidates of a part, at most
 constexpr uint32_t kRanked = 128;  // of a row
@@ -130,27 +131,28 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
   uint64_t* const lists = reinterpret_cast<uint64_t*>(parts + (uint64_t)a.n * S);
 
   // ---- the part's values, requested first
+  // (Dealt by token, wherever the row begins: rows with the same logits have the same sums, bit for bit, and
+  // so the same scores.  Rows that begin inside a vector take loads across lines for it.)
   u32x4 raw[U];
   const uint32_t es = F32 ? 4 : 2;
   const uint8_t* const base = reinterpret_cast<const uint8_t*>(a.logits) + row * a.stride * es;
-  const uint32_t skew = (uint32_t)((uintptr_t)base / es % V);   // the row's first value within its vector
-  const uint32_t token_0 = split * T * N + t * V - skew;        // of this thread (below zero: before the row)
+  const uint32_t token_0 = split * T * N + t * V;   // of this thread
   constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;   // -inf
   if (row < a.n) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t e = token_0 + i * T * V;
       raw[i] = u32x4{kNone, kNone, kNone, kNone};
-      if (e < a.vocab && e + V <= a.vocab) {
-        raw[i] = *reinterpret_cast<const u32x4*>(base + (uint64_t)e * es);
-      } else if ((int32_t)e > -V && (int32_t)e < (int32_t)a.vocab) {   // at an end of the row
+      if (e + V <= a.vocab) {
+        raw[i] = *reinterpret_cast<const u32x4_any*>(base + (uint64_t)e * es);
+      } else if (e < a.vocab) {   // at the row's end
 #pragma unroll
         for (int j = 0; j < V; ++j)
           if (e + j < a.vocab) {
             if constexpr (F32) {
-              raw[i][j] = reinterpret_cast<const uint32_t*>(base)[(int32_t)(e + j)];
+              raw[i][j] = reinterpret_cast<const uint32_t*>(base)[e + j];
             } else {
-              const uint32_t x = reinterpret_cast<const uint16_t*>(base)[(int32_t)(e + j)];
+              const uint32_t x = reinterpret_cast<const uint16_t*>(base)[e + j];
               raw[i][j / 2] = j & 1 ? (raw[i][j / 2] & 0xffffu) | x << 16 : (raw[i][j / 2] & 0xffff0000u) | x;
             }
           }
@@ -193,11 +195,10 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
   const uint32_t grp = s_grp - 1, r0 = (uint32_t)a.grp_off[grp], rows = (uint32_t)a.grp_off[grp + 1] - r0;
 
   // ---- maximum, sum, and a bound that at least k values reach
-  bool any = false;
+  const bool any = token_0 < a.vocab;
   float most = -INFINITY, vec[U];   // of the vectors too
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    any |= (int32_t)token(i, 0) > -V && (int32_t)token(i, 0) < (int32_t)a.vocab;   // (a vector may hold more than the row)
     vec[i] = at(i, 0);
 #pragma unroll
     for (int j = 1; j < V; ++j) vec[i] = fmaxf(vec[i], at(i, j));
