@@ -648,7 +648,7 @@ w12_status w12_attn_shared(const uint16_t* q, uint64_t q_stride, uint32_t m, uin
  * as w12_kv_fork takes it where beams are requests), token, and score_out (the score in FP32).  A
  * group without rows gets -1, -1, -inf.  Everything is -1, -1, NaN when grp_off is not 0 <=
  * grp_off[0] <= grp_off[1] <= ... <= n or a group has more than W12_MAX_BEAMS rows.
- * (A row's log-sum-exp is within about 1e-7 of exact: scores of different rows that are closer than that
+ * (A row's log-sum-exp is within 1e-7 of exact: scores of different rows that are closer than two of that
  * may change places, those of rows with the same logits do not.)
  * logits device BF16 or FP32 [n][vocab], rows `stride` >= vocab elements apart, of any alignment;
  * scores device FP32 [n]; grp_off device int32 [n_grp + 1]; parent, token int32, score_out FP32

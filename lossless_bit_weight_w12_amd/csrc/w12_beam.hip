@@ -11,12 +11,14 @@
 // candidates' ranks among themselves give their order.  Where equal values make them too many,
 // the k are taken one after the other.
 //
-// Exponentials: exp2 of the hardware on the correctly rounded product with log2(e) (of 48 bits, so
-// that roundings have no side they prefer); sums of a thread in FP32, of threads and parts in FP64.
-// That keeps lse within about 1e-7, so the choice is that of FP64 unless scores are as close as that.
+// Exponentials: exp2 of the hardware, whose own error is the only one that is left (see Exps); sums in FP64.
+// That keeps lse within 1e-7 whatever the logits are, so the choice is that of FP64 unless scores are as close
+// as that.  (Terms are alike in a row of few values, and behind one that stands out, and then so are their
+// roundings: sums of a thread in FP32 were off by up to 2.5e-6.  They took 19.5 us in place of 20.5 for 96 rows
+// in BF16; terms of exactly reduced arguments 23.0.)
 //
-// Bound by the dependent steps behind the reads: 4 rows of 151936 FP32 logits 12.2 us, of them 4 for the
-// part, 1.2 for the ticket, 5 for the join; 96 rows in BF16 (29 MB, 4.9 us of reading) 19.4, of them 7 to
+// Bound by the dependent steps behind the reads: 4 rows of 151936 FP32 logits 12.4 us, of them 4 for the
+// part, 1.2 for the ticket, 5 for the join; 96 rows in BF16 (29 MB, 4.9 us of reading) 20.5, of them 7 to
 // 12 for the part; k = 64 takes 24 to 27 us more.  Tickets of a call lie as far apart as their 16 KB allow: beside
 // each other in one line they passed one after the other, 18 ns each (38 us in place of 20).
 #include "w12.h"
@@ -82,11 +84,34 @@ __device__ __forceinline__ double wave_sum(double v) {
                                         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63));
 }
 
-// exp(t), t <= 0.
-__device__ __forceinline__ float exp_of(float t) {
-  constexpr float kL = 1.44269502f, kLow = 1.92596299e-8f;   // log2(e)
-  return __builtin_amdgcn_exp2f(fmaf(t, kL, t * kLow));
-}
+// What a part's exponentials are relative to: exp(0), so that nothing is lost in a difference, or, where the
+// largest value is far from 0, that.
+__device__ __forceinline__ float base_of(float top) { return (top >= -24.f && top < 32.f) || top == -INFINITY ? 0.f : top; }
+
+// Sum of exp(x - base).  x log2(e) is taken as h + l, h in FP32: exp2 of the hardware of h (off by 8.5e-8 of
+// itself at most, over all h), and what l makes of it to first order, l exp2(h), in a sum of its own.  FP32
+// values: h rounded, l what that leaves out, 2^-18 at most.  BF16 values: h exact, with a factor of 16 bits, l
+// the rest of log2(e), 7.1e-6 of x (whose second order is 1.3e-8 of a term where x is 32).  Below -150 a term
+// is nothing (the largest is 2^-35 at least), -inf among them.
+template <bool F32>
+struct Exps {
+  static constexpr float kL = F32 ? 1.44269502f : 1.44268798828125f;       // 24 bits, 16 bits
+  static constexpr float kLow = F32 ? 1.92596299e-8f : 7.05260771e-6f;     // log2(e) - kL
+  double sum = 0;
+  float rest = 0.f;
+  __device__ __forceinline__ void add(float given) {
+    const float x = __builtin_elementwise_maximum(given, -150.f), h = x * kL, e = __builtin_amdgcn_exp2f(h);   // (NaN stays)
+    sum += (double)e;
+    rest = fmaf(e, F32 ? fmaf(x, kLow, fmaf(x, kL, -h)) : x, rest);
+  }
+  __device__ __forceinline__ void add(float x, double base) {
+    const double t = (double)x - base, y = (t < -150.0 ? -150.0 : t) * 1.4426950408889634;
+    const float h = (float)y, e = __builtin_amdgcn_exp2f(h);
+    sum += (double)e;
+    rest = fmaf(e, (float)(y - (double)h) * (F32 ? 1.f : 1.f / kLow), rest);
+  }
+  __device__ __forceinline__ double all() const { return sum + (double)rest * ((F32 ? 1.0 : (double)kLow) * 0.6931471805599453); }
+};
 
 // LDS that the wave has written and reads: it keeps the order.
 __device__ __forceinline__ void wave_sync() {
@@ -244,13 +269,20 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
     for (int i = 0; i < U; ++i) asm volatile("" : "+v"(raw[i]));
   };
   packed();
-  const float shift = most == -INFINITY ? 0.f : most;
-  float sum = 0.f;
+  const float from = base_of(most);
+  Exps<F32> exps;
+  if (from == 0.f) {
 #pragma unroll
-  for (int i = 0; i < U; ++i)
+    for (int i = 0; i < U; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum += exp_of(at(i, j) - shift);
-  const double all = wave_sum((double)sum);
+      for (int j = 0; j < V; ++j) exps.add(at(i, j));
+  } else {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) exps.add(at(i, j), (double)from);
+  }
+  const double all = wave_sum(exps.all());
   if (lane == 0) s_sum[wave] = all;
 
   // ---- candidates, and the k best of them in order
@@ -352,13 +384,13 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
     }
     const uint32_t top_order = wave_max(order(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]))));
     const float top = value(top_order);
-    const double to = top == -INFINITY ? 0.0 : (double)top;
+    const double to = base_of(top);
     double all_sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (64u * i < S) all_sum += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)tops[i] - to);   // (0, or NaN that stays)
+      if (64u * i < S) all_sum += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)base_of(tops[i]) - to);   // (0, or NaN that stays)
     all_sum = wave_sum(all_sum);
-    if (lane == 0) s.join.lse[b] = (top == -INFINITY ? -(double)INFINITY : to) + log(all_sum);
+    if (lane == 0) s.join.lse[b] = to + log(all_sum);
     // As in a part: a bound that at least k keys reach and not many more, and those by their ranks among
     // themselves.  (Taking the largest head of the lists k times took 0.2 us a time.)
     uint32_t count = kRanked + 1;
