@@ -652,10 +652,10 @@ w12_status w12_attn_shared(const uint16_t* q, uint64_t q_stride, uint32_t m, uin
  * may change places, those of rows with the same logits do not.)
  * logits device BF16 or FP32 [n][vocab], rows `stride` >= vocab elements apart, of any alignment;
  * scores device FP32 [n]; grp_off device int32 [n_grp + 1]; parent, token int32, score_out FP32
- * [n_grp][k].  ws: w12_beam_ws_bytes(n, vocab, k) bytes (0 for arguments that are none), 256-byte aligned,
- * beginning with 16384 bytes of tickets that must be zero before its first use
- * (w12_workspace_init) and that every call leaves zero; calls sharing one must be ordered.  Same inputs,
- * same bits.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (vocab outside 1..W12_MAX_VOCAB, k outside
+ * [n_grp][k].  ws: w12_beam_ws_bytes(n, vocab, k) bytes (0 for arguments that are none; enough for
+ * every call with n, vocab and k no larger), 256-byte aligned, beginning with 16384 bytes of tickets that
+ * must be zero before its first use (w12_workspace_init) and that every call leaves zero; calls sharing one
+ * must be ordered.  Same inputs, same bits.  Errors: W12_ERR_NULL; W12_ERR_SHAPE (vocab outside 1..W12_MAX_VOCAB, k outside
  * 1..W12_MAX_BEAM_K or above vocab, stride); W12_ERR_RANGE (n > W12_MAX_REQ, n_grp outside
  * 1..W12_MAX_REQ); W12_ERR_FORMAT (dtype); W12_ERR_WORKSPACE; W12_ERR_ALIGN. */
 #define W12_LOGITS_BF16 0

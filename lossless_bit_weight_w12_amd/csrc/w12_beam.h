@@ -23,21 +23,30 @@ struct BeamArgs {
 // at most four workgroups to a CU (us for 151936 BF16 logits, k = 8: 12 x 4 rows 20.3, 16.4, 20.4; 24 x 4
 // rows 27.6, 22.4, 20.2), and the largest for long lists and rows, whose parts a join takes up to
 // 256 of.
-constexpr uint32_t kBeamT = 256, kBeamShort = 16;
+constexpr uint32_t kBeamT = 256, kBeamShort = 16, kBeamParts = 1024;
 inline uint32_t beam_values(uint32_t n, uint32_t vocab, uint32_t k) {
   if (k > kBeamShort || vocab > (1u << 19)) return 64;
   for (uint32_t v = 16; v < 64; v *= 2)
-    if ((uint64_t)n * ((vocab + kBeamT * v - 1) / (kBeamT * v)) <= 1024) return v;
+    if ((uint64_t)n * ((vocab + kBeamT * v - 1) / (kBeamT * v)) <= kBeamParts) return v;
   return 64;
 }
 inline uint32_t beam_splits(uint32_t n, uint32_t vocab, uint32_t k) {
   const uint32_t per = kBeamT * beam_values(n, vocab, k);
   return (vocab + per - 1) / per;
 }
-// Workspace: a ticket per group; per row and part its maximum, its sum and its k best.
+// Workspace: a ticket per group; per row and part its maximum, its sum and its k best.  The size is what this
+// call and every smaller one need, which may have smaller shares and so more parts: of either kind of
+// those at most 1024 parts, and lists of kBeamShort at most.
 constexpr uint64_t kBeamTickets = 4096 * 4;
 inline uint64_t beam_bytes(uint32_t n, uint32_t vocab, uint32_t k) {
-  return kBeamTickets + (uint64_t)n * beam_splits(n, vocab, k) * (16 + 8ull * k);
+  uint64_t most = 0;
+  for (uint32_t v = 16; v <= 64; v *= 2) {
+    const uint64_t all = (uint64_t)n * ((vocab + kBeamT * v - 1) / (kBeamT * v));
+    const uint64_t parts = v < 64 && all > kBeamParts ? kBeamParts : all, keys = v < 64 && k > kBeamShort ? kBeamShort : k;
+    const uint64_t bytes = parts * (16 + 8 * keys);
+    most = bytes > most ? bytes : most;
+  }
+  return kBeamTickets + most;
 }
 hipError_t launch_beam_select(const BeamArgs& a, bool f32, hipStream_t s);
 

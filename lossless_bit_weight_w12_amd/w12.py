@@ -1244,8 +1244,9 @@ _BEAM_WS = {}
 
 
 def beam_workspace(n: int, vocab: int, k: int, device="cuda"):
-    """A workspace for beam_select (zero tickets), for callers that keep their own: one for each stream
-    or captured graph that may run at the same time as others.  It is zeroed on the current stream."""
+    """A workspace for beam_select (zero tickets) of up to n rows, vocab logits and k pairs, for callers
+    that keep their own: one for each stream or captured graph that may run at the same time as others.
+    It is zeroed on the current stream."""
     size = int(lib().w12_beam_ws_bytes(n, vocab, k))
     if size == 0:
         raise ValueError("beam_workspace: no such call")
