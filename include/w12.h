@@ -627,7 +627,8 @@ w12_status w12_kv_compact(const w12_pages* p, int32_t* refs, uint32_t first, uin
  * group sees is shared, in whole units of 64 tokens; the rest is read per request.)
  * grp_off [n_grp + 1] and grp_len [n_grp] device int32; everything else as w12_attn_paged, but for
  * the workspace: w12_attn_shared_ws_bytes(m, n_heads, head_dim) bytes (0 for arguments that are
- * none), 256-byte aligned, in any state; calls sharing one must be ordered.  Same inputs, same bits.
+ * none; enough for every call with m, n_heads and head_dim no larger), 256-byte aligned, in any state;
+ * calls sharing one must be ordered.  Same inputs, same bits.
  * Errors as w12_attn_paged, and W12_ERR_RANGE (n_grp outside 1..W12_MAX_REQ, m * n_heads >
  * W12_MAX_SHARED_ROWS, (m * n_heads + 64 * n_req * n_kv_heads) * (max_pages * page_size + 1024) >=
  * 2^38). */

@@ -48,8 +48,15 @@ inline uint64_t shared_region(uint32_t m, uint32_t n_heads, uint32_t d) {
 inline uint64_t shared_slots(uint32_t m, uint32_t n_heads, uint32_t d) {
   return shared_region(m, n_heads, d) + 2ull * m * n_heads + (uint64_t)kSharedGrid * shared_waves(d) * 32;
 }
+// (What heads of d values and narrower ones need: workgroups of heads of 256 have half the waves, and so, in
+// calls of few rows, less to keep than those of 128.)
 inline uint64_t shared_bytes(uint32_t m, uint32_t n_heads, uint32_t d) {
-  return kSharedMl + shared_slots(m, n_heads, d) * (8 + 4ull * d);
+  uint64_t most = 0;
+  for (uint32_t w = 64; w <= d; w *= 2) {
+    const uint64_t bytes = kSharedMl + shared_slots(m, n_heads, w) * (8 + 4ull * w);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
 }
 hipError_t launch_attn_shared(const SharedArgs& a, uint32_t head_dim, uint32_t dtype, hipStream_t s);
 

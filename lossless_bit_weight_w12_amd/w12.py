@@ -1177,8 +1177,9 @@ _SHARED_WS = {}
 
 
 def attn_shared_workspace(m: int, n_heads: int, head_dim: int, device="cuda"):
-    """A workspace for attn_shared, in no particular state, for callers that keep their own: one for
-    each stream or captured graph that may run at the same time as others."""
+    """A workspace for attn_shared of up to m rows, n_heads heads and head_dim values, in no particular
+    state, for callers that keep their own: one for each stream or captured graph that may run at the
+    same time as others."""
     n = int(lib().w12_attn_shared_ws_bytes(m, n_heads, head_dim))
     if n == 0:
         raise ValueError("attn_shared_workspace: no such call")

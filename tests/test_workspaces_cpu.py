@@ -44,3 +44,9 @@ def test_beam_workspace_holds_the_parts(L):
         values = 64 if k > 16 or vocab > 1 << 19 else next(
             (v for v in (16, 32) if n * -(-vocab // (256 * v)) <= 1024), 64)
         assert L.w12_beam_ws_bytes(n, vocab, k) >= 16384 + n * -(-vocab // (256 * values)) * (16 + 8 * k)
+
+
+def test_shared_attention_workspace_never_falls(L):
+    f = lambda d, m, n: L.w12_attn_shared_ws_bytes(m, n, d)
+    assert grows(f, [64, 128, 256], [0, 1, 4, 10, 11, 42, 43, 44, 96, 128], [1, 2, 8, 40, 128, 1023, 1024]) == []
+    assert f(256, 4, 8) >= f(128, 4, 8) > f(64, 4, 8) > 0
