@@ -619,10 +619,11 @@ w12_status w12_kv_compact(const w12_pages* p, int32_t* refs, uint32_t first, uin
 /* w12_attn_paged where requests share their first tokens, which are read once for all of them: group
  * g is requests grp_off[g] .. grp_off[g+1]-1, and the first grp_len[g] tokens of each are the same, in
  * the same pages or in copies of them (the pages in the table row of its first request that has rows
- * and a length are read; below 1: nothing is shared).  Requests in no company are groups of one.  Results are those of w12_attn_paged up to the
- * order of the FP32 sums, with the same rules for rows that see no token, for what lies behind a
- * row's last token, for rows of no request, and for requests and pages that are none (a shared
- * page that is none makes the rows of its whole group NaN).  Every row gets NaN when grp_off is not
+ * and a length are read; below 1: nothing is shared).  Requests in no company are groups of one.  Results
+ * are those of w12_attn_paged up to the order of the FP32 sums and the weights' roundings (to the same
+ * types, with the same range below the largest), with the same rules for rows that see no token, for
+ * what lies behind a row's last token, for rows of no request, and for requests and pages that are none
+ * (a shared page that is none makes the rows of its whole group NaN).  Every row gets NaN when grp_off is not
  * 0 = grp_off[0] <= grp_off[1] <= ... <= grp_off[n_grp] = n_req.  (Of grp_len what every row of the
  * group sees is shared, in whole units of 64 tokens; the rest is read per request.)
  * grp_off [n_grp + 1] and grp_len [n_grp] device int32; everything else as w12_attn_paged, but for

@@ -51,19 +51,25 @@ struct Shared {
     return row_tiles > 4 ? 8u : (row_tiles > 2 ? 6u : 5u);
   }
 
-  // The running softmax of a query row in the staged loop.  Weights are 2^(c s + bias - fine), the
-  // reference bias following the maximum only when that has risen by a factor of 2^8 (so the results are
-  // seldom rescaled; weights reach 2^8, in FP16 times 2^7).  c s + bias is one fused operation, exact
-  // but for its own rounding, and the bias is a number of its own, no rounded product that would have
-  // to be the same elsewhere; where c s is so large (2^24) that the bias cannot follow it within a
-  // factor of 2, `fine` takes the rest.
-  static constexpr float kUp = F8 ? 7.f : 0.f, kRise = 8.f;
+  // The running softmax of a query row in the staged loop.  Weights are 2^(c s + bias), the reference bias
+  // following the maximum only when that has risen by a factor of 2^kRise (so the results are seldom
+  // rescaled).  BF16 weights may reach 2^8.  FP16 ones begin at 2^15, as in the waves' path, so that as many
+  // of the small ones are kept (11 bits down to 2^-29 of the largest, a part of them down to 2^-39), and
+  // 2^15.9 is what the type leaves for them to rise to.  (From 2^7, with 2^8 to rise by, 320 query rows a head over
+  // 8000 tokens took 110.7 us in place of 112.8, and weights of 2^-32 were lost.)
+  // c s + bias is one fused operation, exact but for its own rounding, and the bias is a number of its own, no
+  // rounded product that would have to be the same elsewhere; where c s is so large (kFar) that the bias cannot
+  // follow it (within a factor of 2, in FP16 2^(1/512)), `fine` takes the rest, and kUp is kept apart.
+  static constexpr float kUp = F8 ? 15.f : 0.f, kRise = F8 ? 0.9f : 8.f, kFar = F8 ? 65536.f : 16777216.f;
   struct Row {
     float ref;    // raw score that the reference was taken from
-    float bias;   // kUp - c ref, rounded
-    float fine;
+    float bias;   // kUp - c ref, rounded; far out -c ref
+    float fine;   // 0; far out what the rounding left, or kNothing
     float sum;    // this lane's part, of the weights as they enter the product
+    __device__ __forceinline__ float up() const { return fine == 0.f ? 0.f : kUp; }
+    __device__ __forceinline__ float power(float c, float x) const { return (fmaf(x, c, bias) - fine) + up(); }
   };
+  static constexpr float kNothing = 1e-30f;
   static __device__ __forceinline__ Row row() { return Row{-INFINITY, kUp, 0.f, 0.f}; }
   // The reference brought up to a span's largest score mx.
   static __device__ __forceinline__ void rise(float c, float mx, Row& r, f32x16 (&o)[DR]) {
@@ -72,12 +78,12 @@ struct Shared {
     if (__any((mx - r.ref) * c > kRise)) {
       const bool none = r.ref == -INFINITY;
       if (mx > r.ref) {
-        const float bias = r.bias, fine = r.fine;
+        const float bias = r.bias, fine = r.fine, up = r.up(), to = -(mx * c), rest = fmaf(mx, c, to);
+        const bool far = fabsf(to) >= kFar;
         r.ref = mx;
-        r.bias = fmaf(-mx, c, kUp);
-        const float rest = fmaf(mx, c, r.bias) - kUp;
-        r.fine = fabsf(r.bias) < 16777216.f ? 0.f : rest;
-        const float fade = none ? 0.f : pow2((r.bias - bias) - (r.fine - fine));
+        r.bias = far ? to : fmaf(-mx, c, kUp);
+        r.fine = far ? (rest == 0.f ? kNothing : rest) : 0.f;
+        const float fade = none ? 0.f : pow2(((r.bias - bias) - (r.fine - fine)) + (r.up() - up));
         r.sum *= fade;
 #pragma unroll
         for (int d = 0; d < DR; ++d) o[d] *= fade;
@@ -105,7 +111,7 @@ struct Shared {
   }
   // What brings a row's results to the reference of the waves' path: weights 2^(c (s - ref) + Own::kUp).
   static __device__ __forceinline__ float adjust(float c, const Row& r) {
-    return r.ref == -INFINITY ? pow2(Own::kUp - kUp) : pow2(Own::kUp - (fmaf(r.ref, c, r.bias) - r.fine));
+    return r.ref == -INFINITY ? pow2(Own::kUp - kUp) : pow2(Own::kUp - r.power(c, r.ref));
   }
 };
 
@@ -612,9 +618,9 @@ __global__ __launch_bounds__((Shared<D, F8>::T)) void k_shared(SharedArgs a) {
           fence();
           A::rise(cs, fmaxf(m0, m1), soft, o);
           float scale = cs, bias = soft.bias;
-          if (__any(soft.fine != 0.f)) {   // scores beyond 2^24
+          if (__any(soft.fine != 0.f)) {   // scores far out
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = fmaf(x[k], cs, soft.bias) - soft.fine;
+            for (int k = 0; k < 16; ++k) x[k] = soft.power(cs, x[k]);
             scale = 1.f;
             bias = 0.f;
           }
