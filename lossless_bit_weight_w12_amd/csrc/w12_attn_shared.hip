@@ -56,7 +56,7 @@ struct Shared {
   // rescaled).  BF16 weights may reach 2^8.  FP16 ones begin at 2^15, as in the waves' path, so that as many
   // of the small ones are kept (11 bits down to 2^-29 of the largest, a part of them down to 2^-39), and
   // 2^15.9 is what the type leaves for them to rise to.  (From 2^7, with 2^8 to rise by, 320 query rows a head over
-  // 8000 tokens took 110.7 us in place of 112.8, and weights of 2^-32 were lost.)
+  // 8000 tokens took 109 us in place of 115.5, and weights of 2^-32 were lost.)
   // c s + bias is one fused operation, exact but for its own rounding, and the bias is a number of its own, no
   // rounded product that would have to be the same elsewhere; where c s is so large (kFar) that the bias cannot
   // follow it (within a factor of 2, in FP16 2^(1/512)), `fine` takes the rest, and kUp is kept apart.

@@ -178,8 +178,11 @@ class DecodeStack:
             self.plan_calls = [w12.prepare_kv_plan(at.pages, at.length, at.req_off, self.kv_len, self.pos, self.slot)]
         else:
             self.plan_calls = [w12.prepare_kv_fork(at.pages, at.parent, at.length, at.req_off, self.kv_len, self.pos,
-                                                   self.slot, self.copies),
-                               w12.prepare_kv_copy(at.caches, self.copies)]
+                                                   self.slot, self.copies)]
+            alike = {}   # (a copy takes caches of one form; the layers' may differ)
+            for c in at.caches:
+                alike.setdefault((tuple(c.k.shape), c.k.dtype), []).append(c)
+            self.plan_calls += [w12.prepare_kv_copy(caches, self.copies) for caches in alike.values()]
         self.verify_call = w12.prepare_verify_batched(self.h, self.head, at.req_off, req_ndraft, draft,
                                                       self.argmax, self.accepted)
 
