@@ -7,11 +7,11 @@
 // length), as in w12_attn_paged.  Every part leaves values, maximum and sum in FP32; a second
 // kernel joins a row's parts in a fixed order.
 //
-// Both kinds of items lie on lines that are cut into equal pieces (see w12_attn_paged).  Items of
-// more than 32 query rows are cut for workgroups: K and V pass through LDS once for up to 32 rows
-// per wave, the waves taking rows, and, where there are fewer rows than waves, tokens too.  The
-// others (the requests' own tokens, and shared ones of few rows) are cut for single waves, which read
-// K and V straight into registers, so that many short requests run side by side.
+// Both kinds of items lie on lines that are cut into equal pieces (see w12_attn_paged).  Items of more query
+// rows than a wave of the second line holds (32, 16 with heads of 256) are cut for workgroups: K and V pass
+// through LDS once for up to 32 rows per wave, the waves taking rows, and, where there are fewer rows
+// than waves, tokens too.  The others (the requests' own tokens, and shared ones of few rows) are cut for
+// single waves, which read K and V straight into registers, so that many short requests run side by side.
 //
 // Bound by HBM where few rows share tokens: 24 prompts of up to 8000 tokens, 20 query rows a head (520 MB)
 // 120 us at 87 of reading, of them 5 before the first load (tables, lines), 8 in the join; 80 rows a head over
