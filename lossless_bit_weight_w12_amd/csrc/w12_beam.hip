@@ -86,7 +86,9 @@ __device__ __forceinline__ double wave_sum(double v) {
 
 // What a part's exponentials are relative to: exp(0), so that nothing is lost in a difference, or, where the
 // largest value is far from 0, that.
-__device__ __forceinline__ float base_of(float top) { return (top >= -24.f && top < 32.f) || top == -INFINITY ? 0.f : top; }
+__device__ __forceinline__ float base_of(float top) {
+  return (top >= -24.f && top < 32.f) || top == -INFINITY ? 0.f : top;
+}
 
 // Sum of exp(x - base).  x log2(e) is taken as h + l, h in FP32: exp2 of the hardware of h (off by 8.5e-8 of
 // itself at most, over all h), and what l makes of it to first order, l exp2(h), in a sum of its own.  FP32
@@ -100,7 +102,8 @@ struct Exps {
   double sum = 0;
   float rest = 0.f;
   __device__ __forceinline__ void add(float given) {
-    const float x = __builtin_elementwise_maximum(given, -150.f), h = x * kL, e = __builtin_amdgcn_exp2f(h);   // (NaN stays)
+    const float x = __builtin_elementwise_maximum(given, -150.f);   // (NaN stays)
+    const float h = x * kL, e = __builtin_amdgcn_exp2f(h);
     sum += (double)e;
     rest = fmaf(e, F32 ? fmaf(x, kLow, fmaf(x, kL, -h)) : x, rest);
   }
@@ -110,7 +113,9 @@ struct Exps {
     sum += (double)e;
     rest = fmaf(e, (float)(y - (double)h) * (F32 ? 1.f : 1.f / kLow), rest);
   }
-  __device__ __forceinline__ double all() const { return sum + (double)rest * ((F32 ? 1.0 : (double)kLow) * 0.6931471805599453); }
+  __device__ __forceinline__ double all() const {
+    return sum + (double)rest * ((F32 ? 1.0 : (double)kLow) * 0.6931471805599453);
+  }
 };
 
 // LDS that the wave has written and reads: it keeps the order.
@@ -388,7 +393,8 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
     double all_sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (64u * i < S) all_sum += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)base_of(tops[i]) - to);   // (0, or NaN that stays)
+      if (64u * i < S)   // (without a maximum: 0, or NaN that stays)
+        all_sum += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)base_of(tops[i]) - to);
     all_sum = wave_sum(all_sum);
     if (lane == 0) s.join.lse[b] = to + log(all_sum);
     // As in a part: a bound that at least k keys reach and not many more, and those by their ranks among

@@ -262,8 +262,8 @@ __device__ __forceinline__ uint32_t fork_look(const ForkArgs& a, ForkLds<T, N>& 
   return block_sum<T>(freed, s.w);
 }
 
-// The second half.  ring: its head and count as they were; none: the first one has found a table that is none; before, freed: pages given back
-// by the workgroups before and by all.
+// The second half.  ring: its head and count as they were; none: the first one has found a table that is
+// none; before, freed: pages given back by the workgroups before and by all.
 template <int T, int N>
 __device__ __forceinline__ void fork_apply(const ForkArgs& a, ForkLds<T, N>& s, uint2 ring, bool none, uint32_t before,
                                            uint32_t freed) {
