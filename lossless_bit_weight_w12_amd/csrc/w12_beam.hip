@@ -85,36 +85,33 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 // What a part's exponentials are relative to: exp(0), so that nothing is lost in a difference, or, where the
-// largest value is far from 0, that.
+// largest value is far from 0, that.  (From 64 on, FP32 values less than 32 below it differ from it by 24 bits at
+// most, BF16 values from 32 on, and below -24 those less than 24 below it, so that the difference is exact; what
+// lies lower is 2^21 values of e^-24 at most.)
+template <bool F32>
 __device__ __forceinline__ float base_of(float top) {
-  return (top >= -24.f && top < 32.f) || top == -INFINITY ? 0.f : top;
+  return (top >= -24.f && top < (F32 ? 64.f : 32.f)) || top == -INFINITY ? 0.f : top;
 }
 
-// Sum of exp(x - base).  x log2(e) is taken as h + l, h in FP32: exp2 of the hardware of h (off by 8.5e-8 of
-// itself at most, over all h), and what l makes of it to first order, l exp2(h), in a sum of its own.  FP32
-// values: h rounded, l what that leaves out, 2^-18 at most.  BF16 values: h exact, with a factor of 16 bits, l
-// the rest of log2(e), 7.1e-6 of x (whose second order is 1.3e-8 of a term where x is 32).  Below -150 a term
-// is nothing (the largest is 2^-35 at least), -inf among them.
-template <bool F32>
+// Sum of exp(x).  x log2(e) is taken as h + l, h in FP32: exp2 of the hardware of h (off by 8.5e-8 of itself at
+// most, over all h), and what l makes of it to first order, l exp2(h), in a sum of its own.  With log2(e) in 24
+// bits, h is rounded and l what that leaves out, 2^-18 at most; for BF16 values below 32, in 16 bits, h is exact
+// and l the rest of log2(e), 7.1e-6 of x (whose second order is 1.3e-8 of a term where x is 32).  Below -150 a
+// term is nothing (the largest is 2^-35 at least), -inf among them.
+template <bool Bits16>
 struct Exps {
-  static constexpr float kL = F32 ? 1.44269502f : 1.44268798828125f;       // 24 bits, 16 bits
-  static constexpr float kLow = F32 ? 1.92596299e-8f : 7.05260771e-6f;     // log2(e) - kL
+  static constexpr float kL = Bits16 ? 1.44268798828125f : 1.44269502f;
+  static constexpr float kLow = Bits16 ? 7.05260771e-6f : 1.92596299e-8f;   // log2(e) - kL
   double sum = 0;
   float rest = 0.f;
   __device__ __forceinline__ void add(float given) {
     const float x = __builtin_elementwise_maximum(given, -150.f);   // (NaN stays)
     const float h = x * kL, e = __builtin_amdgcn_exp2f(h);
     sum += (double)e;
-    rest = fmaf(e, F32 ? fmaf(x, kLow, fmaf(x, kL, -h)) : x, rest);
-  }
-  __device__ __forceinline__ void add(float x, double base) {
-    const double t = (double)x - base, y = (t < -150.0 ? -150.0 : t) * 1.4426950408889634;
-    const float h = (float)y, e = __builtin_amdgcn_exp2f(h);
-    sum += (double)e;
-    rest = fmaf(e, (float)(y - (double)h) * (F32 ? 1.f : 1.f / kLow), rest);
+    rest = fmaf(e, Bits16 ? x : fmaf(x, kLow, fmaf(x, kL, -h)), rest);
   }
   __device__ __forceinline__ double all() const {
-    return sum + (double)rest * ((F32 ? 1.0 : (double)kLow) * 0.6931471805599453);
+    return sum + (double)rest * ((Bits16 ? (double)kLow : 1.0) * 0.6931471805599453);
   }
 };
 
@@ -274,20 +271,23 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
     for (int i = 0; i < U; ++i) asm volatile("" : "+v"(raw[i]));
   };
   packed();
-  const float from = base_of(most);
-  Exps<F32> exps;
+  const float from = base_of<F32>(most);
+  double all;
   if (from == 0.f) {
+    Exps<!F32> exps;
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) exps.add(at(i, j));
+    all = wave_sum(exps.all());
   } else {
+    Exps<false> exps;
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) exps.add(at(i, j), (double)from);
+      for (int j = 0; j < V; ++j) exps.add(at(i, j) - from);
+    all = wave_sum(exps.all());
   }
-  const double all = wave_sum(exps.all());
   if (lane == 0) s_sum[wave] = all;
 
   // ---- candidates, and the k best of them in order
@@ -389,12 +389,12 @@ __global__ __launch_bounds__(kBeamT, K > 16 ? 2 : 4) void k_beam(BeamArgs a) {
     }
     const uint32_t top_order = wave_max(order(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]))));
     const float top = value(top_order);
-    const double to = base_of(top);
+    const double to = base_of<F32>(top);
     double all_sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (64u * i < S)   // (without a maximum: 0, or NaN that stays)
-        all_sum += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)base_of(tops[i]) - to);
+        all_sum += tops[i] == -INFINITY ? sums[i] : sums[i] * exp((double)base_of<F32>(tops[i]) - to);
     all_sum = wave_sum(all_sum);
     if (lane == 0) s.join.lse[b] = to + log(all_sum);
     // As in a part: a bound that at least k keys reach and not many more, and those by their ranks among

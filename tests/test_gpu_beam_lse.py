@@ -37,7 +37,7 @@ def ahead(n):
 
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("n", SHARES)
-@pytest.mark.parametrize("top", [0.0, 8.0, -13.5])
+@pytest.mark.parametrize("top", [0.0, 8.0, -13.5, 31.0, 33.0, 63.5, 64.5, 300.0, -23.5, -24.5, -70.0])
 def test_all_others_equal(top, n, f32):
     x = (top - ahead(n))[:, None].repeat(1, VOCAB)
     x[:, 77] = top
@@ -96,3 +96,16 @@ def test_parts_far_apart(step):
         x = (sign * step * part).repeat(2, 1)
         x[:, 50000] = x.max() + 1.0
         assert (off_by(x, 50000) <= BOUND).all()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("top", [31.5, 32.0, 48.0, 63.0, 64.0, 90.0, -24.0, -25.0])
+def test_rests_of_every_distance(top, f32):
+    """2^18 logits, alike but for the one that stands out, 10 to 30 below it: where together they weigh as much
+    as it does, or nothing, and their distance has more bits than they."""
+    g = np.random.default_rng(86)
+    n, vocab = 41, 1 << 18
+    x = torch.from_numpy(np.repeat((top - np.linspace(10, 30, n) - g.random(n) / 64).astype(np.float32)[:, None], vocab, 1)).to(DEV)
+    x = x if f32 else x.bfloat16()
+    x[:, 5000] = top
+    assert (off_by(x, 5000) <= BOUND).all()
