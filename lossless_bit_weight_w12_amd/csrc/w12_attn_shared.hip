@@ -16,8 +16,8 @@
 // Bound by HBM where few rows share tokens: 24 prompts of up to 8000 tokens, 20 query rows a head (520 MB)
 // 120 us at 87 of reading, of them 5 before the first load (tables, lines), 8 in the join; 80 rows a head over
 // 131001 tokens (547 MB) 119 us at 91.  Bound by the matrix cores' neighbours where many do: 1600 rows a head
-// over 8000 tokens in E4M3 105 us at 47 of products; by their counters the matrix cores have 30 us of work,
-// the vector units some 36, the reads of LDS 15 to 30, and they overlap in part only.
+// over 8000 tokens in E4M3 116 us at 47 of products; by their counters the matrix cores have 30 us of work,
+// the vector units some 45, the reads of LDS 15 to 30, and they overlap in part only.
 #include <type_traits>
 
 #include "w12.h"
@@ -47,7 +47,7 @@ struct Shared {
   static constexpr int NL = F8 ? D / 32 : D / 16;          // 16-byte loads of a wave per step
   // Places on the lines: per item, and per unit (of 64 tokens by row tiles of 32, of UT tokens).  Measured, us,
   // with 8 / 6 / 5, 8 / 5 / 5, 8 / 5 / 3 and 8 for all: 300 query rows a head over 20000 tokens in E4M3 68, 68, 66,
-  // 72, 320 over 8000 117, 118, 114, 118, 80 over 131001 in BF16 121, 119, 119, 122; with leads of 2, 8, 16
+  // 72, 1600 over 8000 117, 118, 114, 118, 80 over 131001 in BF16 121, 119, 119, 122; with leads of 2, 8, 16
   // and 32 places: four groups of 50 rows over 20000 84, 79, 79, 79, 90 rows of heads of 256 100, 97, 98, 97.
   static constexpr uint32_t kLeadW = 8, kLeadV = 3;
   static __device__ __forceinline__ uint32_t cost(uint32_t row_tiles) {
@@ -58,7 +58,7 @@ struct Shared {
   // following the maximum only when that has risen by a factor of 2^kRise (so the results are seldom
   // rescaled).  BF16 weights may reach 2^8.  FP16 ones begin at 2^15, as in the waves' path, so that as many
   // of the small ones are kept (11 bits down to 2^-29 of the largest, a part of them down to 2^-39), and
-  // 2^15.9 is what the type leaves for them to rise to.  (From 2^7, with 2^8 to rise by, 320 query rows a head over
+  // 2^15.9 is what the type leaves for them to rise to.  (From 2^7, with 2^8 to rise by, 1600 query rows a head over
   // 8000 tokens took 109 us in place of 115.5, and weights of 2^-32 were lost.)
   // c s + bias is one fused operation, exact but for its own rounding, and the bias is a number of its own, no
   // rounded product that would have to be the same elsewhere; where c s is so large (kFar) that the bias cannot

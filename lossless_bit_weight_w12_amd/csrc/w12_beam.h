@@ -20,8 +20,8 @@ struct BeamArgs {
 };
 
 // A workgroup takes 256 threads' worth of 16, 32 or 64 values each: the smallest share that leaves
-// at most four workgroups to a CU (us for 151936 BF16 logits, k = 8: 12 x 4 rows 20.3, 16.4, 20.4; 24 x 4
-// rows 27.6, 22.4, 20.2), and the largest for long lists and rows, whose parts a join takes up to
+// at most four workgroups to a CU (us for 151936 BF16 logits, k = 8: 12 x 4 rows 19.9, 16.1, 16.1; 24 x 4
+// rows 29.7, 22.1, 20.6), and the largest for long lists and rows, whose parts a join takes up to
 // 256 of.
 constexpr uint32_t kBeamT = 256, kBeamShort = 16, kBeamParts = 1024;
 inline uint32_t beam_values(uint32_t n, uint32_t vocab, uint32_t k) {

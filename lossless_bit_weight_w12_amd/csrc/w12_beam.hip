@@ -14,12 +14,12 @@
 // Exponentials: exp2 of the hardware, whose own error is the only one that is left (see Exps); sums in FP64.
 // That keeps lse within 1e-7 whatever the logits are, so the choice is that of FP64 unless scores are as close
 // as that.  (Terms are alike in a row of few values, and behind one that stands out, and then so are their
-// roundings: sums of a thread in FP32 were off by up to 2.5e-6.  They took 19.5 us in place of 20.5 for 96 rows
+// roundings: sums of a thread in FP32 were off by up to 2.5e-6.  They took 19.6 us in place of 20.3 for 96 rows
 // in BF16; terms of exactly reduced arguments 23.0.)
 //
-// Bound by the dependent steps behind the reads: 4 rows of 151936 FP32 logits 12.4 us, of them 4 for the
-// part, 1.2 for the ticket, 5 for the join; 96 rows in BF16 (29 MB, 4.9 us of reading) 20.5, of them 7 to
-// 12 for the part; k = 64 takes 24 to 27 us more.  Tickets of a call lie as far apart as their 16 KB allow: beside
+// Bound by the dependent steps behind the reads: 4 rows of 151936 FP32 logits 12.3 us, of them 4 for the
+// part, 1.2 for the ticket, 5 for the join; 96 rows in BF16 (29 MB, 4.9 us of reading) 20.3, of them 8 to
+// 13 for the part; k = 64 takes 24 to 28 us more.  Tickets of a call lie as far apart as their 16 KB allow: beside
 // each other in one line they passed one after the other, 18 ns each (38 us in place of 20).
 #include "w12.h"
 #include "w12_beam.h"
